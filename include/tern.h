@@ -393,6 +393,153 @@ tern_status tern_linear_i8(const void* d_xq, const float* d_a, const void* d_til
                            void* d_ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Attention side of a decoder layer: rotary positions, the paged key/value
+ * cache and attention.  The pages name them around the linear layer ([EMB]
+ * §6: quantising the cache together with the kernel; [B27] and the other
+ * pages: 8-bit caches, 8 key/value heads of dimension 128, contexts to 32K)
+ * without defining them; the definitions are the ones below.
+ *
+ * Common to the calls
+ *   - x_type is the 16-bit type of queries, keys, values and outputs.  A row
+ *     holds the heads of one token one after the other; ld* is the distance
+ *     between rows in elements (so the outputs of a fused projection serve as
+ *     they are).  Data pointers are 16-byte aligned and every ld is a
+ *     multiple of 8, at least heads * D.
+ *   - D is the head dimension, a multiple of 16: up to 256 for tern_rope, up
+ *     to 128 for the cache and attention.
+ *   - Hq query heads share Hkv key/value heads, Hq a multiple of Hkv: query
+ *     head h reads key/value head h / (Hq / Hkv).
+ *   - Inputs and outputs must not overlap unless a call says so.
+ * ---------------------------------------------------------------------- */
+
+/* Pairs that a rotation turns: (i, i + rot_dim/2) or (2i, 2i + 1). */
+typedef enum { TERN_ROPE_HALF = 0, TERN_ROPE_INTERLEAVED = 1 } tern_rope_layout;
+
+/* How tern_rope_freqs stretches the frequencies to contexts `factor` times
+ * the trained one. */
+typedef enum {
+    TERN_ROPE_SCALE_NONE = 0,
+    TERN_ROPE_SCALE_LINEAR = 1, /* every frequency / factor */
+    TERN_ROPE_SCALE_BASE = 2,   /* base * factor^(rot_dim / (rot_dim - 2)): the slowest pair / factor */
+    TERN_ROPE_SCALE_PARTS = 3   /* by the turns a pair makes over the trained context, see below */
+} tern_rope_scaling;
+
+/* What the cache holds: 16-bit values as they are, or 8-bit codes with one
+ * fp32 factor per token and head. */
+typedef enum { TERN_KV_X16 = 0, TERN_KV_E4M3 = 1, TERN_KV_I8 = 2 } tern_kv_type;
+
+/* Frequencies of rotary positions, computed on the host in double:
+ *   h_inv_freq[i] = base^(-2i/rot_dim), i < rot_dim/2   (radians per position),
+ * then stretched.  TERN_ROPE_SCALE_PARTS: with u_i = trained_len *
+ * h_inv_freq[i] / (2 pi), the turns of pair i over the trained context, and
+ * r = clamp((u_i - turns_low) / (turns_high - turns_low), 0, 1), the frequency
+ * becomes f (r + (1 - r) / factor), and *h_amplitude = 0.1 ln(factor) + 1
+ * (1 for factor <= 1); otherwise *h_amplitude = 1.  h_inv_freq and
+ * h_amplitude are HOST memory.  rot_dim positive and even (above 2 for
+ * TERN_ROPE_SCALE_BASE), base > 0, factor > 0; TERN_ROPE_SCALE_PARTS also
+ * trained_len > 0 and turns_high > turns_low. */
+tern_status tern_rope_freqs(int64_t rot_dim, double base, int scaling, double factor, double trained_len,
+                            double turns_low, double turns_high, float* h_inv_freq, float* h_amplitude);
+
+/* Rotary positions of queries and keys in one pass.  Token t at position
+ * p = d_pos[t] turns pair i of every head by the angle p * d_inv_freq[i]:
+ *   (a, b) -> amplitude * (a cos - b sin, b cos + a sin);
+ * elements from rot_dim on are copied.  The angle is reduced in double, the
+ * rest is fp32, rounded once.
+ *   d_pos      device int32 [T]; d_inv_freq device fp32 [rot_dim/2]
+ *   d_Q, d_Qo  device [T, ldq] in, [T, ldqo] out, Hq heads; d_Qo may be d_Q
+ *              with ldqo == ldq
+ *   d_K, d_Ko  likewise with Hk heads; Hk == 0: none (the pointers are unused)
+ *   rot_dim    a multiple of 16, 0 <= rot_dim <= D
+ * T == 0 is a no-op. */
+tern_status tern_rope(int x_type, int layout, int64_t T, int64_t D, int64_t rot_dim, const int32_t* d_pos,
+                      const float* d_inv_freq, float amplitude, int64_t Hq, const void* d_Q, int64_t ldq,
+                      void* d_Qo, int64_t ldqo, int64_t Hk, const void* d_K, int64_t ldk, void* d_Ko,
+                      int64_t ldko, void* stream);
+
+/* The paged cache.  Keys and values each lie in num_pages pages of page_size
+ * tokens (a power of two up to 32768): element (page, head, row, d) at
+ * ((page * Hkv + head) * page_size + row) * D + d, 16-bit values of x_type
+ * or 8-bit codes; with codes, the fp32 factor of (page, head, row) at
+ * (page * Hkv + head) * page_size + row of d_kscale / d_vscale (unused, may
+ * be NULL, for TERN_KV_X16).  Slot s is row s % page_size of page
+ * s / page_size.  The codes of a head's D values x with m = max |x|:
+ *   factor = m / top, code = round(x * (top / m)) in fp32, ties to even,
+ * top = 448 (TERN_KV_E4M3: to 8-bit floats of 4 exponent and 3 mantissa
+ * bits) or 127 (TERN_KV_I8); m == 0 gives factor 0 and codes 0.  A head that
+ * holds a NaN or an infinity gets factor NaN and codes 0: it reads back as
+ * NaN and nothing else does.  Cache pointers are 16-byte aligned, the factors
+ * 4-byte. */
+
+/* Write T tokens: token t's keys d_K [T, ldk] and values d_V [T, ldv] to slot
+ * d_slots[t] (device int64 [T]).  A negative slot skips the token (padding);
+ * one at or above num_pages * page_size is skipped and counted in d_err
+ * (optional device int32).  Two tokens with one slot: either may stay. */
+tern_status tern_kv_write(int x_type, int kv_type, int64_t T, int64_t Hkv, int64_t D, const void* d_K, int64_t ldk,
+                          const void* d_V, int64_t ldv, const int64_t* d_slots, int64_t num_pages, int64_t page_size,
+                          void* d_kcache, void* d_vcache, float* d_kscale, float* d_vscale, int32_t* d_err,
+                          void* stream);
+
+/* tern_rope and tern_kv_write in one pass: queries are rotated to d_Qo, keys
+ * are rotated, rounded to x_type and written to the cache with the values.
+ * Results equal those of the two calls bit for bit. */
+tern_status tern_rope_kv_write(int x_type, int kv_type, int layout, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                               int64_t rot_dim, const int32_t* d_pos, const float* d_inv_freq, float amplitude,
+                               const void* d_Q, int64_t ldq, void* d_Qo, int64_t ldqo, const void* d_K, int64_t ldk,
+                               const void* d_V, int64_t ldv, const int64_t* d_slots, int64_t num_pages,
+                               int64_t page_size, void* d_kcache, void* d_vcache, float* d_kscale, float* d_vscale,
+                               int32_t* d_err, void* stream);
+
+/* Read T tokens back: slot d_slots[t] to row t of d_K [T, ldk] and d_V
+ * [T, ldv], code * factor in fp32 rounded to x_type.  A slot outside the
+ * cache gives a row of zeros. */
+tern_status tern_kv_read(int x_type, int kv_type, int64_t T, int64_t Hkv, int64_t D, const int64_t* d_slots,
+                         int64_t num_pages, int64_t page_size, const void* d_kcache, const void* d_vcache,
+                         const float* d_kscale, const float* d_vscale, void* d_K, int64_t ldk, void* d_V, int64_t ldv,
+                         void* stream);
+
+/* Attention over prompts: B sequences packed along the rows.  Sequence b has
+ * query rows [d_cu_q[b], d_cu_q[b+1]) of Tq and key/value rows
+ * [d_cu_kv[b], d_cu_kv[b+1]) of Tkv (device int32 [B+1] each, non-decreasing;
+ * they may be one array); scale is finite and not negative.  With nq and nk of them, query i attends to every
+ * key (causal == 0) or to the keys j <= i + nk - nq (causal != 0: the last
+ * query sees all, as when nk - nq tokens came before):
+ *   O[i] = sum_j softmax_j(scale * Q[i].K[j]) V[j],
+ *   lse[i] = ln sum_j exp(scale * Q[i].K[j]).
+ * A query that sees no key gets O = 0 and lse = -infinity.  Products of 16-bit
+ * values are exact in fp32, sums, maxima and the softmax are fp32; the weights
+ * are rounded to x_type for their product with V and O is rounded once.
+ *   d_O    device [Tq, ldo] of x_type; rows of no sequence are not written
+ *   d_lse  optional device fp32 [Tq, Hq]
+ *   d_ws   as tern_linear's, of tern_attn_prompt_workspace_bytes
+ * Offsets outside [0, Tq] / [0, Tkv] are read as the nearest end, a sequence
+ * whose offsets decrease as empty. */
+size_t tern_attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, int64_t D);
+
+tern_status tern_attn_prompt(int x_type, int64_t B, const int32_t* d_cu_q, const int32_t* d_cu_kv, int64_t Tq,
+                             int64_t Tkv, int64_t Hq, int64_t Hkv, int64_t D, int causal, float scale, const void* d_Q,
+                             int64_t ldq, const void* d_K, int64_t ldk, const void* d_V, int64_t ldv, void* d_O,
+                             int64_t ldo, float* d_lse, void* d_ws, size_t ws_bytes, void* stream);
+
+/* Attention of single tokens over the paged cache: row b of d_Q [B, ldq]
+ * attends to the first d_lens[b] tokens of its sequence, token j being in row
+ * j % page_size of page d_page_table[b * max_pages + j / page_size] (device
+ * int32).  Definitions as tern_attn_prompt's, with keys and values as
+ * tern_kv_read gives them before rounding; the weights are rounded to x_type
+ * (TERN_KV_X16) or fp16 (codes).  Lengths are read as within
+ * [0, max_pages * page_size] (below 2^31); a page id outside the cache hides
+ * its tokens.  B rows of d_O and (optional) d_lse [B, Hq] are written; a
+ * length of zero gives O = 0 and lse = -infinity.  max_len of the workspace
+ * size is max_pages * page_size. */
+size_t tern_attn_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len);
+
+tern_status tern_attn_decode(int x_type, int kv_type, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, float scale,
+                             const void* d_Q, int64_t ldq, int64_t num_pages, int64_t page_size, const void* d_kcache,
+                             const void* d_vcache, const float* d_kscale, const float* d_vscale,
+                             const int32_t* d_page_table, int64_t max_pages, const int32_t* d_lens, void* d_O,
+                             int64_t ldo, float* d_lse, void* d_ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Workspace maintenance (library conveniences; the pages have none).
  * ---------------------------------------------------------------------- */
 

@@ -17,6 +17,9 @@ from . import build as _build
 TERN_OK = 0
 TERN_X_BF16, TERN_X_F16 = 0, 1
 TERN_OUT_F32, TERN_OUT_BF16, TERN_OUT_F16 = 0, 1, 2
+TERN_ROPE_HALF, TERN_ROPE_INTERLEAVED = 0, 1
+TERN_ROPE_SCALE_NONE, TERN_ROPE_SCALE_LINEAR, TERN_ROPE_SCALE_BASE, TERN_ROPE_SCALE_PARTS = 0, 1, 2, 3
+TERN_KV_X16, TERN_KV_E4M3, TERN_KV_I8 = 0, 1, 2
 STATUS_NAMES = {0: "TERN_OK", 1: "TERN_ERR_NULL", 2: "TERN_ERR_SHAPE", 3: "TERN_ERR_ALIGN",
                 4: "TERN_ERR_SIZE", 5: "TERN_ERR_UNSUPPORTED", 6: "TERN_ERR_CUDA"}
 
@@ -28,7 +31,10 @@ EXPORTED = ("tern_status_string", "tern_version", "tern_pack", "tern_unpack", "t
             "tern_workspace_error", "tern_workspace_reset", "tern_xq_bytes", "tern_quantize_x",
             "tern_i8_workspace_bytes", "tern_linear_i8", "tern_tiled_s8_bytes", "tern_quantize_scales",
             "tern_repack_s8", "tern_linear_s8", "tern_unit_count", "tern_zero_units", "tern_linear_sparse",
-            "tern_grouped_workspace_bytes", "tern_linear_grouped", "tern_repack_grouped")
+            "tern_grouped_workspace_bytes", "tern_linear_grouped", "tern_repack_grouped",
+            "tern_rope_freqs", "tern_rope", "tern_kv_write", "tern_rope_kv_write", "tern_kv_read",
+            "tern_attn_prompt_workspace_bytes", "tern_attn_prompt", "tern_attn_decode_workspace_bytes",
+            "tern_attn_decode")
 
 MAX_GROUP = 8
 
@@ -115,6 +121,29 @@ def _load():
     lib.tern_linear_sparse.argtypes = [vp, i32, i64, vp, vp, i64, i64, i32, ctypes.POINTER(i64),
                                        ctypes.POINTER(vp), ctypes.POINTER(i64), i32, vp, sz, vp]
     lib.tern_linear_sparse.restype = i32
+    f32, f64 = ctypes.c_float, ctypes.c_double
+    lib.tern_rope_freqs.argtypes = [i64, f64, i32, f64, f64, f64, f64, vp, vp]
+    lib.tern_rope_freqs.restype = i32
+    lib.tern_rope.argtypes = [i32, i32, i64, i64, i64, vp, vp, f32, i64, vp, i64, vp, i64, i64, vp, i64, vp, i64, vp]
+    lib.tern_rope.restype = i32
+    cache = [i64, i64, vp, vp, vp, vp]
+    lib.tern_kv_write.argtypes = [i32, i32, i64, i64, i64, vp, i64, vp, i64, vp, *cache, vp, vp]
+    lib.tern_kv_write.restype = i32
+    lib.tern_rope_kv_write.argtypes = [i32, i32, i32, i64, i64, i64, i64, i64, vp, vp, f32, vp, i64, vp, i64, vp, i64,
+                                       vp, i64, vp, *cache, vp, vp]
+    lib.tern_rope_kv_write.restype = i32
+    lib.tern_kv_read.argtypes = [i32, i32, i64, i64, i64, vp, *cache, vp, i64, vp, i64, vp]
+    lib.tern_kv_read.restype = i32
+    lib.tern_attn_prompt_workspace_bytes.argtypes = [i64] * 6
+    lib.tern_attn_prompt_workspace_bytes.restype = sz
+    lib.tern_attn_prompt.argtypes = [i32, i64, vp, vp, i64, i64, i64, i64, i64, i32, f32, vp, i64, vp, i64, vp, i64,
+                                     vp, i64, vp, vp, sz, vp]
+    lib.tern_attn_prompt.restype = i32
+    lib.tern_attn_decode_workspace_bytes.argtypes = [i64] * 5
+    lib.tern_attn_decode_workspace_bytes.restype = sz
+    lib.tern_attn_decode.argtypes = [i32, i32, i64, i64, i64, i64, f32, vp, i64, *cache, vp, i64, vp, vp, i64, vp, vp,
+                                     sz, vp]
+    lib.tern_attn_decode.restype = i32
     return lib
 
 
@@ -373,3 +402,74 @@ def tern_linear_sparse(X, x_type: int, ldx: int, tiled, flags, M: int, K: int, n
         ws_bytes = _nbytes(ws)
     _check(_lib.tern_linear_sparse(_p(X), x_type, ldx, _p(tiled), _p(flags), M, K, n_out, sizes, ptrs, lds,
                                    out_type, _p(ws), ws_bytes, _s(stream)), "tern_linear_sparse")
+
+
+def tern_rope_freqs(rot_dim: int, base: float, scaling: int = TERN_ROPE_SCALE_NONE, factor: float = 1.0,
+                    trained_len: float = 1.0, turns_low: float = 1.0, turns_high: float = 32.0):
+    """Frequencies of rotary positions: (list of rot_dim/2 fp32 values, amplitude)."""
+    freq = (ctypes.c_float * max(1, int(rot_dim) // 2))()
+    amplitude = ctypes.c_float(0.0)
+    _check(_lib.tern_rope_freqs(rot_dim, base, scaling, factor, trained_len, turns_low, turns_high,
+                                ctypes.addressof(freq), ctypes.addressof(amplitude)), "tern_rope_freqs")
+    return list(freq), float(amplitude.value)
+
+
+def tern_rope(x_type: int, layout: int, T: int, D: int, rot_dim: int, pos, inv_freq, amplitude: float, Hq: int, Q,
+              ldq: int, Qo, ldqo: int, Hk: int = 0, K=None, ldk: int = 0, Ko=None, ldko: int = 0, stream=None):
+    """Rotary positions of queries and (Hk > 0) keys in one pass."""
+    _check(_lib.tern_rope(x_type, layout, T, D, rot_dim, _p(pos), _p(inv_freq), amplitude, Hq, _p(Q), ldq, _p(Qo), ldqo,
+                          Hk, _p(K), ldk, _p(Ko), ldko, _s(stream)), "tern_rope")
+
+
+def tern_kv_write(x_type: int, kv_type: int, T: int, Hkv: int, D: int, K, ldk: int, V, ldv: int, slots, num_pages: int,
+                  page_size: int, kcache, vcache, kscale=None, vscale=None, err=None, stream=None):
+    """Store T tokens' keys and values in the paged cache."""
+    _check(_lib.tern_kv_write(x_type, kv_type, T, Hkv, D, _p(K), ldk, _p(V), ldv, _p(slots), num_pages, page_size,
+                              _p(kcache), _p(vcache), _p(kscale), _p(vscale), _p(err), _s(stream)), "tern_kv_write")
+
+
+def tern_rope_kv_write(x_type: int, kv_type: int, layout: int, T: int, Hq: int, Hkv: int, D: int, rot_dim: int, pos,
+                       inv_freq, amplitude: float, Q, ldq: int, Qo, ldqo: int, K, ldk: int, V, ldv: int, slots,
+                       num_pages: int, page_size: int, kcache, vcache, kscale=None, vscale=None, err=None, stream=None):
+    """tern_rope of queries and keys and tern_kv_write of the rotated keys in one pass."""
+    _check(_lib.tern_rope_kv_write(x_type, kv_type, layout, T, Hq, Hkv, D, rot_dim, _p(pos), _p(inv_freq), amplitude,
+                                   _p(Q), ldq, _p(Qo), ldqo, _p(K), ldk, _p(V), ldv, _p(slots), num_pages, page_size,
+                                   _p(kcache), _p(vcache), _p(kscale), _p(vscale), _p(err), _s(stream)),
+           "tern_rope_kv_write")
+
+
+def tern_kv_read(x_type: int, kv_type: int, T: int, Hkv: int, D: int, slots, num_pages: int, page_size: int, kcache,
+                 vcache, kscale, vscale, K, ldk: int, V, ldv: int, stream=None):
+    """Read T tokens of the paged cache back as rows of keys and values."""
+    _check(_lib.tern_kv_read(x_type, kv_type, T, Hkv, D, _p(slots), num_pages, page_size, _p(kcache), _p(vcache),
+                             _p(kscale), _p(vscale), _p(K), ldk, _p(V), ldv, _s(stream)), "tern_kv_read")
+
+
+def tern_attn_prompt_workspace_bytes(B: int, Tq: int, Tkv: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(_lib.tern_attn_prompt_workspace_bytes(B, Tq, Tkv, Hq, Hkv, D))
+
+
+def tern_attn_prompt(x_type: int, B: int, cu_q, cu_kv, Tq: int, Tkv: int, Hq: int, Hkv: int, D: int, causal: bool,
+                     scale: float, Q, ldq: int, K, ldk: int, V, ldv: int, O, ldo: int, lse=None, ws=None,
+                     ws_bytes: int | None = None, stream=None):
+    """Attention over B packed prompts."""
+    if ws_bytes is None:
+        ws_bytes = _nbytes(ws)
+    _check(_lib.tern_attn_prompt(x_type, B, _p(cu_q), _p(cu_kv), Tq, Tkv, Hq, Hkv, D, int(causal), scale, _p(Q), ldq,
+                                 _p(K), ldk, _p(V), ldv, _p(O), ldo, _p(lse), _p(ws), ws_bytes, _s(stream)),
+           "tern_attn_prompt")
+
+
+def tern_attn_decode_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
+    return int(_lib.tern_attn_decode_workspace_bytes(B, Hq, Hkv, D, max_len))
+
+
+def tern_attn_decode(x_type: int, kv_type: int, B: int, Hq: int, Hkv: int, D: int, scale: float, Q, ldq: int,
+                     num_pages: int, page_size: int, kcache, vcache, kscale, vscale, page_table, max_pages: int, lens,
+                     O, ldo: int, lse=None, ws=None, ws_bytes: int | None = None, stream=None):
+    """Attention of one token per sequence over the paged cache."""
+    if ws_bytes is None:
+        ws_bytes = _nbytes(ws)
+    _check(_lib.tern_attn_decode(x_type, kv_type, B, Hq, Hkv, D, scale, _p(Q), ldq, num_pages, page_size, _p(kcache),
+                                 _p(vcache), _p(kscale), _p(vscale), _p(page_table), max_pages, _p(lens), _p(O), ldo,
+                                 _p(lse), _p(ws), ws_bytes, _s(stream)), "tern_attn_decode")

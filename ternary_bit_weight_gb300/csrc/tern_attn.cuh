@@ -1,0 +1,62 @@
+// Device helpers shared by the attention-side kernels (rotary positions,
+// cache, attention).
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "tern_common.cuh"
+
+namespace tern {
+
+// ------------------------------------------------------ 16-bit value pairs
+
+template <bool F16>
+__device__ __forceinline__ float2 unpack_x2(uint32_t w) {
+    if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_x2(float lo, float hi) {
+    uint32_t w;
+    if (F16)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
+template <bool F16>
+__device__ __forceinline__ uint16_t pack_x1(float v) {
+    return F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// ------------------------------------------------------------- cache codes
+
+// Two 8-bit floats (low byte first) as fp16, exactly.
+__device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t codes16) {
+    return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes16), __NV_E4M3));
+}
+
+// ---------------------------------------------------------------- launches
+
+// Launch with programmatic dependent launch: the kernel may be scheduled
+// while its predecessor drains, and waits for it (grid_dependency_wait)
+// before it touches memory.
+template <typename Kernel, typename... Args>
+cudaError_t launch_after(Kernel kernel, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                         const Args&... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace tern

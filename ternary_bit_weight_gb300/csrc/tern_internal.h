@@ -137,6 +137,86 @@ cudaError_t launch_quantize_x(const uint16_t* X, bool x_f16, int64_t ldx, int64_
 cudaError_t launch_i8(const int8_t* xq, const float* a, const uint8_t* tiled, int64_t M, int64_t N,
                       const OutputSplit& out, void* ws, const I8Plan& plan, cudaStream_t stream);
 
+// -------------------------------------------------------- attention side
+
+// What a cache holds (kKvNone: no cache involved).  Internal names of
+// tern_kv_type.
+constexpr int kKvNone = -1, kKvX16 = 0, kKvE4m3 = 1, kKvI8 = 2;
+
+// The paged cache: element (page, head, row, d) at
+// ((page * Hkv + head) << page_shift | row) * D + d, factor at the same
+// index without d.
+struct KvCache {
+    int kv;
+    int64_t num_pages;
+    int page_shift;
+    const void* k;
+    const void* v;
+    const float* kscale;
+    const float* vscale;
+};
+
+// Rotation of Hq query and Hk key heads of dimension D (rot == 0: none).
+struct RopeArgs {
+    bool interleaved;
+    int D, rot;
+    const int32_t* pos;
+    const float* inv_freq;
+    float amplitude;
+    int Hq, Hk;
+    const uint16_t* q;
+    int64_t ldq;
+    uint16_t* qo;
+    int64_t ldqo;
+    const uint16_t* k;
+    int64_t ldk;
+    uint16_t* ko;      // unused when keys go to a cache
+    int64_t ldko;
+};
+cudaError_t launch_rope(bool x_f16, int64_t T, const RopeArgs& r, cudaStream_t stream);
+cudaError_t launch_kv_write(bool x_f16, int64_t T, const RopeArgs& r, const uint16_t* v, int64_t ldv,
+                            const int64_t* slots, const KvCache& c, int32_t* err, cudaStream_t stream);
+cudaError_t launch_kv_read(bool x_f16, int64_t T, int Hkv, int D, const int64_t* slots, const KvCache& c, uint16_t* k,
+                           int64_t ldk, uint16_t* v, int64_t ldv, cudaStream_t stream);
+
+struct PromptArgs {
+    int B;
+    const int32_t* cu_q;
+    const int32_t* cu_kv;
+    int Tq, Tkv;
+    int Hq, Hkv, D;
+    bool causal;
+    float scale;
+    const uint16_t* q;
+    int64_t ldq;
+    const uint16_t* k;
+    int64_t ldk;
+    const uint16_t* v;
+    int64_t ldv;
+    uint16_t* o;
+    int64_t ldo;
+    float* lse;        // optional
+};
+size_t prompt_ws_bytes(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, int64_t D, int sm_count);
+cudaError_t launch_prompt(bool x_f16, const PromptArgs& a, void* ws, int sm_count, cudaStream_t stream);
+
+struct DecodeArgs {
+    int B;
+    int Hq, Hkv, D;
+    float scale;
+    const uint16_t* q;
+    int64_t ldq;
+    KvCache cache;
+    const int32_t* table;
+    int64_t max_pages;
+    const int32_t* lens;
+    uint16_t* o;
+    int64_t ldo;
+    float* lse;        // optional
+};
+size_t decode_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, int sm_count);
+cudaError_t launch_decode(bool x_f16, const DecodeArgs& a, void* ws, int sm_count, cudaStream_t stream);
+
 // Size of the error word + padding at the start of every linear workspace.
 constexpr size_t kWorkspaceErrBytes = 256;
 

@@ -1,0 +1,392 @@
+// Rotary positions and the paged key/value cache (bandwidth-bound passes
+// over token rows).
+//
+// Mathematics.  A rotation turns the pair (a, b) of a head by the angle
+// p * f (position times the pair's frequency): (a cos - b sin, b cos + a sin).
+// p * f reaches 10^5 radians and beyond, where an fp32 product is off by more
+// than a 16-bit result's rounding; the angle is formed and reduced in
+// double, in turns, and only the remainder goes to fp32.  A cached head of D
+// values x is stored as codes round(x * (top / m)) with m = max |x| and the
+// factor m / top, both divisions and the product IEEE fp32, so that any other
+// implementation of the rule gets the same codes.
+//
+// Layout of the work: a head is one task of LANES lanes (8 for D <= 128, 16
+// above), a lane owning two runs of 8 elements (16 bytes each).  In the half
+// layout the two runs are the partners of one another (elements 8j.. and
+// rot/2 + 8j..), in the interleaved layout they are neighbours; either way
+// lane j needs the angles of pairs 8j .. 8j+7 and a rotation stays inside a
+// lane.  m is a butterfly over the task's lanes.  One CTA serves one token,
+// so that its rot/2 angles are computed once for all heads, after the first
+// task's loads are on their way.
+
+#include <cuda_fp8.h>
+#include <float.h>
+
+#include "tern_attn.cuh"
+#include "tern_common.cuh"
+#include "tern_internal.h"
+
+namespace tern {
+namespace {
+
+constexpr int kMaxTokenThreads = 512;
+constexpr int kReadThreads = 256;
+constexpr int kMaxPairs = 128;   // rot_dim <= 256
+
+struct TokenArgs {
+    const int32_t* pos;
+    const float* inv_freq;
+    float amplitude;
+    int interleaved;
+    int D, rot;
+    int Hq, Hk, Hv;            // heads rotated to qo, then keys, then values
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    uint16_t* qo;
+    uint16_t* ko;              // no cache: rotated keys
+    int64_t ldq, ldk, ldv, ldqo, ldko;
+    const int64_t* slots;
+    int64_t capacity;          // num_pages * page_size
+    int page_shift;
+    uint8_t* kcache;
+    uint8_t* vcache;
+    float* kscale;
+    float* vscale;
+    int32_t* err;
+};
+
+// Rotation of pair angle `turns` (fraction of a full turn in double).
+__device__ __forceinline__ float2 cos_sin(int32_t pos, float f, float amplitude) {
+    const double turns = static_cast<double>(pos) * static_cast<double>(f) * 0.15915494309189533577;   // 1 / (2 pi)
+    const float r = static_cast<float>(turns - rint(turns));   // [-1/2, 1/2]
+    float s, c;
+    sincospif(2.0f * r, &s, &c);
+    return make_float2(c * amplitude, s * amplitude);
+}
+
+template <bool F16>
+__device__ __forceinline__ void unpack8(const uint4& u, float* x) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_x2<F16>(w[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+template <bool F16>
+__device__ __forceinline__ uint4 pack8(const float* x) {
+    return make_uint4(pack_x2<F16>(x[0], x[1]), pack_x2<F16>(x[2], x[3]), pack_x2<F16>(x[4], x[5]),
+                      pack_x2<F16>(x[6], x[7]));
+}
+
+// 8 codes of x * inv as two words.
+template <int KV>
+__device__ __forceinline__ uint2 encode8(const float* x, float inv) {
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = __fmul_rn(x[4 * h + i], inv);
+        if (KV == kKvE4m3) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+            w[h] = lo | (hi << 16);
+        } else {
+            w[h] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[h] |= (static_cast<uint32_t>(__float2int_rn(y[i])) & 0xFFu) << (8 * i);
+        }
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// One token per CTA: rotate queries and keys, and (KV != kKvNone) store keys
+// and values in the cache.
+template <int LANES, bool F16, int KV>
+__global__ void __launch_bounds__(kMaxTokenThreads) token_kernel(const TokenArgs a) {
+    __shared__ float2 cs[kMaxPairs];
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x % LANES;
+    const int tasks = a.Hq + a.Hk + a.Hv;
+    const int step = blockDim.x / LANES;
+    const bool live = lane * 16 < a.D;
+    const bool turned = live && lane * 16 < a.rot;
+    // the lane's two runs of 8 elements
+    int ea = lane * 16, eb = ea + 8;
+    if (!a.interleaved && turned) {
+        ea = lane * 8;
+        eb = a.rot / 2 + lane * 8;
+    }
+    const uint16_t* qrow = a.q + t * a.ldq;
+    const uint16_t* krow = a.k + t * a.ldk;
+    const uint16_t* vrow = KV == kKvNone ? nullptr : a.v + t * a.ldv;
+    auto source = [&](int h) {
+        return h < a.Hq             ? qrow + h * a.D
+               : h < a.Hq + a.Hk    ? krow + (h - a.Hq) * a.D
+                                    : vrow + (h - a.Hq - a.Hk) * a.D;
+    };
+    int h = threadIdx.x / LANES;
+    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
+    if (h < tasks && live) {
+        const uint16_t* src = source(h);
+        ua = *reinterpret_cast<const uint4*>(src + ea);
+        ub = *reinterpret_cast<const uint4*>(src + eb);
+    }
+    int64_t slot = -1;
+    if (KV != kKvNone) {
+        slot = a.slots[t];
+        if (slot >= a.capacity) {
+            if (threadIdx.x == 0 && a.err != nullptr) atomicAdd(a.err, 1);
+            slot = -1;
+        }
+    }
+    if (a.rot > 0) {
+        const int32_t p = a.pos[t];
+        for (int i = threadIdx.x; i < a.rot / 2; i += blockDim.x) cs[i] = cos_sin(p, a.inv_freq[i], a.amplitude);
+        __syncthreads();
+    }
+    const int64_t page = slot >> a.page_shift;
+    const int64_t row = slot & ((int64_t(1) << a.page_shift) - 1);
+    // a task's lanes are in one warp and leave the loop together; whole
+    // warps stay for the butterfly, with idle tasks masked
+    for (int h0 = 0; h0 < tasks; h0 += step, h += step) {
+        const bool mine = h < tasks && live;
+        const int h_now = h;
+        uint4 na = make_uint4(0, 0, 0, 0), nb = na;   // the next task's loads run beside this one's work
+        if (h + step < tasks && live) {
+            const uint16_t* src = source(h + step);
+            na = *reinterpret_cast<const uint4*>(src + ea);
+            nb = *reinterpret_cast<const uint4*>(src + eb);
+        }
+        const bool is_v = h_now >= a.Hq + a.Hk;
+        if (turned && !is_v) {
+            float x[16], y[16];
+            unpack8<F16>(ua, x);
+            unpack8<F16>(ub, x + 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 c = cs[lane * 8 + i];
+                // pair i of the lane: (x[i], x[8 + i]) or (x[2i], x[2i + 1])
+                const float p0 = a.interleaved ? x[2 * i] : x[i], p1 = a.interleaved ? x[2 * i + 1] : x[8 + i];
+                const float r0 = p0 * c.x - p1 * c.y, r1 = p1 * c.x + p0 * c.y;
+                if (a.interleaved) {
+                    y[2 * i] = r0;
+                    y[2 * i + 1] = r1;
+                } else {
+                    y[i] = r0;
+                    y[8 + i] = r1;
+                }
+            }
+            ua = pack8<F16>(y);
+            ub = pack8<F16>(y + 8);
+        }
+        if (KV == kKvNone || h_now < a.Hq) {
+            if (mine) {
+                uint16_t* dst = h_now < a.Hq ? a.qo + t * a.ldqo + h_now * a.D : a.ko + t * a.ldko + (h_now - a.Hq) * a.D;
+                *reinterpret_cast<uint4*>(dst + ea) = ua;
+                *reinterpret_cast<uint4*>(dst + eb) = ub;
+            }
+        }
+        if (KV != kKvNone) {
+            const int g = is_v ? h_now - a.Hq - a.Hk : h_now - a.Hq;
+            const int64_t cell = ((page * a.Hk + g) << a.page_shift) + row;
+            const bool store = mine && h_now >= a.Hq && slot >= 0;
+            uint8_t* cache = is_v ? a.vcache : a.kcache;
+            if (KV == kKvX16) {
+                if (store) {
+                    uint16_t* dst = reinterpret_cast<uint16_t*>(cache) + cell * a.D;
+                    *reinterpret_cast<uint4*>(dst + ea) = ua;
+                    *reinterpret_cast<uint4*>(dst + eb) = ub;
+                }
+            } else {
+                // codes from the values rounded to 16 bits, as a separate write sees them
+                float x[16], m = 0.0f;
+                bool finite = true;
+                unpack8<F16>(ua, x);
+                unpack8<F16>(ub, x + 8);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    m = fmaxf(m, fabsf(x[i]));
+                    finite = finite && fabsf(x[i]) <= FLT_MAX;
+                }
+                if (!finite) m = __int_as_float(0x7f800000);   // marks the whole head
+#pragma unroll
+                for (int d = LANES / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                if (store) {
+                    const float top = KV == kKvE4m3 ? 448.0f : 127.0f;
+                    const bool bad = m > FLT_MAX;
+                    // m below top / FLT_MAX: the largest finite inverse keeps codes within the range
+                    const float inv = m > 0.0f && !bad ? fminf(__fdiv_rn(top, m), FLT_MAX) : 0.0f;
+                    if (bad) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+                    }
+                    uint8_t* dst = cache + cell * a.D;
+                    *reinterpret_cast<uint2*>(dst + ea) = encode8<KV>(x, inv);
+                    *reinterpret_cast<uint2*>(dst + eb) = encode8<KV>(x + 8, inv);
+                    if (lane == 0) (is_v ? a.vscale : a.kscale)[cell] = bad ? __int_as_float(0x7fc00000) : __fdiv_rn(m, top);
+                }
+            }
+        }
+        ua = na;
+        ub = nb;
+    }
+}
+
+struct ReadArgs {
+    int D, Hkv;
+    int64_t T;
+    const int64_t* slots;
+    int64_t capacity;
+    int page_shift;
+    const uint8_t* kcache;
+    const uint8_t* vcache;
+    const float* kscale;
+    const float* vscale;
+    uint16_t* k;
+    uint16_t* v;
+    int64_t ldk, ldv;
+};
+
+// 16 codes -> 16 values of x_type, code * factor in fp32 rounded once.
+template <bool F16, int KV>
+__device__ __forceinline__ void decode16(const uint4& u, float factor, uint4& lo, uint4& hi) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (KV == kKvE4m3) {
+            const float2 p = __half22float2(e4m3x2_to_half2(w[i] & 0xFFFFu)), r = __half22float2(e4m3x2_to_half2(w[i] >> 16));
+            x[4 * i] = p.x;
+            x[4 * i + 1] = p.y;
+            x[4 * i + 2] = r.x;
+            x[4 * i + 3] = r.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[4 * i + j] = static_cast<float>(static_cast<int8_t>((w[i] >> (8 * j)) & 0xFFu));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], factor);
+    lo = pack8<F16>(x);
+    hi = pack8<F16>(x + 8);
+}
+
+// Eight lanes per (token, keys or values, head), 16 elements each.
+template <bool F16, int KV>
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 7;
+    if (lane * 16 >= a.D) return;
+    const int per = 2 * a.Hkv;
+    const int64_t tasks = a.T * per, step = (int64_t)gridDim.x * (kReadThreads / 8);
+    for (int64_t i = (int64_t)blockIdx.x * (kReadThreads / 8) + (threadIdx.x >> 3); i < tasks; i += step) {
+        const int64_t t = i / per;
+        int g = static_cast<int>(i - t * per);
+        const bool is_v = g >= a.Hkv;
+        if (is_v) g -= a.Hkv;
+        const int64_t slot = a.slots[t];
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        if (slot >= 0 && slot < a.capacity) {
+            const int64_t cell = (((slot >> a.page_shift) * a.Hkv + g) << a.page_shift) +
+                                 (slot & ((int64_t(1) << a.page_shift) - 1));
+            const uint8_t* cache = is_v ? a.vcache : a.kcache;
+            if (KV == kKvX16) {
+                const uint4* src = reinterpret_cast<const uint4*>(cache + (cell * a.D + lane * 16) * 2);
+                lo = src[0];
+                hi = src[1];
+            } else {
+                const uint4 u = *reinterpret_cast<const uint4*>(cache + cell * a.D + lane * 16);
+                decode16<F16, KV>(u, (is_v ? a.vscale : a.kscale)[cell], lo, hi);
+            }
+        }
+        uint4* dst = reinterpret_cast<uint4*>((is_v ? a.v + t * a.ldv : a.k + t * a.ldk) + g * a.D + lane * 16);
+        dst[0] = lo;
+        dst[1] = hi;
+    }
+}
+
+template <int LANES, bool F16>
+cudaError_t launch_token(int kv, const TokenArgs& a, int64_t T, cudaStream_t stream) {
+    const int tasks = a.Hq + a.Hk + a.Hv;
+    const int64_t want = round_up((int64_t)tasks * LANES, 32);
+    const unsigned threads = static_cast<unsigned>(want < kMaxTokenThreads ? want : kMaxTokenThreads);
+    const dim3 grid(static_cast<unsigned>(T));
+    if constexpr (LANES == 8) {
+        if (kv == kKvX16) return launch_after(token_kernel<8, F16, kKvX16>, grid, threads, 0, stream, a);
+        if (kv == kKvE4m3) return launch_after(token_kernel<8, F16, kKvE4m3>, grid, threads, 0, stream, a);
+        if (kv == kKvI8) return launch_after(token_kernel<8, F16, kKvI8>, grid, threads, 0, stream, a);
+    }
+    return launch_after(token_kernel<LANES, F16, kKvNone>, grid, threads, 0, stream, a);
+}
+
+TokenArgs token_args(const RopeArgs& r) {
+    TokenArgs a = {};
+    a.pos = r.pos;
+    a.inv_freq = r.inv_freq;
+    a.amplitude = r.amplitude;
+    a.interleaved = r.interleaved ? 1 : 0;
+    a.D = r.D;
+    a.rot = r.rot;
+    a.Hq = r.Hq;
+    a.Hk = r.Hk;
+    a.q = r.q;
+    a.ldq = r.ldq;
+    a.qo = r.qo;
+    a.ldqo = r.ldqo;
+    a.k = r.k;
+    a.ldk = r.ldk;
+    a.ko = r.ko;
+    a.ldko = r.ldko;
+    return a;
+}
+
+}  // namespace
+
+cudaError_t launch_rope(bool x_f16, int64_t T, const RopeArgs& r, cudaStream_t stream) {
+    const TokenArgs a = token_args(r);
+    if (r.D <= 128)
+        return x_f16 ? launch_token<8, true>(kKvNone, a, T, stream) : launch_token<8, false>(kKvNone, a, T, stream);
+    return x_f16 ? launch_token<16, true>(kKvNone, a, T, stream) : launch_token<16, false>(kKvNone, a, T, stream);
+}
+
+cudaError_t launch_kv_write(bool x_f16, int64_t T, const RopeArgs& r, const uint16_t* v, int64_t ldv,
+                            const int64_t* slots, const KvCache& c, int32_t* err, cudaStream_t stream) {
+    TokenArgs a = token_args(r);
+    a.Hv = r.Hk;
+    a.v = v;
+    a.ldv = ldv;
+    a.slots = slots;
+    a.capacity = c.num_pages << c.page_shift;
+    a.page_shift = c.page_shift;
+    a.kcache = static_cast<uint8_t*>(const_cast<void*>(c.k));
+    a.vcache = static_cast<uint8_t*>(const_cast<void*>(c.v));
+    a.kscale = const_cast<float*>(c.kscale);
+    a.vscale = const_cast<float*>(c.vscale);
+    a.err = err;
+    return x_f16 ? launch_token<8, true>(c.kv, a, T, stream) : launch_token<8, false>(c.kv, a, T, stream);
+}
+
+template <bool F16>
+static cudaError_t launch_read(const ReadArgs& a, int kv, cudaStream_t stream) {
+    const int64_t blocks = ceil_div(a.T * 2 * a.Hkv, kReadThreads / 8);
+    const dim3 grid(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30)));
+    if (kv == kKvX16) return launch_after(kv_read_kernel<F16, kKvX16>, grid, kReadThreads, 0, stream, a);
+    if (kv == kKvE4m3) return launch_after(kv_read_kernel<F16, kKvE4m3>, grid, kReadThreads, 0, stream, a);
+    return launch_after(kv_read_kernel<F16, kKvI8>, grid, kReadThreads, 0, stream, a);
+}
+
+cudaError_t launch_kv_read(bool x_f16, int64_t T, int Hkv, int D, const int64_t* slots, const KvCache& c, uint16_t* k,
+                           int64_t ldk, uint16_t* v, int64_t ldv, cudaStream_t stream) {
+    const ReadArgs a = {D,   Hkv, T, slots, c.num_pages << c.page_shift, c.page_shift, static_cast<const uint8_t*>(c.k),
+                        static_cast<const uint8_t*>(c.v), c.kscale, c.vscale, k, v, ldk, ldv};
+    return x_f16 ? launch_read<true>(a, c.kv, stream) : launch_read<false>(a, c.kv, stream);
+}
+
+}  // namespace tern
