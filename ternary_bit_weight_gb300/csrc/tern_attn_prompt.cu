@@ -1,80 +1,769 @@
-// Attention over packed prompts.
+// Attention over packed prompts:
+//   O = softmax(scale Q K^T, keys a query may see) V.
 //
-// Plain form: one warp per (query row, head), each lane holding four of the
-// head's elements; keys are taken one after the other with a running maximum
-// and sum (the softmax's numerator and denominator are rescaled whenever the
-// maximum grows), all in fp32.
+// Mathematics.  One pass over the keys in tiles of 128 with the softmax in
+// base 2: a row keeps a reference m, l = sum 2^(s-m) and o = sum 2^(s-m) v
+// (s = scale log2(e) q.k), rescaled when m moves.  m follows the running
+// maximum lazily: it moves only when a tile's maximum passes it by 8, so
+// weights stay below 2^8 and the rescaling of o is rare.  Weights are rounded
+// to the 16-bit type for the product with V; l sums them unrounded in fp32.
+//
+// What bounds it: for long prompts the tensor cores (4 D flops per pair that
+// attends) and, beside them, the exponential of every score; for short ones
+// the launch and the chain load -> scores -> softmax -> values -> store.
+//
+// Rows of a tile.  A tile is `tok` tokens x `gs` of the heads that share one
+// key/value head, gs * tok <= 128 rows (gs = 1: 128 tokens of one head).  With
+// gs > 1 short sequences fill the tile with the group's heads; the host takes
+// the gs that needs the fewest tiles.  A CTA works on two tiles of consecutive
+// tokens against the same keys: while the softmax of one runs, the tensor
+// cores multiply for the other.
+//
+// Roles (12 warps):
+//   * warp 0 issues all tcgen05.mma: scores S_i = Q_i K_j^T (both operands in
+//     shared memory) into tensor memory, and O_i += P_i V_j with P_i in tensor
+//     memory over the columns of S_i (operations of one thread run in order,
+//     so S_i of the next tile follows the product that reads P_i);
+//   * warp 1 brings Q and the K and V tiles by TMA (128-byte swizzle);
+//   * warp 2 makes V tiles safe that hold keys some row must not see: 0 * NaN
+//     is NaN, so non-finite values there become 0 before the product, and the
+//     epilogue adds them to the rows that do see them;
+//   * warps 4-7 and 8-11, one warpgroup per tile and one thread per row:
+//     softmax, rescaling of O in tensor memory, epilogue.
+// Few rows against many keys: the keys are split over CTAs, which leave
+// (m, l, o) in the workspace for a second kernel that adds them in split order.
+// Every wait is bounded; a timeout raises the workspace error word.
 
+#include <cuda.h>
 #include <math_constants.h>
+#include <string.h>
+
+#include <mutex>
 
 #include "tern_attn.cuh"
 #include "tern_common.cuh"
 #include "tern_internal.h"
+#include "tern_sm100.cuh"
 
 namespace tern {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kMmaWarp = 0, kLoadWarp = 1, kGuardWarp = 2, kSoftWarp0 = 4;
+constexpr int kNT = 2;                        // tiles per CTA
+constexpr int kThreads = (kSoftWarp0 + 4 * kNT) * 32;
+constexpr int kTileM = 128, kTileN = 128;
+constexpr int kHalf = kTileM * 128;           // 128 rows x 64 elements of 16 bits
+constexpr int kSlots = 4;                     // K and V tiles, alternating: K in 0 and 2, V in 1 and 3
+static_assert(kSlots == 4, "two V slots: as many guarded tiles in flight");
+constexpr int kSCol = 0, kOCol = kNT * kTileN;
+constexpr int kTmemCols = 512;
+constexpr int kCtrlBytes = 256;
+constexpr float kLazy = 8.0f;
+constexpr float kNone = -1.0e38f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
+// Registers: 168 a thread at launch; the 128 threads of warps 0-3 give up 80
+// each for the 256 of the softmax (88 * 128 + 208 * 256 = 168 * 384).
+constexpr int kRegsLaunch = 168, kRegsUtil = 88, kRegsSoft = 208;
+static_assert(kRegsUtil * 128 + kRegsSoft * 128 * kNT <= kRegsLaunch * kThreads, "register split");
+
+// control block
+constexpr int kBarFull = 0;                          // [kSlots] tile landed
+constexpr int kBarEmpty = kBarFull + 8 * kSlots;     // [kSlots] tile consumed
+constexpr int kBarRaw = kBarEmpty + 8 * kSlots;      // [2] V tile landed that the guard looks over
+constexpr int kBarSafe = kBarRaw + 8 * 2;            // [2] and is ready
+constexpr int kBarQ = kBarSafe + 8 * 2;              // [kNT]
+constexpr int kBarS = kBarQ + 8 * kNT;               // [kNT] scores ready
+constexpr int kBarP = kBarS + 8 * kNT;               // [kNT] weights ready
+constexpr int kBarO = kBarP + 8 * kNT;               // [kNT] product with V done
+constexpr int kBarDrain = kBarO + 8 * kNT;
+constexpr int kTmemPtr = kBarDrain + 8;
+constexpr int kAbort = kTmemPtr + 4;
+constexpr int kBad = kAbort + 4;                     // a value was taken out by the guard
+static_assert(kBad + 4 <= kCtrlBytes, "control block");
+
+template <int DP>
+constexpr int smem_bytes() {
+    return 1024 + (kNT + kSlots) * (DP / 64) * kHalf + kCtrlBytes;
+}
+static_assert(smem_bytes<128>() <= 232448, "shared-memory budget");
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+struct Args {
+    const int32_t* cu_q;
+    const int32_t* cu_kv;
+    const uint16_t* v;
+    uint16_t* o;
+    float* lse;
+    float* part;          // split keys: [rows][splits][D] unnormalised outputs
+    float* part_ml;       // [rows][splits][2]: reference, sum
+    int* err;
+    int64_t ldv, ldo;
+    int B, Tq, Tkv, Hq, G, D;
+    int gs, tok, chunks;  // heads and tokens of a tile; chunks = ceil(G / gs)
+    int HC;               // key/value heads x chunks
+    int splits;
+    int causal;
+    float scale2;         // scale * log2(e)
+};
+
+// Where a block works: tokens [t0, t0 + kNT * tok) of sequence b, its rows of Q
+// from q0 and of K from k0.
+struct Item {
+    int q0, nq, k0, nk, t0;
+};
+
+__device__ __forceinline__ void clamp_range(const int32_t* cu, int b, int total, int& lo, int& n) {
+    lo = min(max(cu[b], 0), total);
+    n = max(0, min(max(cu[b + 1], 0), total) - lo);
+}
+
+// Block `index` of the sequences' token blocks in order; the blocks of a
+// sequence run from its end, whose causal rows see most keys.  One warp; false
+// past the last block.
+__device__ __forceinline__ bool find_item(const Args& a, int index, int lane, Item& it) {
+    int base = 0;
+    const int step = kNT * a.tok;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        int q0 = 0, nq = 0;
+        if (b0 + lane < a.B) clamp_range(a.cu_q, b0 + lane, a.Tq, q0, nq);
+        const int blocks = (nq + step - 1) / step;
+        int incl = blocks;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += up;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, base + incl > index);
+        if (past != 0) {
+            const int src = __ffs(past) - 1;
+            it.q0 = __shfl_sync(0xffffffffu, q0, src);
+            it.nq = __shfl_sync(0xffffffffu, nq, src);
+            const int end = base + __shfl_sync(0xffffffffu, incl, src);
+            it.t0 = (end - 1 - index) * step;
+            clamp_range(a.cu_kv, b0 + src, a.Tkv, it.k0, it.nk);
+            return true;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return false;
+}
+
+// Keys that token t of the item sees.
+__device__ __forceinline__ int visible(const Args& a, const Item& it, int t) {
+    return a.causal ? max(0, min(it.nk, t + 1 + it.nk - it.nq)) : it.nk;
+}
+
+// Wait for the phase with the given parity; false when *abort is set or after
+// kWaitTimeoutNs, in which case it sets *abort.  Inline, unlike mbar_wait: a
+// call would spill the row of scores that a softmax thread holds.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+    bool got = mbar_test_wait(bar, parity);
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !got; ++i) {
+        got = mbar_try_wait(bar, parity);
+        if (!got && (i & 15u) == 0) {
+            if (*abort) break;
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0) {
+                t0 = t;
+            } else if (t - t0 > kWaitTimeoutNs) {
+                *abort = 1;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, got);
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+// D[tmem] (+)= A[smem] . B[smem]^T
+__device__ __forceinline__ void umma_smem_a(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// MN-major operand in the 128-byte swizzle: rows of 64 elements along MN, one
+// per K index, in atoms of 8 rows (1024 bytes): stride (bits 32-45) 1024 bytes
+// between atoms along K, leading offset (16-29) between runs of 64 along MN.
+__device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t saddr, uint32_t next64) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((next64 >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+constexpr uint32_t kBMnMajor = 1u << 16;   // instruction descriptor: B is MN-major
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The non-finite halves of a word become 0 (bf16: exponent 0xFF; fp16: 0x1F).
 template <bool F16>
-__device__ __forceinline__ float4 load4(const uint16_t* p) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    const float2 a = unpack_x2<F16>(u.x), b = unpack_x2<F16>(u.y);
-    return make_float4(a.x, a.y, b.x, b.y);
+__device__ __forceinline__ uint32_t non_finite(uint32_t w) {
+    constexpr uint32_t ones = F16 ? 0x7C007C00u : 0x7F807F80u, one = F16 ? 0x04000400u : 0x00800080u;
+    return ((w & ones) + one) & 0x80008000u;   // no carry passes a half's top bit
 }
 
 template <bool F16>
-__global__ void __launch_bounds__(kWarps * 32) prompt_kernel(const PromptArgs a) {
+__device__ __forceinline__ bool value_non_finite(uint16_t u) {
+    constexpr uint16_t ones = F16 ? 0x7C00 : 0x7F80;
+    return (u & ones) == ones;
+}
+
+template <int DP, bool F16>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Maps maps,
+                                                             const __grid_constant__ Args a) {
+    constexpr int kHalves = DP / 64, kTileBytes = kHalves * kHalf;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t sq = smem_u32(smem), skv = sq + kNT * kTileBytes;
+    uint8_t* ctrl = smem + (kNT + kSlots) * kTileBytes;
+    const uint32_t cb = smem_u32(ctrl);
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(ctrl + kTmemPtr);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + kAbort);
+    volatile int* bad_flag = reinterpret_cast<volatile int*>(ctrl + kBad);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(cb + kBarFull + 8 * i, 1);
+            mbar_init(cb + kBarEmpty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(cb + kBarRaw + 8 * i, 1);
+            mbar_init(cb + kBarSafe + 8 * i, 1);
+        }
+        for (int i = 0; i < kNT; ++i) {
+            mbar_init(cb + kBarQ + 8 * i, 1);
+            mbar_init(cb + kBarS + 8 * i, 1);
+            mbar_init(cb + kBarP + 8 * i, 4);
+            mbar_init(cb + kBarO + 8 * i, 1);
+        }
+        mbar_init(cb + kBarDrain, 1);
+        *abort_flag = 0;
+        *bad_flag = 0;
+        mbar_fence_init();
+    }
+    if (warp == kLoadWarp && lane < 3) prefetch_tensormap(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v);
     grid_launch_dependents();
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t task = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int row = static_cast<int>(task / a.Hq), h = static_cast<int>(task % a.Hq);
-    if (row >= a.Tq) return;
-    int k0 = 0, k1 = -1;
-    for (int b = 0; b < a.B; ++b) {
-        const int q0 = min(max(a.cu_q[b], 0), a.Tq), q1 = min(max(a.cu_q[b + 1], 0), a.Tq);
-        if (row < q0 || row >= q1) continue;
-        k0 = min(max(a.cu_kv[b], 0), a.Tkv);
-        k1 = max(k0, min(max(a.cu_kv[b + 1], 0), a.Tkv));
-        if (a.causal) k1 = max(k0, min(k1, k0 + (k1 - k0) - (q1 - q0) + (row - q0) + 1));
-        break;
+    Item it;
+    const int hc = blockIdx.x % a.HC, rest = blockIdx.x / a.HC;
+    const int split = rest % a.splits, block = rest / a.splits;
+    if (!find_item(a, block, lane, it)) return;   // the whole CTA
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_ptr), kTmemCols);
+        tmem_relinquish();
     }
-    if (k1 < 0) return;   // a row of no sequence
-    const int g = h / (a.Hq / a.Hkv), d = lane * 4;
-    const bool live = d < a.D;
-    const float4 zero = make_float4(0, 0, 0, 0);
-    const float4 q = live ? load4<F16>(a.q + (int64_t)row * a.ldq + h * a.D + d) : zero;
-    float m = -CUDART_INF_F, l = 0.0f;
-    float4 o = zero;
-    for (int j = k0; j < k1; ++j) {
-        const float4 k = live ? load4<F16>(a.k + (int64_t)j * a.ldk + g * a.D + d) : zero;
-        const float4 v = live ? load4<F16>(a.v + (int64_t)j * a.ldv + g * a.D + d) : zero;
-        float s = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_ptr;
+
+    const int hk = hc / a.chunks, head0 = hk * a.G + (hc - hk * a.chunks) * a.gs;
+    const int heads = min(a.gs, (hk + 1) * a.G - head0);   // of the tile's gs, those that exist
+    // key tiles: tile i works on [j0, e[i])
+    int e[kNT], last[kNT];   // last: tokens of tile i
+    int most = 0;
 #pragma unroll
-        for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-        s *= a.scale;
-        const float mn = fmaxf(m, s);
-        const float keep = m == mn ? 1.0f : expf(m - mn), p = expf(s - mn);
-        m = mn;
-        l = l * keep + p;
-        o = make_float4(o.x * keep + p * v.x, o.y * keep + p * v.y, o.z * keep + p * v.z, o.w * keep + p * v.w);
+    for (int i = 0; i < kNT; ++i) {
+        last[i] = min(a.tok, it.nq - it.t0 - i * a.tok);
+        const int keys = last[i] > 0 ? visible(a, it, it.t0 + i * a.tok + last[i] - 1) : 0;
+        e[i] = (keys + kTileN - 1) / kTileN;
+        most = max(most, e[i]);
     }
-    const float inv = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : CUDART_NAN_F;
-    if (live)
-        *reinterpret_cast<uint2*>(a.o + (int64_t)row * a.ldo + h * a.D + d) =
-            make_uint2(pack_x2<F16>(o.x * inv, o.y * inv), pack_x2<F16>(o.z * inv, o.w * inv));
-    if (lane == 0 && a.lse != nullptr) a.lse[(int64_t)row * a.Hq + h] = l == 0.0f ? -CUDART_INF_F : m + logf(l);
+    int j0 = 0, j1 = most;
+    if (a.splits > 1) {
+        j0 = static_cast<int>(static_cast<int64_t>(most) * split / a.splits);
+        j1 = static_cast<int>(static_cast<int64_t>(most) * (split + 1) / a.splits);
+    }
+#pragma unroll
+    for (int i = 0; i < kNT; ++i) e[i] = max(j0, min(e[i], j1));
+    // first tile that holds a key which some row does not see
+    const int jm = visible(a, it, it.t0) / kTileN;
+    // guarded V tiles are jg, jg + 1, ...: they complete on barriers of their own,
+    // two in turn, which count guarded tiles only
+    const int jg = max(j0, jm);
+
+    // each side changes its registers inside its own branch: the compiler
+    // allocates by the path
+    if (warp < kSoftWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUtil));
+        if (warp == kLoadWarp) {
+            // ------------------------------------------------------------ loads
+            if (j1 > j0) {
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < kNT; ++i) {
+                        if (e[i] == j0) continue;
+                        mbar_arrive_expect_tx(cb + kBarQ + 8 * i, kHalves * a.gs * a.tok * 128);
+                        for (int h = 0; h < kHalves; ++h)
+                            tma_load_3d(sq + i * kTileBytes + h * kHalf, &maps.q, 64 * h, head0, it.q0 + it.t0 + i * a.tok,
+                                        cb + kBarQ + 8 * i);
+                    }
+                }
+                __syncwarp();
+                bool ok = true;
+                for (int n = 0; n < 2 * (j1 - j0) && ok; ++n) {   // K and V of each tile in turn
+                    const int slot = n % kSlots, round = n / kSlots;
+                    if (round > 0 && !(ok = warp_wait(cb + kBarEmpty + 8 * slot, (round - 1) & 1, abort_flag))) break;
+                    const int j = j0 + n / 2;
+                    const uint32_t bar = cb + ((n & 1) && j >= jm ? kBarRaw + 8 * ((j - jg) & 1) : kBarFull + 8 * slot);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(bar, kTileBytes);
+                        for (int h = 0; h < kHalves; ++h)
+                            tma_load_3d(skv + slot * kTileBytes + h * kHalf, n & 1 ? &maps.v : &maps.k, 64 * h, hk,
+                                        it.k0 + j * kTileN, bar);
+                    }
+                    __syncwarp();
+                }
+                if (*abort_flag) {   // copies in flight must land before the CTA ends
+                    volatile int no_abort = 0;
+                    for (int s = 0; s < kSlots; ++s) {
+                        (void)warp_wait(cb + kBarFull + 8 * s, 0, &no_abort);
+                        (void)warp_wait(cb + kBarFull + 8 * s, 1, &no_abort);
+                    }
+                    for (int s = 0; s < 2; ++s) {
+                        (void)warp_wait(cb + kBarRaw + 8 * s, 0, &no_abort);
+                        (void)warp_wait(cb + kBarRaw + 8 * s, 1, &no_abort);
+                    }
+                    for (int i = 0; i < kNT; ++i) (void)warp_wait(cb + kBarQ + 8 * i, 0, &no_abort);
+                }
+            }
+        } else if (warp == kMmaWarp) {
+            // -------------------------------------------------------------- MMA
+            const uint32_t type = F16 ? idesc_fp16_f32(128, 0) : idesc_bf16_f32(128, 0);
+            const uint32_t idesc_s = type | ((kTileN >> 3) << 17);
+            const uint32_t idesc_o = type | (static_cast<uint32_t>(a.D >> 3) << 17) | kBMnMajor;
+            const int steps = a.D / 16;
+            auto scores = [&](int i, int n) {   // S_i = Q_i K^T, K in load n
+                const uint64_t ad = smem_desc_kmajor_sw128(sq + i * kTileBytes);
+                const uint64_t bd = smem_desc_kmajor_sw128(skv + (n % kSlots) * kTileBytes);
+                if (elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < DP / 16; ++s)
+                        if (s < steps) {
+                            const uint32_t off = (s >> 2) * (kHalf / 16) + 2 * (s & 3);
+                            umma_smem_a(tmem + kSCol + i * kTileN, ad + off, bd + off, idesc_s, s > 0);
+                        }
+                    umma_commit(cb + kBarS + 8 * i);
+                }
+                __syncwarp();
+            };
+            bool ok = j1 > j0;
+            for (int i = 0; i < kNT && ok; ++i) {
+                if (e[i] == j0) continue;
+                ok = warp_wait(cb + kBarQ + 8 * i, 0, abort_flag) && warp_wait(cb + kBarFull, 0, abort_flag);
+                tc_fence_after_sync();
+                if (ok) scores(i, 0);
+            }
+            if (ok) {
+                if (elect_one()) umma_commit(cb + kBarEmpty);
+                __syncwarp();
+            }
+            for (int j = j0; j < j1 && ok; ++j) {
+                const int n = 2 * (j - j0) + 1, slot = n % kSlots;
+                const int kslot = (n + 1) % kSlots;
+                const uint32_t kph = ((n + 1) / kSlots) & 1;
+                // a guarded tile is ready when the guard says so
+                const uint32_t vbar = cb + (j >= jm ? kBarSafe + 8 * ((j - jg) & 1) : kBarFull + 8 * slot);
+                const uint32_t vph = j >= jm ? ((j - jg) >> 1) & 1 : (n / kSlots) & 1;
+                if (!(ok = warp_wait(vbar, vph, abort_flag))) break;
+                const uint64_t bd = smem_desc_mnmajor_sw128(skv + slot * kTileBytes, kHalf);
+#pragma unroll
+                for (int i = 0; i < kNT; ++i) {
+                    if (j >= e[i]) continue;
+                    if (!(ok = warp_wait(cb + kBarP + 8 * i, (j - j0) & 1, abort_flag))) break;
+                    tc_fence_after_sync();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int s = 0; s < kTileN / 16; ++s)   // 16 keys: 16 rows of 128 bytes
+                            umma_bf16_tmem_a(tmem + kOCol + i * DP, tmem + kSCol + i * kTileN + 8 * s, bd + s * (2048 / 16),
+                                             idesc_o, (j > j0 || s > 0) ? 1u : 0u);
+                        umma_commit(cb + kBarO + 8 * i);
+                    }
+                    __syncwarp();
+                    if (j + 1 < e[i]) {
+                        if (!(ok = warp_wait(cb + kBarFull + 8 * kslot, kph, abort_flag))) break;
+                        tc_fence_after_sync();
+                        scores(i, n + 1);
+                    }
+                }
+                if (!ok) break;
+                if (elect_one()) {
+                    umma_commit(cb + kBarEmpty + 8 * slot);
+                    if (j + 1 < j1) umma_commit(cb + kBarEmpty + 8 * kslot);
+                }
+                __syncwarp();
+            }
+            if (elect_one()) umma_commit(cb + kBarDrain);
+            __syncwarp();
+            volatile int no_abort = 0;
+            (void)warp_wait(cb + kBarDrain, 0, &no_abort);
+        } else if (warp == kGuardWarp) {
+            // ------------------------------------------------------------ guard
+            for (int j = jg; j < j1; ++j) {
+                const int slot = (2 * (j - j0) + 1) % kSlots, bar = 8 * ((j - jg) & 1);
+                if (!warp_wait(cb + kBarRaw + bar, ((j - jg) >> 1) & 1, abort_flag)) break;
+                uint4* tile = reinterpret_cast<uint4*>(smem + (kNT + slot) * kTileBytes);
+                uint32_t any = 0;
+#pragma unroll 8
+                for (int i = lane; i < kTileBytes / 16; i += 32) {
+                    const uint4 u = tile[i];
+                    any |= non_finite<F16>(u.x) | non_finite<F16>(u.y) | non_finite<F16>(u.z) | non_finite<F16>(u.w);
+                }
+                if (__any_sync(0xffffffffu, any != 0)) {
+                    uint16_t* value = reinterpret_cast<uint16_t*>(tile);
+                    for (int i = lane; i < kTileBytes / 2; i += 32)
+                        if (value_non_finite<F16>(value[i])) value[i] = 0;
+                    if (lane == 0) *bad_flag = 1;
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(cb + kBarSafe + bar);
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        const int i = (warp - kSoftWarp0) >> 2;
+        const int r = threadIdx.x & 127;                      // row = tensor-memory lane
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + kSCol + i * kTileN, to = tmem + lanes + kOCol + i * DP;
+        const int token = r / a.gs, head = r - token * a.gs;  // of the tile
+        const bool live = token < last[i] && head < heads;
+        const int t = it.t0 + i * a.tok + token;
+        const int lim = live ? visible(a, it, t) : 0;
+        const int end = i == 0 ? e[0] : e[kNT - 1];
+        const float scale2 = a.scale2;
+        float m = kNone, l = 0.0f;
+        bool ok = true;
+        for (int j = j0; j < end; ++j) {
+            if (!(ok = warp_wait(cb + kBarS + 8 * i, (j - j0) & 1, abort_flag))) break;
+            tc_fence_after_sync();
+            float s[kTileN];
+#pragma unroll
+            for (int c = 0; c < kTileN / 32; ++c) tmem_ld32_sync(ts + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
+            if (j >= jm) {
+                const int keys = lim - j * kTileN;   // keys of the tile that the row sees
+#pragma unroll
+                for (int c = 0; c < kTileN; ++c)
+                    if (c >= keys) s[c] = -CUDART_INF_F;
+            }
+            float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < kTileN; c += 8) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    top[q] = c + 4 + q < kTileN ? fmaxf(fmaxf(top[q], s[c + q]), s[c + 4 + q]) : fmaxf(top[q], s[c + q]);
+            }
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale2;
+            if (__any_sync(0xffffffffu, mx > m + kLazy)) {
+                const float up = fmaxf(m, mx), f = exp2_approx(m - up);
+                m = up;
+                l *= f;
+                if (j > j0) {
+                    if (!(ok = warp_wait(cb + kBarO + 8 * i, (j - j0 - 1) & 1, abort_flag))) break;
+                    tc_fence_after_sync();
+                    for (int c = 0; c < a.D; c += 16) {
+                        uint32_t u[16];
+                        tmem_ld16_sync(to + c, u);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(__uint_as_float(u[q]) * f);
+                        tmem_st_32x32b_x16(to + c, u);
+                    }
+                }
+            }
+            float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int h = 0; h < kTileN / 32; ++h) {
+                uint32_t p[16];
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    const float x = exp2_approx(fmaf(s[32 * h + c], scale2, -m));
+                    const float y = exp2_approx(fmaf(s[32 * h + c + 1], scale2, -m));
+                    sum[(c >> 1) & 3] += x + y;
+                    p[c >> 1] = pack_x2<F16>(x, y);
+                }
+                tmem_st_32x32b_x16(ts + 16 * h, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cb + kBarP + 8 * i);
+        }
+        // --------------------------------------------------------- epilogue
+        if (ok && end > j0) {
+            ok = warp_wait(cb + kBarO + 8 * i, (end - j0 - 1) & 1, abort_flag);
+            tc_fence_after_sync();
+        }
+        if (ok) {
+            const int64_t row = it.q0 + t;
+            const int h = head0 + head;
+            const bool bad = *bad_flag != 0;
+            const bool split_keys = a.splits > 1;
+            const int64_t prow = ((static_cast<int64_t>(block) * a.HC + hc) * kNT + i) * kTileM + r;
+            const float inv = split_keys ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : CUDART_NAN_F;
+            for (int c = 0; c < a.D; c += 16) {
+                uint32_t u[16];
+                if (end > j0) {
+                    tmem_ld16_sync(to + c, u);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 16; ++q) u[q] = 0;
+                }
+                float x[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(u[q]) * inv;
+                if (bad && live) {   // values taken out by the guard
+                    for (int key = jg * kTileN; key < min(lim, j1 * kTileN); ++key) {
+                        const uint16_t* src = a.v + (it.k0 + key) * a.ldv + static_cast<int64_t>(hk) * a.D + c;
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) {
+                            const uint32_t w = src[q];
+                            if (value_non_finite<F16>(static_cast<uint16_t>(w))) x[q] += unpack_x2<F16>(w).x;
+                        }
+                    }
+                }
+                if (split_keys) {
+                    float4* dst = reinterpret_cast<float4*>(a.part + (prow * a.splits + split) * a.D + c);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) dst[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                } else if (live) {
+                    uint4* dst = reinterpret_cast<uint4*>(a.o + row * a.ldo + static_cast<int64_t>(h) * a.D + c);
+                    dst[0] = make_uint4(pack_x2<F16>(x[0], x[1]), pack_x2<F16>(x[2], x[3]), pack_x2<F16>(x[4], x[5]),
+                                        pack_x2<F16>(x[6], x[7]));
+                    dst[1] = make_uint4(pack_x2<F16>(x[8], x[9]), pack_x2<F16>(x[10], x[11]), pack_x2<F16>(x[12], x[13]),
+                                        pack_x2<F16>(x[14], x[15]));
+                }
+            }
+            if (split_keys) {
+                *reinterpret_cast<float2*>(a.part_ml + (prow * a.splits + split) * 2) = make_float2(m, l);
+            } else if (live && a.lse != nullptr) {
+                a.lse[row * a.Hq + h] = l == 0.0f ? -CUDART_INF_F : m * kLn2 + logf(l);
+            }
+        }
+    }
+
+    // -------------------------------------------------------------- teardown
+    tc_fence_before_sync();
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) atomicOr(a.err, 1);
+    if (warp == 0) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Sum of the splits' partial results, one warp per row, in split order.
+constexpr int kCombineWarps = 8, kCombineRows = 32;
+template <bool F16>
+__global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Args a) {
+    grid_launch_dependents();
+    grid_dependency_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kParts = kNT * kTileM / kCombineRows;
+    const int64_t item = blockIdx.x / kParts;
+    const int r0 = (blockIdx.x % kParts) * kCombineRows;
+    const int hc = static_cast<int>(item % a.HC), block = static_cast<int>(item / a.HC);
+    Item it;
+    if (!find_item(a, block, lane, it)) return;
+    const int hk = hc / a.chunks, head0 = hk * a.G + (hc - hk * a.chunks) * a.gs;
+    const int heads = min(a.gs, (hk + 1) * a.G - head0);
+    for (int r = r0 + warp; r < r0 + kCombineRows; r += kCombineWarps) {
+        const int i = r / kTileM, rr = r % kTileM, token = rr / a.gs, head = rr - token * a.gs;
+        const int t = it.t0 + i * a.tok + token;
+        if (token >= a.tok || t >= it.nq || head >= heads) continue;
+        const int64_t prow = item * kNT * kTileM + r;
+        const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + prow * a.splits;
+        float M = kNone, L = 0.0f;
+        for (int s = 0; s < a.splits; ++s) M = fmaxf(M, ml[s].x);
+        float4 sum = make_float4(0, 0, 0, 0);
+        const int d = lane * 4;
+        for (int s = 0; s < a.splits; ++s) {
+            const float f = exp2_approx(ml[s].x - M);
+            L += ml[s].y * f;
+            if (d < a.D) {
+                const float4 u = *reinterpret_cast<const float4*>(a.part + (prow * a.splits + s) * a.D + d);
+                // a split that the row sees nothing of adds nothing
+                if (ml[s].y != 0.0f) sum.x += u.x * f, sum.y += u.y * f, sum.z += u.z * f, sum.w += u.w * f;
+            }
+        }
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+        const int64_t row = it.q0 + t;
+        const int h = head0 + head;
+        if (d < a.D)
+            *reinterpret_cast<uint2*>(a.o + row * a.ldo + static_cast<int64_t>(h) * a.D + d) =
+                make_uint2(pack_x2<F16>(sum.x * inv, sum.y * inv), pack_x2<F16>(sum.z * inv, sum.w * inv));
+        if (lane == 0 && a.lse != nullptr) a.lse[row * a.Hq + h] = L == 0.0f ? -CUDART_INF_F : M * kLn2 + logf(L);
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// Heads [rows, ld] as a [rows][heads][D] tensor; a box is 64 elements x
+// `box_heads` heads x `box_rows` rows.
+bool encode_heads(CUtensorMap* map, bool f16, const uint16_t* p, int64_t rows, int64_t ld, int heads, int D, int box_heads,
+                  int box_rows) {
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(ld) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode_tiled_fn()(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                             const_cast<uint16_t*>(p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Plan {
+    int gs, tok, chunks, HC, splits;
+    int64_t blocks;   // token blocks, at most
+    size_t off_part, off_ml, ws_bytes;
+};
+
+Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, int64_t D, int sm_count) {
+    Plan p = {};
+    const int64_t G = Hq / Hkv, avg_q = ceil_div(Tq, B), avg_k = Tkv / B;
+    // fewest tiles for sequences of the average length; of equals, the most heads
+    int64_t best = INT64_MAX;
+    for (int64_t gs = G < 128 ? G : 128; gs >= 1; --gs) {
+        const int64_t tok = kTileM / gs, tiles = ceil_div(avg_q, tok) * ceil_div(G, gs);
+        if (tiles < best) {
+            best = tiles;
+            p.gs = static_cast<int>(gs);
+            p.tok = static_cast<int>(tok);
+        }
+    }
+    p.chunks = static_cast<int>(ceil_div(G, p.gs));
+    p.HC = static_cast<int>(Hkv) * p.chunks;
+    p.blocks = Tq / (kNT * p.tok) + B;
+    if (p.blocks > Tq) p.blocks = Tq;
+    // split the keys when the blocks fill less than half of the SMs, a split
+    // keeping at least four key tiles
+    const int64_t items = B * ceil_div(avg_q, kNT * p.tok) * p.HC;
+    int64_t splits = 1;
+    if (2 * items <= sm_count) {
+        splits = sm_count / items;
+        const int64_t most = avg_k / (4 * kTileN);
+        if (splits > most) splits = most;
+        if (splits < 1) splits = 1;
+    }
+    p.splits = static_cast<int>(splits);
+    size_t off = kWorkspaceErrBytes;
+    p.off_part = p.off_ml = off;
+    if (splits > 1) {
+        const int64_t rows = p.blocks * p.HC * kNT * kTileM * splits;
+        off += static_cast<size_t>(rows * D) * sizeof(float);
+        p.off_ml = off;
+        off += static_cast<size_t>(rows) * 2 * sizeof(float);
+    }
+    p.ws_bytes = off;
+    return p;
+}
+
+template <int DP, bool F16>
+cudaError_t launch_tiles(const Maps& maps, const Args& a, int64_t grid, cudaStream_t stream) {
+    static const cudaError_t limit =
+        cudaFuncSetAttribute(prompt_kernel<DP, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
+    if (limit != cudaSuccess) return limit;
+    cudaError_t e = launch_after(prompt_kernel<DP, F16>, dim3(static_cast<unsigned>(grid)), kThreads, smem_bytes<DP>(),
+                                 stream, maps, a);
+    if (e != cudaSuccess || a.splits == 1) return e;
+    const int64_t combine = grid / a.splits * (kNT * kTileM / kCombineRows);
+    return launch_after(combine_kernel<F16>, dim3(static_cast<unsigned>(combine)), kCombineWarps * 32, 0, stream, a);
 }
 
 }  // namespace
 
-size_t prompt_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int) { return kWorkspaceErrBytes; }
+size_t prompt_ws_bytes(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, int64_t D, int sm_count) {
+    return plan_prompt(B, Tq, Tkv, Hq, Hkv, D, sm_count < 1 ? 1 : sm_count).ws_bytes;
+}
 
-cudaError_t launch_prompt(bool x_f16, const PromptArgs& a, void*, int, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(ceil_div((int64_t)a.Tq * a.Hq, kWarps)));
-    return x_f16 ? launch_after(prompt_kernel<true>, grid, kWarps * 32, 0, stream, a)
-                 : launch_after(prompt_kernel<false>, grid, kWarps * 32, 0, stream, a);
+cudaError_t launch_prompt(bool x_f16, const PromptArgs& pa, void* ws, int sm_count, cudaStream_t stream) {
+    const Plan p = plan_prompt(pa.B, pa.Tq, pa.Tkv, pa.Hq, pa.Hkv, pa.D, sm_count);
+    const int64_t grid = p.blocks * p.HC * p.splits;
+    if (grid > INT32_MAX / 8) return cudaErrorInvalidValue;
+    if (encode_tiled_fn() == nullptr) return cudaErrorNotSupported;
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    bool ok = encode_heads(&maps.q, x_f16, pa.q, pa.Tq, pa.ldq, pa.Hq, pa.D, p.gs, p.tok);
+    if (pa.Tkv > 0) {   // without keys there is nothing to load
+        ok = ok && encode_heads(&maps.k, x_f16, pa.k, pa.Tkv, pa.ldk, pa.Hkv, pa.D, 1, kTileN);
+        ok = ok && encode_heads(&maps.v, x_f16, pa.v, pa.Tkv, pa.ldv, pa.Hkv, pa.D, 1, kTileN);
+    } else {
+        maps.k = maps.v = maps.q;
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    Args a = {};
+    a.cu_q = pa.cu_q;
+    a.cu_kv = pa.cu_kv;
+    a.v = pa.v;
+    a.o = pa.o;
+    a.lse = pa.lse;
+    a.part = reinterpret_cast<float*>(w + p.off_part);
+    a.part_ml = reinterpret_cast<float*>(w + p.off_ml);
+    a.err = reinterpret_cast<int*>(w);
+    a.ldv = pa.ldv;
+    a.ldo = pa.ldo;
+    a.B = pa.B;
+    a.Tq = pa.Tq;
+    a.Tkv = pa.Tkv;
+    a.Hq = pa.Hq;
+    a.G = pa.Hq / pa.Hkv;
+    a.D = pa.D;
+    a.gs = p.gs;
+    a.tok = p.tok;
+    a.chunks = p.chunks;
+    a.HC = p.HC;
+    a.splits = p.splits;
+    a.causal = pa.causal ? 1 : 0;
+    // a scale of zero as the smallest normal: products stay zero, and keys that
+    // are not seen stay at minus infinity
+    a.scale2 = fmaxf(pa.scale * kLog2e, 1.17549435e-38f);
+    if (pa.D > 64) return x_f16 ? launch_tiles<128, true>(maps, a, grid, stream) : launch_tiles<128, false>(maps, a, grid, stream);
+    return x_f16 ? launch_tiles<64, true>(maps, a, grid, stream) : launch_tiles<64, false>(maps, a, grid, stream);
 }
 
 }  // namespace tern
