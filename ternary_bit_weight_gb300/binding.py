@@ -168,10 +168,25 @@ def _p(x):
     return x.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """cudaStream_t of torch's current stream.  Through torch's raw-stream
+    lookup, 0.1 us: building a ``torch.cuda.Stream`` object takes 3 us, a third
+    of a small call's time on the host."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.init()
+        get, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _raw_stream = lambda: get(device())  # noqa: E731
+    return _raw_stream()
+
+
 def _s(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
