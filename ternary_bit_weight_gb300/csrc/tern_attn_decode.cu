@@ -19,23 +19,33 @@
 // Work.  A unit is a tile of 16 keys of one (sequence, key/value head); all
 // units in that order are cut into equal contiguous ranges, one per CTA, so
 // unequal lengths load the SMs equally.  Within a CTA a segment (the part of
-// one item in its range) is dealt to the 8 warps tile by tile; at its end the
+// one item in its range) is dealt to the warps tile by tile; at its end the
 // warps' (m, l, o) meet in shared memory.  An item inside one CTA is then
 // finished; otherwise the CTAs leave partial results in the workspace and the
 // last to arrive adds them in CTA order (the result does not depend on
 // timing).
 //
-// A warp's tile goes global -> shared by cp.async in a ring of its own, each
-// lane writing and reading back its own 16-byte runs: no barrier and no bank
-// conflict, and the ring holds what a memory latency needs beside the
-// registers.  The products are mma.sync m16n8k16: heads are the 16 rows, keys
-// the columns, and the score fragment of a thread is its weight fragment for
-// the product with V.  The order of dimensions inside a product is free, so
-// each thread multiplies the dimensions it has loaded: keys need no
-// transposition, values only a byte or half-word interleave of two rows.
-// (tcgen05 would take 128-row tiles of which 1 to 16 rows exist here.)
+// A warp's tiles land in a ring of its own, so warps never wait for one
+// another inside a segment.  Pages of 16 tokens and more hold a tile as one
+// block: two TMA copies per 128 bytes of a row's width bring it, 128-byte
+// swizzled, issued by one lane.  (A copy per lane and 16 bytes instead costs
+// some 60 instructions of a tile's 500 and fills the load/store queue.)
+// Smaller pages take that per-lane form, cp.async to the same layout.
+//
+// The products are mma.sync m16n8k16 with the heads as the 8 columns:
+// S^T = K q^T (16 keys x 8 heads), then o^T += V^T P^T (16 dimensions x 8
+// heads), P transposed between the two by movmatrix.  With the heads as the 16
+// rows instead, half of every product and accumulator is empty for groups of
+// up to 8 heads.  The order of dimensions inside a product is free, so each
+// thread multiplies the dimensions it has loaded: keys need no transposition,
+// values only a byte or half-word interleave of two rows.  The order of keys in
+// a tile is free too: kKey picks it so that the reads of keys and of values
+// both meet every bank once.  (tcgen05 would take 128-row tiles of which 1 to
+// 16 rows exist here.)
 
+#include <cuda.h>
 #include <math_constants.h>
+#include <string.h>
 
 #include "tern_attn.cuh"
 #include "tern_common.cuh"
@@ -45,10 +55,9 @@
 namespace tern {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;              // keys per unit
 constexpr int kRows = 16;              // query heads per pass over the keys
+constexpr int kMinTiles = 8;           // of a CTA's range, where there are fewer CTAs than SMs
 constexpr float kLazy = 8.0f;          // how far a score may pass the reference
 constexpr float kNone = -1.0e38f;      // reference before any key
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
@@ -64,6 +73,7 @@ struct Args {
     const uint16_t* q;
     uint16_t* o;
     float* lse;
+    int* err;
     int32_t* arrived;      // [grid], zero between calls
     float* slots;          // [2 * grid] partial results
     int64_t ldq, ldo, max_pages, num_pages;
@@ -71,39 +81,75 @@ struct Args {
     int B, D, G;           // G query heads share a key/value head
     int Hkv, passes, Hv;   // Hv = Hkv * passes: (key/value head, 16 of its query heads)
     int shift;
+    int tma;               // tiles come by TMA (else a copy per lane)
     float scale2;          // scale * log2(e)
 };
 
-template <int DP, int KV>
+struct Maps {
+    CUtensorMap k, v;
+};
+
+
+// Key of the tile at row g (or slot g) of a product's 8-key half.  Rows are
+// 128 bytes, their 16-byte runs swizzled by the row: run c of row r is at
+// c ^ (r mod 8).  Keys are read as runs 0-3 (or 4-7) of rows kKey(2i) and
+// kKey(2i + 1) together, which must differ in bit 2; values as runs 2i, 2i + 1
+// of the four rows kKey(0, 2, 4, 6) (or 1, 3, 5, 7), which must differ above
+// bit 0.
+__device__ __forceinline__ int key_at(int g) { return (0x37156240u >> (4 * g)) & 7; }   // 0 4 2 6 5 1 7 3
+
+// COLS: columns of heads, 8 each (1 for groups of up to 8 heads, else 2).
+template <int DP, int KV, int COLS>
 struct Shape {
     static constexpr int kElem = KV == kKvX16 ? 2 : 1;
+    // Coded tiles are half the bytes and take twice the instructions per byte:
+    // 16 warps of 128 registers; the wider forms need the registers of 8.
+    static constexpr int kWarps = KV != kKvX16 && COLS == 1 ? 16 : 8;
+    static constexpr int kThreads = kWarps * 32;
     static constexpr int kRowBytes = DP * kElem;
+    static constexpr int kWidth = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one block of the tile
+    static constexpr int kBlocks = kRowBytes / kWidth;
     static constexpr int kKPieces = kRowBytes / 64;                   // 16-byte runs per lane and key row
     static constexpr int kVRun = kRowBytes / 8 < 16 ? kRowBytes / 8 : 16;
     static constexpr int kVPieces = kRowBytes / 8 / kVRun;            // runs per lane and value row
     static constexpr int kKBytes = kTile * kRowBytes;
+    static constexpr int kStage = 2 * kKBytes;
     static constexpr int kScaleBytes = KV == kKvX16 ? 0 : 2 * kTile * 4;
-    static constexpr int kStage = 2 * kKBytes + kScaleBytes + 16;     // + mask of the keys that exist
-    static constexpr int kSteps = DP / 16;                            // K-steps of a score
-    static constexpr int kCols = DP / 8;                              // column tiles of the output
-    static constexpr int kMergeLd = DP + 4;
-    static constexpr int kMerge = kWarps * 8 * kMergeLd * 4;
-    static constexpr int kStat = kWarps * kRows * 3 * 4;
-    static constexpr int kFit = (kSmemMax - kMerge - kStat - 16) / (kWarps * kStage);
-    static constexpr int kStages = kFit < 6 ? kFit : 6;
-    static constexpr int kSmem = kWarps * kStages * kStage + kMerge + kStat + 16;
-    static_assert(kStages >= 3, "ring depth");
-    // dimension of output column n (0..7) in column tile j
-    static __device__ __forceinline__ int dim(int n, int j) {
-        constexpr int run = KV == kKvX16 ? 8 : DP / 8;
-        return (j / run) * 64 + n * run + j % run;
+    static constexpr int kSteps = DP / 16;                            // K-steps of a score, row tiles of the output
+    static constexpr int kMerge = kWarps * 8 * DP * 4;
+    static constexpr int kStat = kWarps * 8 * COLS * 3 * 4;
+    static constexpr int kFit = (kSmemMax - 1024 - kMerge - kStat - 16) / (kWarps * (kStage + kScaleBytes + 8));
+    static constexpr int kStages = kFit < 4 ? kFit : 4;
+    static constexpr int kSmem = 1024 + kWarps * kStages * (kStage + kScaleBytes + 8) + kMerge + kStat + 16;
+    static constexpr int kEach = 8 * DP / kThreads;                   // merged elements per thread
+    static_assert(kStages >= 2 && kEach >= 1 && kSmem <= kSmemMax, "shape");
+    // Dimension of row g (half 0) or g + 8 (half 1) of output row tile j: a
+    // thread's dimensions are those of the value runs it loads.
+    static __device__ __forceinline__ int dim(int g, int half, int j) {
+        return KV == kKvX16 && DP == 128 ? 64 * half + 8 * g + j : (DP / 8) * g + (DP / 16) * half + j;
+    }
+    // Byte `at` (a multiple of 16, or 8 in narrow rows) of a row of the tile.
+    static __device__ __forceinline__ int place(int row, int at) {
+        if (kWidth < 128) return row * kWidth + at;
+        return (at >> 7) * (kTile * 128) + row * 128 + ((at & 127) ^ ((row & 7) << 4));
+    }
+    // Element d of a head's row in a warp's merge block (spread over the banks).
+    static __device__ __forceinline__ int merge_at(int row, int d) {
+        return row * DP + ((((d >> 2) ^ (row >> 1)) << 2) | (d & 3));
     }
 };
 
-__host__ __device__ constexpr int slot_floats(int DP, int rows) { return rows * DP + 3 * kRows; }
+__host__ __device__ constexpr int slot_floats(int DP, int rows) { return rows * (DP + 3); }
 
 template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_async_or_zero(uint32_t dst, const void* src, bool there) {
     const int n = there ? BYTES : 0;   // the rest is filled with zeros
     if constexpr (BYTES == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -126,6 +172,14 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values, thread (g, t) holding
+// elements 2t, 2t + 1 of row g.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -228,19 +282,34 @@ struct Request {
     int tile;        // -1: none
 };
 
-template <int DP, int KV, bool F16, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a) {
-    using S = Shape<DP, KV>;
+template <int DP, int KV, bool F16, int COLS>
+__global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, 1) decode_kernel(const __grid_constant__ Maps maps,
+                                                                                const __grid_constant__ Args a) {
+    using S = Shape<DP, KV, COLS>;
     constexpr bool kCoded = KV != kKvX16;
     constexpr bool kMma16 = kCoded || F16;       // products in fp16 (else bf16)
-    constexpr int kR = WIDE ? 2 : 1;             // rows per thread: head g, and g + 8
-    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kSlotRows = 8 * COLS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kStage;
-    uint8_t* ring_ptr = smem + warp * S::kStages * S::kStage;
-    float* merge = reinterpret_cast<float*>(smem + kWarps * S::kStages * S::kStage);
+    uint8_t* ring = smem + warp * S::kStages * S::kStage;
+    uint8_t* factors = smem + kWarps * S::kStages * S::kStage + warp * S::kStages * S::kScaleBytes;
+    float* merge = reinterpret_cast<float*>(smem + kWarps * S::kStages * (S::kStage + S::kScaleBytes));
     float* stat = merge + S::kMerge / 4;         // [warp][row][m, mo, l]
-    volatile int* last_flag = reinterpret_cast<volatile int*>(stat + S::kStat / 4);
+    const uint32_t bars = smem_u32(stat + S::kStat / 4) + warp * S::kStages * 8;   // a warp's stages
+    volatile int* last_flag = reinterpret_cast<volatile int*>(reinterpret_cast<uint8_t*>(stat) + S::kStat +
+                                                             kWarps * S::kStages * 8);
+    volatile int* abort_flag = last_flag + 1;
+    if (threadIdx.x == 0) *abort_flag = 0;
+    if (lane == 0) {
+        for (int i = 0; i < S::kStages; ++i) mbar_init(bars + 8 * i, 1);
+        mbar_fence_init();
+    }
+    if (threadIdx.x == 0 && a.tma) {
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
+    }
+    __syncthreads();
 
     grid_launch_dependents();
     grid_dependency_wait();
@@ -256,9 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a) {
                 a.lse[static_cast<int64_t>(b) * a.Hkv * a.G + h] = -CUDART_INF_F;
     }
 
-    // a CTA's range holds a tile for every warp, or there are fewer CTAs
+    // a CTA's range holds a tile for each of 8 warps, or there are fewer CTAs
     const int64_t U = total_units(a, lane);
-    const int64_t V = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), (U + kWarps - 1) / kWarps));
+    const int64_t V = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), (U + kMinTiles - 1) / kMinTiles));
     if (blockIdx.x >= V || U == 0) return;
     const int64_t u0 = U * blockIdx.x / V, u1 = U * (blockIdx.x + 1) / V;
     Segment seg = first_segment(a, u0, u1, lane);
@@ -288,45 +357,60 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a) {
         return r;
     };
     const int bytes = a.D * S::kElem;
-    auto issue = [&](const Request& r, int stage) {
+    const int page_mask = (1 << a.shift) - 1;
+    uint64_t masks = 0;   // 16 bits per tile in flight: its keys that exist
+    auto issue = [&](const Request& r, int stage, int ahead) {
+        uint32_t mask = 0;
         if (r.tile >= 0) {
-            const uint32_t st = ring + stage * S::kStage;
+            const uint32_t st = smem_u32(ring + stage * S::kStage), fs = smem_u32(factors + stage * S::kScaleBytes);
             const int key0 = r.tile * kTile;
-            // cell of the lane's key (lane mod 16), negative where there is none
-            const int key = key0 + (lane & 15);
-            int64_t cell = -1;
-            if (key < r.len && r.page >= 0 && r.page < a.num_pages)
-                cell = ((static_cast<int64_t>(r.page) * a.Hkv + r.hk) << a.shift) + (key & ((1 << a.shift) - 1));
-            const uint32_t mask = __ballot_sync(0xffffffffu, cell >= 0) & 0xFFFFu;
+            if (a.tma) {
+                // a tile lies in one page
+                const bool there = r.page >= 0 && r.page < a.num_pages;
+                mask = there ? 0xFFFFu >> max(0, key0 + kTile - r.len) : 0u;
+                const uint32_t bar = bars + 8 * stage;
+                const int pos = r.page * a.Hkv + r.hk, row = key0 & page_mask;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, there ? S::kStage + S::kScaleBytes : 0);
+                    if (there) {
 #pragma unroll
-            for (int r8 = 0; r8 < 2; ++r8) {
-                const int64_t c = __shfl_sync(0xffffffffu, cell, g + 8 * r8);
+                        for (int i = 0; i < S::kBlocks; ++i) {
+                            tma_load_3d(st + i * kTile * S::kWidth, &maps.k, i * (S::kWidth / S::kElem), row, pos, bar);
+                            tma_load_3d(st + S::kKBytes + i * kTile * S::kWidth, &maps.v, i * (S::kWidth / S::kElem), row, pos, bar);
+                        }
+                        if constexpr (kCoded) {
+                            const int64_t cell = (static_cast<int64_t>(pos) << a.shift) + row;
+                            bulk_load(fs, a.kscale + cell, kTile * 4, bar);
+                            bulk_load(fs + kTile * 4, a.vscale + cell, kTile * 4, bar);
+                        }
+                    }
+                }
+                __syncwarp();
+            } else {
+                // cell of the lane's key (lane mod 16), negative where there is none
+                const int key = key0 + (lane & 15);
+                int64_t cell = -1;
+                if (key < r.len && r.page >= 0 && r.page < a.num_pages)
+                    cell = ((static_cast<int64_t>(r.page) * a.Hkv + r.hk) << a.shift) + (key & page_mask);
+                mask = __ballot_sync(0xffffffffu, cell >= 0) & 0xFFFFu;
+                constexpr int kRuns = S::kRowBytes / 16, kAtOnce = 32 / kRuns;   // rows per step
 #pragma unroll
-                for (int i = 0; i < S::kKPieces; ++i) {
-                    const int off = (i * 4 + t) * 16;
-                    const bool there = c >= 0 && off < bytes;
-                    copy_async<16>(st + ((i * 2 + r8) * 32 + lane) * 16, there ? a.k + c * bytes + off : a.k, there);
+                for (int i = 0; i < kTile / kAtOnce; ++i) {
+                    const int row = i * kAtOnce + lane / kRuns, at = (lane % kRuns) * 16;
+                    const int64_t c = __shfl_sync(0xffffffffu, cell, row);
+                    const bool there = c >= 0 && at < bytes;
+                    const int dst = S::place(row, at);
+                    copy_async_or_zero<16>(st + dst, there ? a.k + c * bytes + at : a.k, there);
+                    copy_async_or_zero<16>(st + S::kKBytes + dst, there ? a.v + c * bytes + at : a.v, there);
+                }
+                if constexpr (kCoded) {
+                    const float* src = lane < 16 ? a.kscale : a.vscale;
+                    copy_async_or_zero<4>(fs + lane * 4, cell >= 0 ? src + cell : src, cell >= 0);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t c = __shfl_sync(0xffffffffu, cell, 2 * t + (j & 1) + 8 * (j >> 1));
-#pragma unroll
-                for (int i = 0; i < S::kVPieces; ++i) {
-                    const int off = i * 128 + g * S::kVRun;
-                    const bool there = c >= 0 && off < bytes;
-                    copy_async<S::kVRun>(st + S::kKBytes + ((j * S::kVPieces + i) * 32 + lane) * S::kVRun,
-                                         there ? a.v + c * bytes + off : a.v, there);
-                }
-            }
-            if constexpr (kCoded) {
-                const float* src = lane < 16 ? a.kscale : a.vscale;
-                copy_async<4>(st + 2 * S::kKBytes + lane * 4, cell >= 0 ? src + cell : src, cell >= 0);
-            }
-            if (lane == 0)
-                *reinterpret_cast<uint32_t*>(ring_ptr + stage * S::kStage + 2 * S::kKBytes + S::kScaleBytes) = mask;
         }
-        copy_commit();
+        if (!a.tma) copy_commit();
+        masks |= static_cast<uint64_t>(mask) << (16 * ahead);
     };
 
     Request next = request();
@@ -334,9 +418,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a) {
     for (int i = 0; i < S::kStages - 1; ++i) {
         const Request now = next;
         next = request();
-        issue(now, i);
+        issue(now, i, i);
     }
+    const int kr = key_at(g);   // keys kr and kr + 8 are the thread's rows of the scores
+    const int vr[4] = {key_at(2 * t), key_at(2 * t + 1), key_at(2 * t) + 8, key_at(2 * t + 1) + 8};
     int stage = 0, fill = S::kStages - 1;
+    uint32_t phase = 0;
 
     // ------------------------------------------------------------ segments
     for (bool first = true;; first = false) {
@@ -345,21 +432,24 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a) {
         const int head0 = (seg.hv - hk * a.passes) * kRows;               // first of the group's heads
         const int heads = min(kRows, a.G - head0);
         const int64_t q_head = static_cast<int64_t>(hk) * a.G + head0;
-        float m[kR], mo[kR], l[kR], fac[kR];
-        float o[S::kCols][4];
-        uint32_t qa[S::kSteps][4];
+        // the thread's heads: 8c + 2t, 8c + 2t + 1
+        float m[COLS][2], mo[COLS][2], l[COLS][2], fac[COLS][2];
+        float o[COLS][S::kSteps][4];
+        uint32_t qb[COLS][S::kSteps][2];
         const bool mine = seg.begin + warp < seg.end;
         if (mine) {
-            // queries: the four dimensions of each K-step that the thread's key runs hold
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                uint2 u[S::kSteps];
-                const bool live = r < kR && g + 8 * r < heads;
-                const uint16_t* src = a.q + seg.b * a.ldq + (q_head + g + 8 * r) * a.D;
+            for (int c = 0; c < COLS; ++c) {
+                // queries of head 8c + g: the four dimensions of each K-step that the
+                // thread's key runs hold
+                const bool live = 8 * c + g < heads;
+                const uint16_t* src = a.q + seg.b * a.ldq + (q_head + 8 * c + g) * a.D;
 #pragma unroll
                 for (int w = 0; w < S::kSteps; ++w) {
                     const int d = kCoded ? ((w / 4) * 4 + t) * 16 + (w % 4) * 4 : ((w / 2) * 4 + t) * 8 + (w % 2) * 4;
-                    u[w] = live && d < a.D ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0, 0);
+                    const uint2 u = live && d < a.D ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0, 0);
+                    qb[c][w][0] = u.x;
+                    qb[c][w][1] = u.y;
                 }
                 float f = a.scale2;
                 if constexpr (kCoded) {
@@ -367,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a) {
                     float top = 0.0f;
 #pragma unroll
                     for (int w = 0; w < S::kSteps; ++w) {
-                        const float2 x = unpack_x2<F16>(u[w].x), y = unpack_x2<F16>(u[w].y);
+                        const float2 x = unpack_x2<F16>(qb[c][w][0]), y = unpack_x2<F16>(qb[c][w][1]);
                         top = fmaxf(top, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y))));
                     }
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -378,144 +468,166 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a) {
                     f = f * exp2f(static_cast<float>(-(e / 2))) * exp2f(static_cast<float>(-(e - e / 2)));
 #pragma unroll
                     for (int w = 0; w < S::kSteps; ++w) {
-                        const float2 x = unpack_x2<F16>(u[w].x), y = unpack_x2<F16>(u[w].y);
-                        u[w].x = pack_x2<true>(x.x * up0 * up1, x.y * up0 * up1);
-                        u[w].y = pack_x2<true>(y.x * up0 * up1, y.y * up0 * up1);
+                        const float2 x = unpack_x2<F16>(qb[c][w][0]), y = unpack_x2<F16>(qb[c][w][1]);
+                        qb[c][w][0] = pack_x2<true>(x.x * up0 * up1, x.y * up0 * up1);
+                        qb[c][w][1] = pack_x2<true>(y.x * up0 * up1, y.y * up0 * up1);
                     }
                 }
 #pragma unroll
-                for (int w = 0; w < S::kSteps; ++w) {
-                    qa[w][r] = u[w].x;
-                    qa[w][2 + r] = u[w].y;
+                for (int h = 0; h < 2; ++h) {
+                    fac[c][h] = kCoded ? __shfl_sync(0xffffffffu, f, 4 * (2 * t + h)) : f;
+                    m[c][h] = mo[c][h] = kNone;
+                    l[c][h] = 0.0f;
                 }
-                if (r < kR) {
-                    fac[r] = f;
-                    m[r] = mo[r] = kNone;
-                    l[r] = 0.0f;
-                }
+#pragma unroll
+                for (int j = 0; j < S::kSteps; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[c][j][i] = 0.0f;
             }
-#pragma unroll
-            for (int j = 0; j < S::kCols; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
         }
 
         for (int tile = seg.begin + warp; tile < seg.end; tile += kWarps) {
             __syncwarp();   // every lane has read the stage that is filled now
             const Request now = next;
             next = request();
-            issue(now, fill);
+            issue(now, fill, S::kStages - 1);
             if (++fill == S::kStages) fill = 0;
-            copy_wait<S::kStages - 1>();
-            __syncwarp();   // the lanes' copies and the mask are visible to one another
-            const uint8_t* st = ring_ptr + stage * S::kStage;
-            if (++stage == S::kStages) stage = 0;
-            const uint32_t mask = *reinterpret_cast<const uint32_t*>(st + 2 * S::kKBytes + S::kScaleBytes);
+            if (a.tma) {
+                // after a timeout the rest runs through without waiting
+                if (!mbar_wait(bars + 8 * stage, phase, abort_flag) && lane == 0) atomicOr(a.err, 1);
+            } else {
+                copy_wait<S::kStages - 1>();
+            }
+            __syncwarp();   // the lanes' copies are visible to one another
+            const uint8_t* st = ring + stage * S::kStage;
+            const float* ks = reinterpret_cast<const float*>(factors + stage * S::kScaleBytes);
+            if (++stage == S::kStages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            const uint32_t mask = static_cast<uint32_t>(masks) & 0xFFFFu;
+            masks >>= 16;
 
             // ------------------------------------------------ scores
-            float s[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+            // two chains of products, added at the end
+            float s[COLS][2][4];
+#pragma unroll
+            for (int c = 0; c < COLS; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[c][i >> 2][i & 3] = 0.0f;
 #pragma unroll
             for (int i = 0; i < S::kKPieces; ++i) {
-                const uint4 u0 = *reinterpret_cast<const uint4*>(st + ((i * 2) * 32 + lane) * 16);
-                const uint4 u1 = *reinterpret_cast<const uint4*>(st + ((i * 2 + 1) * 32 + lane) * 16);
+                const uint4 u0 = *reinterpret_cast<const uint4*>(st + S::place(kr, i * 64 + t * 16));
+                const uint4 u1 = *reinterpret_cast<const uint4*>(st + S::place(kr + 8, i * 64 + t * 16));
                 const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
-                if constexpr (kCoded) {
+                constexpr int kPer = kCoded ? 4 : 2;   // K-steps of a run
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t lo, hi;
-                        decode4<KV>(w0[w], lo, hi);
-                        mma<kMma16>(s[0], qa[i * 4 + w], lo, hi);
-                        decode4<KV>(w1[w], lo, hi);
-                        mma<kMma16>(s[1], qa[i * 4 + w], lo, hi);
+                for (int w = 0; w < kPer; ++w) {
+                    uint32_t k[4];   // (key g, key g + 8) x (dimensions 0-1, 2-3)
+                    if constexpr (kCoded) {
+                        decode4<KV>(w0[w], k[0], k[2]);
+                        decode4<KV>(w1[w], k[1], k[3]);
+                    } else {
+                        k[0] = w0[2 * w], k[2] = w0[2 * w + 1];
+                        k[1] = w1[2 * w], k[3] = w1[2 * w + 1];
                     }
-                } else {
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        mma<kMma16>(s[0], qa[i * 2 + w], w0[2 * w], w0[2 * w + 1]);
-                        mma<kMma16>(s[1], qa[i * 2 + w], w1[2 * w], w1[2 * w + 1]);
-                    }
+                    for (int c = 0; c < COLS; ++c) mma<kMma16>(s[c][w & 1], k, qb[c][i * kPer + w][0], qb[c][i * kPer + w][1]);
                 }
             }
-            // the thread's keys: 2t, 2t+1, 8+2t, 9+2t
-            float kf[4] = {1, 1, 1, 1}, vl[4] = {0, 0, 0, 0};
+            // the thread's keys: kr, kr + 8
+            float kf[2] = {1, 1}, vl[2] = {0, 0};
             if constexpr (kCoded) {
-                const float* ks = reinterpret_cast<const float*>(st + 2 * S::kKBytes);
-                const float2 k0 = *reinterpret_cast<const float2*>(ks + 2 * t), k1 = *reinterpret_cast<const float2*>(ks + 8 + 2 * t);
-                const float2 v0 = *reinterpret_cast<const float2*>(ks + 16 + 2 * t), v1 = *reinterpret_cast<const float2*>(ks + 24 + 2 * t);
-                kf[0] = k0.x, kf[1] = k0.y, kf[2] = k1.x, kf[3] = k1.y;
-                vl[0] = log2_approx(v0.x), vl[1] = log2_approx(v0.y), vl[2] = log2_approx(v1.x), vl[3] = log2_approx(v1.y);
-            }
-            float x[kR][4];
 #pragma unroll
-            for (int r = 0; r < kR; ++r)
+                for (int k = 0; k < 2; ++k) {
+                    kf[k] = ks[kr + 8 * k];
+                    vl[k] = log2_approx(ks[kTile + kr + 8 * k]);
+                }
+            }
+            float x[COLS][4];   // [key][head]: key kr heads 2t, 2t+1; key kr + 8 the same
+#pragma unroll
+            for (int c = 0; c < COLS; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[r][i] = s[i >> 1][2 * r + (i & 1)] * fac[r];
-                    if (kCoded) x[r][i] *= kf[i];
+                    x[c][i] = (s[c][0][i] + s[c][1][i]) * fac[c][i & 1];
+                    if (kCoded) x[c][i] *= kf[i >> 1];
                 }
             if (mask != 0xFFFFu) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (!((mask >> (2 * t + (i & 1) + 8 * (i >> 1))) & 1u)) {
+                for (int k = 0; k < 2; ++k)
+                    if (!((mask >> (kr + 8 * k)) & 1u)) {
+                        vl[k] = 0.0f;
 #pragma unroll
-                        for (int r = 0; r < kR; ++r) x[r][i] = -CUDART_INF_F;
+                        for (int c = 0; c < COLS; ++c) x[c][2 * k] = x[c][2 * k + 1] = -CUDART_INF_F;
                     }
             }
             // ------------------------------------------- references
-            float top[kR], topo[kR];
+            float top[COLS][2], topo[COLS][2];
             bool past = false;
 #pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                top[r] = fmaxf(fmaxf(x[r][0], x[r][1]), fmaxf(x[r][2], x[r][3]));
-                past = past || top[r] > m[r] + kLazy;
-                if (kCoded) {
-                    topo[r] = fmaxf(fmaxf(x[r][0] + vl[0], x[r][1] + vl[1]), fmaxf(x[r][2] + vl[2], x[r][3] + vl[3]));
-                    past = past || topo[r] > mo[r] + kLazy;
+            for (int c = 0; c < COLS; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    top[c][h] = fmaxf(x[c][h], x[c][2 + h]);
+                    past = past || top[c][h] > m[c][h] + kLazy;
+                    if (kCoded) {
+                        topo[c][h] = fmaxf(x[c][h] + vl[0], x[c][2 + h] + vl[1]);
+                        past = past || topo[c][h] > mo[c][h] + kLazy;
+                    }
                 }
-            }
             if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
-                for (int r = 0; r < kR; ++r) {
-                    float up = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                    up = fmaxf(m[r], fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2)));
-                    l[r] *= exp2_approx(m[r] - up);
-                    float f = exp2_approx(m[r] - up);
-                    m[r] = up;
-                    if (kCoded) {
-                        up = fmaxf(topo[r], __shfl_xor_sync(0xffffffffu, topo[r], 1));
-                        up = fmaxf(mo[r], fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2)));
-                        f = exp2_approx(mo[r] - up);
-                        mo[r] = up;
+                for (int c = 0; c < COLS; ++c) {
+                    float f[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float up = top[c][h];   // over the lanes that share t
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
+                        up = fmaxf(m[c][h], up);
+                        f[h] = exp2_approx(m[c][h] - up);
+                        l[c][h] *= f[h];
+                        m[c][h] = up;
+                        if (kCoded) {
+                            up = topo[c][h];
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
+                            up = fmaxf(mo[c][h], up);
+                            f[h] = exp2_approx(mo[c][h] - up);
+                            mo[c][h] = up;
+                        }
                     }
 #pragma unroll
-                    for (int j = 0; j < S::kCols; ++j) {
-                        o[j][2 * r] *= f;
-                        o[j][2 * r + 1] *= f;
+                    for (int j = 0; j < S::kSteps; ++j) {
+                        o[c][j][0] *= f[0], o[c][j][1] *= f[1];
+                        o[c][j][2] *= f[0], o[c][j][3] *= f[1];
                     }
                 }
             }
             // ---------------------------------------------- weights
-            uint32_t p[4] = {0, 0, 0, 0};
+            uint32_t p[COLS][2];
 #pragma unroll
-            for (int r = 0; r < kR; ++r) {
+            for (int c = 0; c < COLS; ++c) {
                 float w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    w[i] = exp2_approx(x[r][i] - m[r]);
-                    l[r] += w[i];
-                    if (kCoded) w[i] = exp2_approx(x[r][i] + vl[i] - mo[r]);
+                    w[i] = exp2_approx(x[c][i] - m[c][i & 1]);
+                    l[c][i & 1] += w[i];
+                    if (kCoded) w[i] = exp2_approx(x[c][i] + vl[i >> 1] - mo[c][i & 1]);
                 }
-                p[r] = pack_x2<kMma16>(w[0], w[1]);
-                p[2 + r] = pack_x2<kMma16>(w[2], w[3]);
+                p[c][0] = transpose8(pack_x2<kMma16>(w[0], w[1]));
+                p[c][1] = transpose8(pack_x2<kMma16>(w[2], w[3]));
             }
             // ----------------------------------------------- values
+            // row tile j of the output: dimensions dim(g, 0, j) and dim(g, 1, j); an
+            // operand register holds two keys of a dimension: slots 2t, 2t + 1 or 8 more
             const uint8_t* sv = st + S::kKBytes;
             if constexpr (kCoded) {
-                constexpr int kWords = S::kVRun / 4;
+                constexpr int kWords = S::kVRun / 4, kHalf = kWords / 2;
                 uint32_t v[4][kWords];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint8_t* src = sv + (j * 32 + lane) * S::kVRun;
+                    const uint8_t* src = sv + S::place(vr[j], g * S::kVRun);
                     if constexpr (kWords == 4) {
                         const uint4 u = *reinterpret_cast<const uint4*>(src);
                         v[j][0] = u.x, v[j][1] = u.y, v[j][2] = u.z, v[j][3] = u.w;
@@ -524,33 +636,57 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a) {
                         v[j][0] = u.x, v[j][1] = u.y;
                     }
                 }
+                if (mask != 0xFFFFu) {   // what lies there for keys that do not exist must not meet a weight of zero
 #pragma unroll
-                for (int q = 0; q < kWords; ++q)
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < kWords; ++i) v[j][i] = (mask >> vr[j]) & 1u ? v[j][i] : 0u;
+                }
+#pragma unroll
+                for (int q = 0; q < kHalf; ++q)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        uint32_t b0[2], b1[2];
-                        decode4<KV>(__byte_perm(v[0][q], v[1][q], h ? 0x7362 : 0x5140), b0[0], b0[1]);
-                        decode4<KV>(__byte_perm(v[2][q], v[3][q], h ? 0x7362 : 0x5140), b1[0], b1[1]);
-                        mma<kMma16>(o[4 * q + 2 * h], p, b0[0], b1[0]);
-                        mma<kMma16>(o[4 * q + 2 * h + 1], p, b0[1], b1[1]);
+                        const uint32_t sel = h ? 0x7362 : 0x5140;
+                        uint32_t x0[2], x1[2], x2[2], x3[2];
+                        decode4<KV>(__byte_perm(v[0][q], v[1][q], sel), x0[0], x0[1]);
+                        decode4<KV>(__byte_perm(v[0][q + kHalf], v[1][q + kHalf], sel), x1[0], x1[1]);
+                        decode4<KV>(__byte_perm(v[2][q], v[3][q], sel), x2[0], x2[1]);
+                        decode4<KV>(__byte_perm(v[2][q + kHalf], v[3][q + kHalf], sel), x3[0], x3[1]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t av[4] = {x0[i], x1[i], x2[i], x3[i]};
+#pragma unroll
+                            for (int c = 0; c < COLS; ++c) mma<kMma16>(o[c][4 * q + 2 * h + i], av, p[c][0], p[c][1]);
+                        }
                     }
             } else {
+                uint32_t v[4][4 * S::kVPieces];
 #pragma unroll
-                for (int i = 0; i < S::kVPieces; ++i) {
-                    uint32_t v[4][4];
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(sv + ((j * S::kVPieces + i) * 32 + lane) * 16);
-                        v[j][0] = u.x, v[j][1] = u.y, v[j][2] = u.z, v[j][3] = u.w;
+                    for (int i = 0; i < S::kVPieces; ++i) {
+                        const uint4 u = *reinterpret_cast<const uint4*>(sv + S::place(vr[j], i * 128 + g * 16));
+                        v[j][4 * i] = u.x, v[j][4 * i + 1] = u.y, v[j][4 * i + 2] = u.z, v[j][4 * i + 3] = u.w;
                     }
+                if (mask != 0xFFFFu) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        mma<kMma16>(o[8 * i + 2 * q], p, __byte_perm(v[0][q], v[1][q], 0x5410),
-                                    __byte_perm(v[2][q], v[3][q], 0x5410));
-                        mma<kMma16>(o[8 * i + 2 * q + 1], p, __byte_perm(v[0][q], v[1][q], 0x7632),
-                                    __byte_perm(v[2][q], v[3][q], 0x7632));
-                    }
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4 * S::kVPieces; ++i) v[j][i] = (mask >> vr[j]) & 1u ? v[j][i] : 0u;
                 }
+                constexpr int kHalf = 2 * S::kVPieces;   // words from a tile's first dimension to its second
+#pragma unroll
+                for (int q = 0; q < kHalf; ++q)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t sel = h ? 0x7632 : 0x5410;
+                        const uint32_t av[4] = {__byte_perm(v[0][q], v[1][q], sel),
+                                                __byte_perm(v[0][q + kHalf], v[1][q + kHalf], sel),
+                                                __byte_perm(v[2][q], v[3][q], sel),
+                                                __byte_perm(v[2][q + kHalf], v[3][q + kHalf], sel)};
+#pragma unroll
+                        for (int c = 0; c < COLS; ++c) mma<kMma16>(o[c][2 * q + h], av, p[c][0], p[c][1]);
+                    }
             }
         }
 
@@ -559,58 +695,75 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a) {
         const bool whole = seg.begin == 0 && seg.end == seg.tiles;
         if (mine) {
 #pragma unroll
-            for (int r = 0; r < kR; ++r) {
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-                if (t == 0) {
-                    float* dst = stat + (warp * kRows + g + 8 * r) * 3;
-                    dst[0] = m[r];
-                    dst[1] = kCoded ? mo[r] : m[r];
-                    dst[2] = l[r];
+            for (int c = 0; c < COLS; ++c)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[c][h] += __shfl_xor_sync(0xffffffffu, l[c][h], d);
+                    if (g == 0) {
+                        float* dst = stat + (warp * kSlotRows + 8 * c + 2 * t + h) * 3;
+                        dst[0] = m[c][h];
+                        dst[1] = kCoded ? mo[c][h] : m[c][h];
+                        dst[2] = l[c][h];
+                    }
                 }
-            }
         }
         // partial results: the CTA that begins an item uses its odd slot, the
         // others their even one
-        constexpr int kSlotRows = 8 * kR;
         float* slot = a.slots + (2 * static_cast<int64_t>(blockIdx.x) + (seg.begin == 0 ? 1 : 0)) * slot_floats(DP, kSlotRows);
+        const int row = threadIdx.x * S::kEach / DP, d = threadIdx.x * S::kEach % DP;   // the thread's merged elements
+        auto finish = [&](int head, const float (&sum)[S::kEach], float M, float MO, float L) {
+            const float f = L == 0.0f ? 0.0f : exp2_approx(MO - M) / L;
+            if (d < a.D) {
+                uint16_t* dst = a.o + seg.b * a.ldo + (q_head + head) * a.D + d;
+                if constexpr (S::kEach == 4)
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_x2<F16>(sum[0] * f, sum[1] * f), pack_x2<F16>(sum[2] * f, sum[3] * f));
+                else if constexpr (S::kEach == 2)
+                    *reinterpret_cast<uint32_t*>(dst) = pack_x2<F16>(sum[0] * f, sum[1] * f);
+                else
+                    *dst = pack_x1<F16>(sum[0] * f);
+            }
+            if (d == 0 && a.lse != nullptr)
+                a.lse[static_cast<int64_t>(seg.b) * a.Hkv * a.G + q_head + head] = L == 0.0f ? -CUDART_INF_F : M * kLn2 + logf(L);
+        };
 #pragma unroll
-        for (int r = 0; r < kR; ++r) {
+        for (int c = 0; c < COLS; ++c) {
             if (mine) {
-                float* dst = merge + (warp * 8 + g) * S::kMergeLd;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int h = 0; h < 2; ++h) {
+                    float* dst = merge + warp * 8 * DP;
 #pragma unroll
-                    for (int j = 0; j < S::kCols; j += 4)
-                        *reinterpret_cast<float4*>(dst + S::dim(2 * t + n, j)) =
-                            make_float4(o[j][2 * r + n], o[j + 1][2 * r + n], o[j + 2][2 * r + n], o[j + 3][2 * r + n]);
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int j = 0; j < S::kSteps; j += 4)
+                            *reinterpret_cast<float4*>(dst + S::merge_at(2 * t + h, S::dim(g, half, j))) =
+                                make_float4(o[c][j][2 * half + h], o[c][j + 1][2 * half + h], o[c][j + 2][2 * half + h],
+                                            o[c][j + 3][2 * half + h]);
+                }
             }
             __syncthreads();
-            const int row = threadIdx.x / (DP / 4), d = (threadIdx.x % (DP / 4)) * 4, head = row + 8 * r;
-            if (row < 8 && head < heads) {
+            const int head = row + 8 * c;
+            if (head < heads) {
                 float M = kNone, MO = kNone, L = 0.0f;
                 for (int w = 0; w < active; ++w) {
-                    M = fmaxf(M, stat[(w * kRows + head) * 3]);
-                    MO = fmaxf(MO, stat[(w * kRows + head) * 3 + 1]);
+                    M = fmaxf(M, stat[(w * kSlotRows + head) * 3]);
+                    MO = fmaxf(MO, stat[(w * kSlotRows + head) * 3 + 1]);
                 }
-                float4 sum = make_float4(0, 0, 0, 0);
+                float sum[S::kEach];
+#pragma unroll
+                for (int i = 0; i < S::kEach; ++i) sum[i] = 0.0f;
                 for (int w = 0; w < active; ++w) {
-                    const float* sp = stat + (w * kRows + head) * 3;
+                    const float* sp = stat + (w * kSlotRows + head) * 3;
                     L += sp[2] * exp2_approx(sp[0] - M);
                     const float f = exp2_approx(sp[1] - MO);
-                    const float4 u = *reinterpret_cast<const float4*>(merge + (w * 8 + row) * S::kMergeLd + d);
-                    sum.x += u.x * f, sum.y += u.y * f, sum.z += u.z * f, sum.w += u.w * f;
+#pragma unroll
+                    for (int i = 0; i < S::kEach; ++i) sum[i] += merge[w * 8 * DP + S::merge_at(row, d + i)] * f;
                 }
                 if (whole) {
-                    const float f = L == 0.0f ? 0.0f : exp2_approx(MO - M) / L;
-                    if (d < a.D)
-                        *reinterpret_cast<uint2*>(a.o + seg.b * a.ldo + (q_head + head) * a.D + d) =
-                            make_uint2(pack_x2<F16>(sum.x * f, sum.y * f), pack_x2<F16>(sum.z * f, sum.w * f));
-                    if (d == 0 && a.lse != nullptr)
-                        a.lse[static_cast<int64_t>(seg.b) * a.Hkv * a.G + q_head + head] =
-                            L == 0.0f ? -CUDART_INF_F : M * kLn2 + logf(L);
+                    finish(head, sum, M, MO, L);
                 } else {
-                    *reinterpret_cast<float4*>(slot + head * DP + d) = sum;
+#pragma unroll
+                    for (int i = 0; i < S::kEach; ++i) slot[head * DP + d + i] = sum[i];
                     if (d == 0) {
                         float* dst = slot + kSlotRows * DP + head * 3;
                         dst[0] = M;
@@ -634,33 +787,32 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a) {
             }
             __syncthreads();
             if (*last_flag) {
-                for (int e = threadIdx.x; e < heads * (DP / 4); e += kThreads) {
-                    const int head = e / (DP / 4), d = (e % (DP / 4)) * 4;
-                    auto part = [&](int c) {
-                        return a.slots + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * slot_floats(DP, kSlotRows);
-                    };
+                auto part = [&](int cta) {
+                    return a.slots + (2 * static_cast<int64_t>(cta) + (cta == c0 ? 1 : 0)) * slot_floats(DP, kSlotRows);
+                };
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) {
+                    const int head = row + 8 * c;
+                    if (head >= heads) continue;
                     float M = kNone, MO = kNone, L = 0.0f;
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* sp = part(c) + kSlotRows * DP + head * 3;
+                    for (int i = c0; i <= c1; ++i) {
+                        const float* sp = part(i) + kSlotRows * DP + head * 3;
                         M = fmaxf(M, __ldcg(sp));
                         MO = fmaxf(MO, __ldcg(sp + 1));
                     }
-                    float4 sum = make_float4(0, 0, 0, 0);
+                    float sum[S::kEach];
+#pragma unroll
+                    for (int i = 0; i < S::kEach; ++i) sum[i] = 0.0f;
 #pragma unroll 4
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* sp = part(c) + kSlotRows * DP + head * 3;
-                        const float4 u = __ldcg(reinterpret_cast<const float4*>(part(c) + head * DP + d));
+                    for (int k = c0; k <= c1; ++k) {
+                        const float* sp = part(k) + kSlotRows * DP + head * 3;
+                        const float* src = part(k) + head * DP + d;
                         L += __ldcg(sp + 2) * exp2_approx(__ldcg(sp) - M);
                         const float f = exp2_approx(__ldcg(sp + 1) - MO);
-                        sum.x += u.x * f, sum.y += u.y * f, sum.z += u.z * f, sum.w += u.w * f;
+#pragma unroll
+                        for (int i = 0; i < S::kEach; ++i) sum[i] += __ldcg(src + i) * f;
                     }
-                    const float f = L == 0.0f ? 0.0f : exp2_approx(MO - M) / L;
-                    if (d < a.D)
-                        *reinterpret_cast<uint2*>(a.o + seg.b * a.ldo + (q_head + head) * a.D + d) =
-                            make_uint2(pack_x2<F16>(sum.x * f, sum.y * f), pack_x2<F16>(sum.z * f, sum.w * f));
-                    if (d == 0 && a.lse != nullptr)
-                        a.lse[static_cast<int64_t>(seg.b) * a.Hkv * a.G + q_head + head] =
-                            L == 0.0f ? -CUDART_INF_F : M * kLn2 + logf(L);
+                    finish(head, sum, M, MO, L);
                 }
                 if (threadIdx.x == 0) a.arrived[c0] = 0;
             }
@@ -668,37 +820,67 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args a) {
         }
         if (seg.left == 0) break;
     }
-    copy_wait<0>();
+    // copies are all consumed, unless a wait ran out: let them land
+    if (a.tma && *abort_flag) {
+        volatile int no_abort = 0;
+        for (int i = 0; i < S::kStages; ++i) {
+            (void)mbar_wait(bars + 8 * i, 0, &no_abort);
+            (void)mbar_wait(bars + 8 * i, 1, &no_abort);
+        }
+    }
 }
 
 int group_rows(int64_t G) { return G > 8 ? 16 : 8; }
 
 int grid_size(int64_t B, int64_t Hv, int64_t max_len, int sm_count) {
     const int64_t units = B * Hv * ceil_div(max_len, kTile);
-    const int64_t ctas = ceil_div(units, kWarps);
+    const int64_t ctas = ceil_div(units, kMinTiles);
     return static_cast<int>(ctas < 1 ? 1 : ctas < sm_count ? ctas : sm_count);
 }
 
-template <int DP, int KV, bool F16, bool WIDE>
-cudaError_t launch(const Args& a, int grid, cudaStream_t stream) {
-    using S = Shape<DP, KV>;
-    static const cudaError_t limit = cudaFuncSetAttribute(decode_kernel<DP, KV, F16, WIDE>,
+template <int DP, int KV, bool F16, int COLS>
+cudaError_t launch(Args& a, const DecodeArgs& d, int grid, cudaStream_t stream) {
+    using S = Shape<DP, KV, COLS>;
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    // pages of a tile and more, whose (page, head) count fits a coordinate
+    a.tma = d.cache.num_pages > 0 && a.shift >= 4 && d.cache.num_pages * d.Hkv <= INT32_MAX &&
+            ((reinterpret_cast<uintptr_t>(a.kscale) | reinterpret_cast<uintptr_t>(a.vscale)) & 15) == 0;
+    if (a.tma) {
+        const EncodeTiledFn enc = encode_tiled_fn();
+        if (enc == nullptr) return cudaErrorNotSupported;
+        const CUtensorMapDataType type = KV != kKvX16 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                         : F16        ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        const cuuint64_t row = static_cast<cuuint64_t>(d.D) * S::kElem;
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d.D), static_cast<cuuint64_t>(1) << a.shift,
+                                    static_cast<cuuint64_t>(d.cache.num_pages * d.Hkv)};
+        const cuuint64_t strides[2] = {row, row << a.shift};
+        const cuuint32_t box[3] = {S::kWidth / S::kElem, kTile, 1};
+        const cuuint32_t estr[3] = {1, 1, 1};
+        for (int i = 0; i < 2; ++i)
+            if (enc(i ? &maps.v : &maps.k, type, 3, const_cast<void*>(i ? d.cache.v : d.cache.k), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, S::kWidth == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return cudaErrorInvalidValue;
+    }
+    static const cudaError_t limit = cudaFuncSetAttribute(decode_kernel<DP, KV, F16, COLS>,
                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (limit != cudaSuccess) return limit;
-    return launch_after(decode_kernel<DP, KV, F16, WIDE>, dim3(static_cast<unsigned>(grid)), kThreads, S::kSmem, stream, a);
+    return launch_after(decode_kernel<DP, KV, F16, COLS>, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, stream,
+                        maps, a);
 }
 
 template <int DP, int KV, bool F16>
-cudaError_t launch_rows(const Args& a, int grid, cudaStream_t stream) {
-    return group_rows(a.G) == 16 ? launch<DP, KV, F16, true>(a, grid, stream)
-                                 : launch<DP, KV, F16, false>(a, grid, stream);
+cudaError_t launch_cols(Args& a, const DecodeArgs& d, int grid, cudaStream_t stream) {
+    return group_rows(a.G) == 16 ? launch<DP, KV, F16, 2>(a, d, grid, stream) : launch<DP, KV, F16, 1>(a, d, grid, stream);
 }
 
 template <int DP, bool F16>
-cudaError_t launch_kind(int kv, const Args& a, int grid, cudaStream_t stream) {
-    if (kv == kKvX16) return launch_rows<DP, kKvX16, F16>(a, grid, stream);
-    if (kv == kKvE4m3) return launch_rows<DP, kKvE4m3, F16>(a, grid, stream);
-    return launch_rows<DP, kKvI8, F16>(a, grid, stream);
+cudaError_t launch_kind(int kv, Args& a, const DecodeArgs& d, int grid, cudaStream_t stream) {
+    if (kv == kKvX16) return launch_cols<DP, kKvX16, F16>(a, d, grid, stream);
+    if (kv == kKvE4m3) return launch_cols<DP, kKvE4m3, F16>(a, d, grid, stream);
+    return launch_cols<DP, kKvI8, F16>(a, d, grid, stream);
 }
 
 int64_t arrived_bytes(int grid) { return round_up(static_cast<int64_t>(grid) * 4, 256); }
@@ -738,10 +920,11 @@ cudaError_t launch_decode(bool x_f16, const DecodeArgs& d, void* ws, int sm_coun
     a.scale2 = d.scale * kLog2e;
     const int grid = grid_size(d.B, a.Hv, a.capacity, sm_count);
     uint8_t* w = static_cast<uint8_t*>(ws) + kWorkspaceErrBytes;
+    a.err = static_cast<int*>(ws);
     a.arrived = reinterpret_cast<int32_t*>(w);
     a.slots = reinterpret_cast<float*>(w + arrived_bytes(grid));
-    if (d.D > 64) return x_f16 ? launch_kind<128, true>(d.cache.kv, a, grid, stream) : launch_kind<128, false>(d.cache.kv, a, grid, stream);
-    return x_f16 ? launch_kind<64, true>(d.cache.kv, a, grid, stream) : launch_kind<64, false>(d.cache.kv, a, grid, stream);
+    if (d.D > 64) return x_f16 ? launch_kind<128, true>(d.cache.kv, a, d, grid, stream) : launch_kind<128, false>(d.cache.kv, a, d, grid, stream);
+    return x_f16 ? launch_kind<64, true>(d.cache.kv, a, d, grid, stream) : launch_kind<64, false>(d.cache.kv, a, d, grid, stream);
 }
 
 }  // namespace tern
