@@ -61,7 +61,6 @@ constexpr int kMinTiles = 8;           // of a CTA's range, where there are fewe
 constexpr float kLazy = 8.0f;          // how far a score may pass the reference
 constexpr float kNone = -1.0e38f;      // reference before any key
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
-constexpr int kSmemMax = 232448;
 
 struct Args {
     const int32_t* lens;
@@ -103,8 +102,11 @@ template <int DP, int KV, int COLS>
 struct Shape {
     static constexpr int kElem = KV == kKvX16 ? 2 : 1;
     // Coded tiles are half the bytes and take twice the instructions per byte:
-    // 16 warps of 128 registers; the wider forms need the registers of 8.
-    static constexpr int kWarps = KV != kKvX16 && COLS == 1 ? 16 : 8;
+    // two CTAs of 8 warps and 128 registers on an SM, so that one streams while
+    // the other ends a segment.  The rest needs the registers, or the ring, of one.
+    static constexpr int kCtas = KV != kKvX16 && COLS == 1 ? 2 : 1;
+    static constexpr int kWarps = 8;
+    static constexpr int kSmemMax = kCtas == 2 ? 115712 : 232448;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRowBytes = DP * kElem;
     static constexpr int kWidth = kRowBytes < 128 ? kRowBytes : 128;  // bytes of a row in one block of the tile
@@ -283,7 +285,7 @@ struct Request {
 };
 
 template <int DP, int KV, bool F16, int COLS>
-__global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, 1) decode_kernel(const __grid_constant__ Maps maps,
+__global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, COLS>::kCtas) decode_kernel(const __grid_constant__ Maps maps,
                                                                                 const __grid_constant__ Args a) {
     using S = Shape<DP, KV, COLS>;
     constexpr bool kCoded = KV != kKvX16;
@@ -832,15 +834,17 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, 1) decode_kerne
 
 int group_rows(int64_t G) { return G > 8 ? 16 : 8; }
 
-int grid_size(int64_t B, int64_t Hv, int64_t max_len, int sm_count) {
+// CTAs of a call; `most` is what the GPU holds at once.
+int grid_size(int64_t B, int64_t Hv, int64_t max_len, int64_t most) {
     const int64_t units = B * Hv * ceil_div(max_len, kTile);
     const int64_t ctas = ceil_div(units, kMinTiles);
-    return static_cast<int>(ctas < 1 ? 1 : ctas < sm_count ? ctas : sm_count);
+    return static_cast<int>(ctas < 1 ? 1 : ctas < most ? ctas : most);
 }
 
 template <int DP, int KV, bool F16, int COLS>
-cudaError_t launch(Args& a, const DecodeArgs& d, int grid, cudaStream_t stream) {
+cudaError_t launch(Args& a, const DecodeArgs& d, int sm_count, cudaStream_t stream) {
     using S = Shape<DP, KV, COLS>;
+    const int grid = grid_size(d.B, a.Hv, a.capacity, static_cast<int64_t>(sm_count) * S::kCtas);
     Maps maps;
     memset(&maps, 0, sizeof(maps));
     // pages of a tile and more, whose (page, head) count fits a coordinate
@@ -872,16 +876,18 @@ cudaError_t launch(Args& a, const DecodeArgs& d, int grid, cudaStream_t stream) 
 }
 
 template <int DP, int KV, bool F16>
-cudaError_t launch_cols(Args& a, const DecodeArgs& d, int grid, cudaStream_t stream) {
-    return group_rows(a.G) == 16 ? launch<DP, KV, F16, 2>(a, d, grid, stream) : launch<DP, KV, F16, 1>(a, d, grid, stream);
+cudaError_t launch_cols(Args& a, const DecodeArgs& d, int sm_count, cudaStream_t stream) {
+    return group_rows(a.G) == 16 ? launch<DP, KV, F16, 2>(a, d, sm_count, stream) : launch<DP, KV, F16, 1>(a, d, sm_count, stream);
 }
 
 template <int DP, bool F16>
-cudaError_t launch_kind(int kv, Args& a, const DecodeArgs& d, int grid, cudaStream_t stream) {
-    if (kv == kKvX16) return launch_cols<DP, kKvX16, F16>(a, d, grid, stream);
-    if (kv == kKvE4m3) return launch_cols<DP, kKvE4m3, F16>(a, d, grid, stream);
-    return launch_cols<DP, kKvI8, F16>(a, d, grid, stream);
+cudaError_t launch_kind(int kv, Args& a, const DecodeArgs& d, int sm_count, cudaStream_t stream) {
+    if (kv == kKvX16) return launch_cols<DP, kKvX16, F16>(a, d, sm_count, stream);
+    if (kv == kKvE4m3) return launch_cols<DP, kKvE4m3, F16>(a, d, sm_count, stream);
+    return launch_cols<DP, kKvI8, F16>(a, d, sm_count, stream);
 }
+
+constexpr int64_t kMostCtas = 2;   // per SM, any form: the workspace does not depend on the form
 
 int64_t arrived_bytes(int grid) { return round_up(static_cast<int64_t>(grid) * 4, 256); }
 
@@ -889,7 +895,7 @@ int64_t arrived_bytes(int grid) { return round_up(static_cast<int64_t>(grid) * 4
 
 size_t decode_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, int sm_count) {
     const int64_t G = Hq / Hkv;
-    const int grid = grid_size(B, Hkv * ceil_div(G, kRows), max_len, sm_count < 1 ? 1 : sm_count);
+    const int grid = grid_size(B, Hkv * ceil_div(G, kRows), max_len, kMostCtas * (sm_count < 1 ? 1 : sm_count));
     return kWorkspaceErrBytes + static_cast<size_t>(arrived_bytes(grid)) +
            static_cast<size_t>(2 * grid) * slot_floats(D > 64 ? 128 : 64, group_rows(G)) * sizeof(float);
 }
@@ -918,13 +924,13 @@ cudaError_t launch_decode(bool x_f16, const DecodeArgs& d, void* ws, int sm_coun
     a.passes = static_cast<int>(ceil_div(a.G, kRows));
     a.Hv = a.Hkv * a.passes;
     a.scale2 = d.scale * kLog2e;
-    const int grid = grid_size(d.B, a.Hv, a.capacity, sm_count);
+    const int grid = grid_size(d.B, a.Hv, a.capacity, kMostCtas * sm_count);
     uint8_t* w = static_cast<uint8_t*>(ws) + kWorkspaceErrBytes;
     a.err = static_cast<int*>(ws);
     a.arrived = reinterpret_cast<int32_t*>(w);
     a.slots = reinterpret_cast<float*>(w + arrived_bytes(grid));
-    if (d.D > 64) return x_f16 ? launch_kind<128, true>(d.cache.kv, a, d, grid, stream) : launch_kind<128, false>(d.cache.kv, a, d, grid, stream);
-    return x_f16 ? launch_kind<64, true>(d.cache.kv, a, d, grid, stream) : launch_kind<64, false>(d.cache.kv, a, d, grid, stream);
+    if (d.D > 64) return x_f16 ? launch_kind<128, true>(d.cache.kv, a, d, sm_count, stream) : launch_kind<128, false>(d.cache.kv, a, d, sm_count, stream);
+    return x_f16 ? launch_kind<64, true>(d.cache.kv, a, d, sm_count, stream) : launch_kind<64, false>(d.cache.kv, a, d, sm_count, stream);
 }
 
 }  // namespace tern
