@@ -135,6 +135,9 @@ struct Shape {
         if (kWidth < 128) return row * kWidth + at;
         return (at >> 7) * (kTile * 128) + row * 128 + ((at & 127) ^ ((row & 7) << 4));
     }
+    // Place of a key row's run 64 * i bytes after the one at `place` (i counts up
+    // from the row's start).
+    static __device__ __forceinline__ int k_run(int place, int i) { return (place ^ ((i & 1) * 64)) + (i >> 1) * kTile * 128; }
     // Element d of a head's row in a warp's merge block (spread over the banks).
     static __device__ __forceinline__ int merge_at(int row, int d) {
         return row * DP + ((((d >> 2) ^ (row >> 1)) << 2) | (d & 3));
@@ -277,13 +280,6 @@ __device__ __forceinline__ Segment first_segment(const Args& a, int64_t u0, int6
     }
 }
 
-// A tile whose page id has been asked for.
-struct Request {
-    int page;        // lane's key (shift < 4: key of lane mod 16; else the tile's one page)
-    int len, hk;
-    int tile;        // -1: none
-};
-
 template <int DP, int KV, bool F16, int COLS>
 __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, COLS>::kCtas) decode_kernel(const __grid_constant__ Maps maps,
                                                                                 const __grid_constant__ Args a) {
@@ -335,53 +331,59 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
     Segment seg = first_segment(a, u0, u1, lane);
 
     // ---------------------------------------------------- loads of a warp
-    Segment ls = seg;                 // segment of the next request
-    int lt = ls.begin + warp;         // and its tile
-    bool more = true;
-    auto request = [&]() {
-        Request r;
-        while (more && lt >= ls.end) {
+    // Page ids are looked up for a batch of up to 32 of the warp's tiles in one
+    // load: lane i holds the (page, head) index of the batch's tile i, or -1
+    // where its page is outside the cache.
+    Segment ls = seg;                 // segment of the batch
+    int lt = ls.begin + warp;         // first tile of the batch
+    int batch = 0, taken = 0, pos = 0;
+    int hk_at = 0;                    // (pages of fewer than 16 tokens look theirs up tile by tile)
+    auto refill = [&]() {
+        lt += taken * kWarps;
+        taken = 0;
+        while (lt >= ls.end) {
             if (ls.left == 0) {
-                more = false;
-            } else {
-                next_segment(a, ls);
-                lt = warp;
+                batch = 0;
+                return;
             }
+            next_segment(a, ls);
+            lt = warp;
         }
-        r.tile = -1;
-        if (!more) return r;
-        r.tile = lt;
-        r.len = ls.len;
-        r.hk = a.passes == 1 ? ls.hv : ls.hv / a.passes;
-        const int key = a.shift >= 4 ? lt * kTile : min(lt * kTile + (lane & 15), ls.len - 1);
-        r.page = a.table[static_cast<int64_t>(ls.b) * a.max_pages + (key >> a.shift)];
-        lt += kWarps;
-        return r;
+        batch = min(32, (ls.end - lt + kWarps - 1) / kWarps);
+        hk_at = a.passes == 1 ? ls.hv : ls.hv / a.passes;
+        if (a.tma) {
+            const int key = min(lt + lane * kWarps, ls.end - 1) * kTile;
+            const int page = a.table[static_cast<int64_t>(ls.b) * a.max_pages + (key >> a.shift)];
+            pos = page >= 0 && page < a.num_pages ? page * a.Hkv + hk_at : -1;
+        }
     };
     const int bytes = a.D * S::kElem;
     const int page_mask = (1 << a.shift) - 1;
     uint64_t masks = 0;   // 16 bits per tile in flight: its keys that exist
-    auto issue = [&](const Request& r, int stage, int ahead) {
+    auto issue = [&](int stage, int ahead) {
+        if (taken == batch) refill();
         uint32_t mask = 0;
-        if (r.tile >= 0) {
+        if (batch > 0) {
             const uint32_t st = smem_u32(ring + stage * S::kStage), fs = smem_u32(factors + stage * S::kScaleBytes);
-            const int key0 = r.tile * kTile;
+            const int key0 = (lt + taken * kWarps) * kTile;
+            const int at = __shfl_sync(0xffffffffu, pos, taken);
+            ++taken;
             if (a.tma) {
                 // a tile lies in one page
-                const bool there = r.page >= 0 && r.page < a.num_pages;
-                mask = there ? 0xFFFFu >> max(0, key0 + kTile - r.len) : 0u;
+                const bool there = at >= 0;
+                mask = there ? 0xFFFFu >> max(0, key0 + kTile - ls.len) : 0u;
                 const uint32_t bar = bars + 8 * stage;
-                const int pos = r.page * a.Hkv + r.hk, row = key0 & page_mask;
+                const int row = key0 & page_mask;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(bar, there ? S::kStage + S::kScaleBytes : 0);
                     if (there) {
 #pragma unroll
                         for (int i = 0; i < S::kBlocks; ++i) {
-                            tma_load_3d(st + i * kTile * S::kWidth, &maps.k, i * (S::kWidth / S::kElem), row, pos, bar);
-                            tma_load_3d(st + S::kKBytes + i * kTile * S::kWidth, &maps.v, i * (S::kWidth / S::kElem), row, pos, bar);
+                            tma_load_3d(st + i * kTile * S::kWidth, &maps.k, i * (S::kWidth / S::kElem), row, at, bar);
+                            tma_load_3d(st + S::kKBytes + i * kTile * S::kWidth, &maps.v, i * (S::kWidth / S::kElem), row, at, bar);
                         }
                         if constexpr (kCoded) {
-                            const int64_t cell = (static_cast<int64_t>(pos) << a.shift) + row;
+                            const int64_t cell = (static_cast<int64_t>(at) << a.shift) + row;
                             bulk_load(fs, a.kscale + cell, kTile * 4, bar);
                             bulk_load(fs + kTile * 4, a.vscale + cell, kTile * 4, bar);
                         }
@@ -392,18 +394,21 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 // cell of the lane's key (lane mod 16), negative where there is none
                 const int key = key0 + (lane & 15);
                 int64_t cell = -1;
-                if (key < r.len && r.page >= 0 && r.page < a.num_pages)
-                    cell = ((static_cast<int64_t>(r.page) * a.Hkv + r.hk) << a.shift) + (key & page_mask);
+                if (key < ls.len) {
+                    const int page = a.table[static_cast<int64_t>(ls.b) * a.max_pages + (key >> a.shift)];
+                    if (page >= 0 && page < a.num_pages)
+                        cell = ((static_cast<int64_t>(page) * a.Hkv + hk_at) << a.shift) + (key & page_mask);
+                }
                 mask = __ballot_sync(0xffffffffu, cell >= 0) & 0xFFFFu;
                 constexpr int kRuns = S::kRowBytes / 16, kAtOnce = 32 / kRuns;   // rows per step
 #pragma unroll
                 for (int i = 0; i < kTile / kAtOnce; ++i) {
-                    const int row = i * kAtOnce + lane / kRuns, at = (lane % kRuns) * 16;
+                    const int row = i * kAtOnce + lane / kRuns, off = (lane % kRuns) * 16;
                     const int64_t c = __shfl_sync(0xffffffffu, cell, row);
-                    const bool there = c >= 0 && at < bytes;
-                    const int dst = S::place(row, at);
-                    copy_async_or_zero<16>(st + dst, there ? a.k + c * bytes + at : a.k, there);
-                    copy_async_or_zero<16>(st + S::kKBytes + dst, there ? a.v + c * bytes + at : a.v, there);
+                    const bool there = c >= 0 && off < bytes;
+                    const int dst = S::place(row, off);
+                    copy_async_or_zero<16>(st + dst, there ? a.k + c * bytes + off : a.k, there);
+                    copy_async_or_zero<16>(st + S::kKBytes + dst, there ? a.v + c * bytes + off : a.v, there);
                 }
                 if constexpr (kCoded) {
                     const float* src = lane < 16 ? a.kscale : a.vscale;
@@ -415,15 +420,13 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
         masks |= static_cast<uint64_t>(mask) << (16 * ahead);
     };
 
-    Request next = request();
 #pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) {
-        const Request now = next;
-        next = request();
-        issue(now, i, i);
-    }
+    for (int i = 0; i < S::kStages - 1; ++i) issue(i, i);
     const int kr = key_at(g);   // keys kr and kr + 8 are the thread's rows of the scores
     const int vr[4] = {key_at(2 * t), key_at(2 * t + 1), key_at(2 * t) + 8, key_at(2 * t + 1) + 8};
+    // where the thread's runs lie in a tile (rows 8 apart are kWidth * 8 apart,
+    // the swizzle being the same; a run 64 bytes on is the one with bit 6 turned)
+    const int k_place = S::place(kr, t * 16), v_place[2] = {S::place(vr[0], g * S::kVRun), S::place(vr[1], g * S::kVRun)};
     int stage = 0, fill = S::kStages - 1;
     uint32_t phase = 0;
 
@@ -490,9 +493,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
 
         for (int tile = seg.begin + warp; tile < seg.end; tile += kWarps) {
             __syncwarp();   // every lane has read the stage that is filled now
-            const Request now = next;
-            next = request();
-            issue(now, fill, S::kStages - 1);
+            issue(fill, S::kStages - 1);
             if (++fill == S::kStages) fill = 0;
             if (a.tma) {
                 // after a timeout the rest runs through without waiting
@@ -519,8 +520,8 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 for (int i = 0; i < 8; ++i) s[c][i >> 2][i & 3] = 0.0f;
 #pragma unroll
             for (int i = 0; i < S::kKPieces; ++i) {
-                const uint4 u0 = *reinterpret_cast<const uint4*>(st + S::place(kr, i * 64 + t * 16));
-                const uint4 u1 = *reinterpret_cast<const uint4*>(st + S::place(kr + 8, i * 64 + t * 16));
+                const uint4 u0 = *reinterpret_cast<const uint4*>(st + S::k_run(k_place, i));
+                const uint4 u1 = *reinterpret_cast<const uint4*>(st + S::k_run(k_place, i) + 8 * S::kWidth);
                 const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
                 constexpr int kPer = kCoded ? 4 : 2;   // K-steps of a run
 #pragma unroll
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 uint32_t v[4][kWords];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint8_t* src = sv + S::place(vr[j], g * S::kVRun);
+                    const uint8_t* src = sv + v_place[j & 1] + (j >> 1) * 8 * S::kWidth;
                     if constexpr (kWords == 4) {
                         const uint4 u = *reinterpret_cast<const uint4*>(src);
                         v[j][0] = u.x, v[j][1] = u.y, v[j][2] = u.z, v[j][3] = u.w;
@@ -667,7 +668,8 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int i = 0; i < S::kVPieces; ++i) {
-                        const uint4 u = *reinterpret_cast<const uint4*>(sv + S::place(vr[j], i * 128 + g * 16));
+                        const uint4 u = *reinterpret_cast<const uint4*>(sv + v_place[j & 1] + (j >> 1) * 8 * S::kWidth +
+                                                                           i * kTile * 128);
                         v[j][4 * i] = u.x, v[j][4 * i + 1] = u.y, v[j][4 * i + 2] = u.z, v[j][4 * i + 3] = u.w;
                     }
                 if (mask != 0xFFFFu) {
