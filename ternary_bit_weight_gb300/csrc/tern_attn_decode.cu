@@ -16,13 +16,12 @@
 // What bounds it: the bytes of the cache, read once (the G query heads of a
 // key/value head are rows of the same products).
 //
-// Work.  A unit is a tile of 16 keys of one (sequence, key/value head); all
-// units in that order are cut into equal contiguous ranges, one per CTA, so
-// unequal lengths load the SMs equally.  Within a CTA a segment (the part of
-// one item in its range) is dealt to the warps tile by tile; at its end the
-// warps' (m, l, o) meet in shared memory.  An item inside one CTA is then
-// finished; otherwise the CTAs leave partial results in the workspace and the
-// last to arrive adds them in CTA order (the result does not depend on
+// Work.  An item is one (sequence, key/value head); its tiles of 16 keys are
+// dealt to the CTAs in one of two ways (see Share), a segment being the part of
+// an item that a CTA has.  Within a segment the warps take the tiles in turn;
+// at its end their (m, l, o) meet in shared memory.  An item inside one CTA is
+// then finished; otherwise the CTAs leave partial results in the workspace and
+// the last to arrive adds them in CTA order (the result does not depend on
 // timing).
 //
 // A warp's tiles land in a ring of its own, so warps never wait for one
@@ -57,7 +56,9 @@ namespace {
 
 constexpr int kTile = 16;              // keys per unit
 constexpr int kRows = 16;              // query heads per pass over the keys
-constexpr int kMinTiles = 8;           // of a CTA's range, where there are fewer CTAs than SMs
+constexpr int kMinTiles = 8;           // of a CTA, one per warp
+constexpr int kEnd = 8;                // what ending a segment costs, in tiles
+constexpr float kPart = 2.4f;          // what adding a part costs, against an eighth of a tile
 constexpr float kLazy = 8.0f;          // how far a score may pass the reference
 constexpr float kNone = -1.0e38f;      // reference before any key
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
@@ -120,11 +121,11 @@ struct Shape {
     static constexpr int kSteps = DP / 16;                            // K-steps of a score, row tiles of the output
     static constexpr int kMerge = kWarps * 8 * DP * 4;
     static constexpr int kStat = kWarps * 8 * COLS * 3 * 4;
-    static constexpr int kFit = (kSmemMax - 1024 - kMerge - kStat - 16) / (kWarps * (kStage + kScaleBytes + 8));
+    static constexpr int kFit = (kSmemMax - 1024 - kMerge - kStat - 64) / (kWarps * (kStage + kScaleBytes + 8));
     static constexpr int kStages = kFit < 4 ? kFit : 4;
-    static constexpr int kSmem = 1024 + kWarps * kStages * (kStage + kScaleBytes + 8) + kMerge + kStat + 16;
+    static constexpr int kSmem = 1024 + kWarps * kStages * (kStage + kScaleBytes + 8) + kMerge + kStat + 64;
     static constexpr int kEach = 8 * DP / kThreads;                   // merged elements per thread
-    static_assert(kStages >= 2 && kEach >= 1 && kSmem <= kSmemMax, "shape");
+    static_assert(kStages >= 2 && (kEach == 2 || kEach == 4) && kWarps == 8 && kSmem <= kSmemMax, "shape");
     // Dimension of row g (half 0) or g + 8 (half 1) of output row tile j: a
     // thread's dimensions are those of the value runs it loads.
     static __device__ __forceinline__ int dim(int g, int half, int j) {
@@ -192,6 +193,24 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Count an arrival; what the CTA wrote before is visible to the CTAs that arrive
+// later, and theirs before to this one.
+__device__ __forceinline__ int arrive(int32_t* counter) {
+    int before;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
+    return before;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+    return x;
+}
+__device__ __forceinline__ float warp_add(float x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
 __device__ __forceinline__ float log2_approx(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -217,12 +236,28 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) 
     }
 }
 
-// One segment: the tiles [t, end) of item (b, hv) that lie in the CTA's range.
+// One segment: the tiles [begin, end) of item (b, hv).
 struct Segment {
     int b, hv;
     int len, tiles;      // keys and tiles of sequence b
     int begin, end;
-    int64_t left;        // units of the range after this segment
+    int64_t start;       // dealing by weight: where the item starts
+    int64_t left;        // and what is left of the CTA's part after it
+};
+
+// How the tiles are dealt to the CTAs.
+//   * whole == 0, by weight: an item weighs its tiles and kEnd more, and the
+//     items' weights, one after the other, are cut into equal parts, one per
+//     CTA, so unequal lengths load the SMs equally.  The first kEnd of an item
+//     stand for no tile: a cut that falls there splits no item.
+//   * whole == q: an item of n tiles goes to ceil(n / q) CTAs of its own, one
+//     segment each.  Fewer segments and partial results than by weight, less
+//     equal loads: taken when its largest load, with the segments' ends, is the
+//     smaller one (few sequences).
+struct Share {
+    int whole;
+    int64_t weight;      // by weight: of all items
+    int64_t ctas;        // that have a part
 };
 
 __device__ __forceinline__ int length_of(const Args& a, int b) {
@@ -230,34 +265,75 @@ __device__ __forceinline__ int length_of(const Args& a, int b) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
+// Quotients of what nearly always fits 32 bits (a 64-bit division takes
+// several hundred cycles of the start, which single sequences feel).
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    return ((x | y) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
+}
+__device__ __forceinline__ int64_t warp_sum(int64_t n) {
+    const int64_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(n) & 0xFFFFFFu);
+    const int64_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(n >> 24));   // n is below 2^51
+    return lo + (hi << 24);
+}
+
+__device__ __forceinline__ Share share_of(const Args& a, int lane) {
+    int64_t tiles = 0;
+    uint32_t some = 0;
+    for (int b = lane; b < a.B; b += 32) {
+        const int n = tiles_of(length_of(a, b));
+        tiles += n;
+        some += n > 0;
+    }
+    tiles = warp_sum(tiles) * a.Hv;
+    const int64_t items = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, some)) * a.Hv;
+    const int64_t grid = gridDim.x;
+    Share s;
+    s.whole = 0;
+    s.weight = tiles + kEnd * items;
+    s.ctas = tiles == 0 ? 0 : max(static_cast<int64_t>(1), min(grid, max(items, s.weight / (kMinTiles + kEnd))));
+    if (tiles > 0 && items < grid) {
+        // an item's parts add up one after the other: n tiles are split no finer
+        // than where a tile less per warp costs as much as the parts it adds
+        const int64_t even = static_cast<int64_t>(sqrtf(kPart * static_cast<float>(tiles) / static_cast<float>(items)));
+        const int64_t q = max(max(static_cast<int64_t>(kMinTiles), even), quotient(tiles + grid - items - 1, grid - items));
+        if (q + kEnd <= quotient(s.weight, s.ctas) + 2 * kEnd && q <= INT32_MAX) {
+            s.whole = static_cast<int>(q);
+            int64_t ctas = 0;
+            for (int b = lane; b < a.B; b += 32)
+                ctas += (static_cast<uint32_t>(tiles_of(length_of(a, b))) + s.whole - 1) / static_cast<uint32_t>(s.whole);
+            s.ctas = warp_sum(ctas) * a.Hv;
+        }
+    }
+    return s;
+}
+
+// The next item's part; the caller has seen that there is one (left > kEnd).
 __device__ __forceinline__ void next_segment(const Args& a, Segment& s) {
+    s.start += s.tiles + kEnd;
     if (++s.hv == a.Hv) {
         s.hv = 0;
         do {
-            s.len = length_of(a, ++s.b);   // units remain, so a sequence that has some follows
+            s.len = length_of(a, ++s.b);   // weight remains, so a sequence that has some follows
         } while (s.len == 0);
         s.tiles = tiles_of(s.len);
     }
     s.begin = 0;
-    s.end = static_cast<int>(min(static_cast<int64_t>(s.tiles), s.left));
-    s.left -= s.end;
+    s.end = static_cast<int>(min(static_cast<int64_t>(s.tiles), s.left - kEnd));
+    s.left -= s.end + kEnd;
 }
 
-// Total units, and (by one warp) the segment at the front of the CTA's range.
-__device__ __forceinline__ int64_t total_units(const Args& a, int lane) {
-    int64_t n = 0;
-    for (int b = lane; b < a.B; b += 32) n += tiles_of(length_of(a, b));
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-    return n * a.Hv;
-}
-__device__ __forceinline__ Segment first_segment(const Args& a, int64_t u0, int64_t u1, int lane) {
+// The CTA's first segment (one warp); begin == end: it has none.
+__device__ __forceinline__ Segment first_segment(const Args& a, const Share& share, int64_t cta, int lane) {
     Segment s;
+    const int64_t u0 = share.whole ? cta : quotient(share.weight * cta, share.ctas);
+    const int64_t u1 = share.whole ? cta + 1 : quotient(share.weight * (cta + 1), share.ctas);
     int64_t base = 0;
     for (int b0 = 0;; b0 += 32) {
         const int len = b0 + lane < a.B ? length_of(a, b0 + lane) : 0;
-        const int64_t units = static_cast<int64_t>(tiles_of(len)) * a.Hv;
-        int64_t incl = units;
+        const uint32_t tiles = tiles_of(len);
+        // CTAs, or weight, of an item: below 2^28, of a sequence's Hv items below 2^40
+        const uint32_t each = tiles == 0 ? 0 : share.whole ? (tiles + share.whole - 1) / static_cast<uint32_t>(share.whole) : tiles + kEnd;
+        int64_t incl = static_cast<int64_t>(each) * a.Hv;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int64_t up = __shfl_up_sync(0xffffffffu, incl, d);
@@ -268,15 +344,41 @@ __device__ __forceinline__ Segment first_segment(const Args& a, int64_t u0, int6
             const int src = __ffs(past) - 1;
             s.b = b0 + src;
             s.len = __shfl_sync(0xffffffffu, len, src);
-            const int64_t in = u0 - base - __shfl_sync(0xffffffffu, incl - units, src);
             s.tiles = tiles_of(s.len);
-            s.hv = static_cast<int>(in / s.tiles);
-            s.begin = static_cast<int>(in - static_cast<int64_t>(s.hv) * s.tiles);
-            s.end = static_cast<int>(min(static_cast<int64_t>(s.tiles), s.begin + (u1 - u0)));
-            s.left = u1 - u0 - (s.end - s.begin);
+            const int64_t n = __shfl_sync(0xffffffffu, each, src);
+            const int64_t in = u0 - base - (__shfl_sync(0xffffffffu, incl, src) - n * a.Hv);
+            s.hv = static_cast<int>(quotient(in, n));
+            const int64_t at = in - s.hv * n;
+            if (share.whole) {
+                const int per = static_cast<int>((s.tiles + static_cast<uint32_t>(n) - 1) / static_cast<uint32_t>(n));
+                s.start = cta - at;
+                s.begin = static_cast<int>(at) * per;
+                s.end = min(s.tiles, s.begin + per);
+                s.left = 0;
+            } else {
+                const int64_t upto = min(n, at + (u1 - u0));
+                s.start = u0 - at;
+                s.begin = static_cast<int>(max(static_cast<int64_t>(0), at - kEnd));
+                s.end = static_cast<int>(max(static_cast<int64_t>(s.begin), upto - kEnd));
+                s.left = (u1 - u0) - (upto - at);
+                if (s.begin == s.end && s.left > kEnd) next_segment(a, s);
+            }
             return s;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+// CTAs that have a part of the segment's item.
+__device__ __forceinline__ void parts_of(const Share& share, const Segment& s, int& c0, int& c1) {
+    if (share.whole) {
+        c0 = static_cast<int>(s.start);
+        c1 = c0 + static_cast<int>((static_cast<uint32_t>(s.tiles) + share.whole - 1) / static_cast<uint32_t>(share.whole)) - 1;
+    } else {
+        // the CTA that has weight unit u of the total W is the last c with W c / C <= u
+        const int64_t u = s.start + kEnd;
+        c0 = static_cast<int>(quotient((u + 1) * share.ctas - 1, share.weight));
+        c1 = static_cast<int>(quotient((u + s.tiles) * share.ctas - 1, share.weight));
     }
 }
 
@@ -297,7 +399,8 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
     const uint32_t bars = smem_u32(stat + S::kStat / 4) + warp * S::kStages * 8;   // a warp's stages
     volatile int* last_flag = reinterpret_cast<volatile int*>(reinterpret_cast<uint8_t*>(stat) + S::kStat +
                                                              kWarps * S::kStages * 8);
-    volatile int* abort_flag = last_flag + 1;
+    volatile int* part_info = last_flag + 2;     // [2][4]
+    volatile int* abort_flag = last_flag + 10;
     if (threadIdx.x == 0) *abort_flag = 0;
     if (lane == 0) {
         for (int i = 0; i < S::kStages; ++i) mbar_init(bars + 8 * i, 1);
@@ -323,12 +426,10 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 a.lse[static_cast<int64_t>(b) * a.Hkv * a.G + h] = -CUDART_INF_F;
     }
 
-    // a CTA's range holds a tile for each of 8 warps, or there are fewer CTAs
-    const int64_t U = total_units(a, lane);
-    const int64_t V = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), (U + kMinTiles - 1) / kMinTiles));
-    if (blockIdx.x >= V || U == 0) return;
-    const int64_t u0 = U * blockIdx.x / V, u1 = U * (blockIdx.x + 1) / V;
-    Segment seg = first_segment(a, u0, u1, lane);
+    const Share share = share_of(a, lane);
+    if (blockIdx.x >= share.ctas) return;
+    Segment seg = first_segment(a, share, blockIdx.x, lane);
+    if (seg.begin == seg.end) return;
 
     // ---------------------------------------------------- loads of a warp
     // Page ids are looked up for a batch of up to 32 of the warp's tiles in one
@@ -342,7 +443,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
         lt += taken * kWarps;
         taken = 0;
         while (lt >= ls.end) {
-            if (ls.left == 0) {
+            if (ls.left <= kEnd) {
                 batch = 0;
                 return;
             }
@@ -430,32 +531,60 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
     int stage = 0, fill = S::kStages - 1;
     uint32_t phase = 0;
 
+    // queries of head 8c + g: the four dimensions of each K-step that the thread's
+    // key runs hold
+    uint32_t qb[COLS][S::kSteps][2];
+    auto load_queries = [&](const Segment& s) {
+        const int hk = a.passes == 1 ? s.hv : s.hv / a.passes;
+        const int head0 = (s.hv - hk * a.passes) * kRows;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+            const bool live = 8 * c + g < min(kRows, a.G - head0);
+            const uint16_t* src = a.q + s.b * a.ldq + (static_cast<int64_t>(hk) * a.G + head0 + 8 * c + g) * a.D;
+#pragma unroll
+            for (int w = 0; w < S::kSteps; ++w) {
+                const int d = kCoded ? ((w / 4) * 4 + t) * 16 + (w % 4) * 4 : ((w / 2) * 4 + t) * 8 + (w % 2) * 4;
+                const uint2 u = live && d < a.D ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0, 0);
+                qb[c][w][0] = u.x;
+                qb[c][w][1] = u.y;
+            }
+        }
+    };
+    load_queries(seg);
+    // partial results left so far (in part_info: b, hv, first and last CTA of the
+    // item) and how many CTAs had arrived before: looked at when the CTA's tiles
+    // are done
+    int parts = 0, arrived0 = 0, arrived1 = 0;
+
+    // a warp stores the finished sums of one head
+    auto finish = [&](const Segment& s, int head, const float (&sum)[S::kEach], float M, float MO, float L) {
+        const int hk = a.passes == 1 ? s.hv : s.hv / a.passes;
+        const int64_t q_head = static_cast<int64_t>(hk) * a.G + (s.hv - hk * a.passes) * kRows + head;
+        const float f = L == 0.0f ? 0.0f : exp2_approx(MO - M) / L;
+        const int d = lane * S::kEach;
+        if (d < a.D) {
+            uint16_t* dst = a.o + s.b * a.ldo + q_head * a.D + d;
+            if constexpr (S::kEach == 4)
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_x2<F16>(sum[0] * f, sum[1] * f), pack_x2<F16>(sum[2] * f, sum[3] * f));
+            else
+                *reinterpret_cast<uint32_t*>(dst) = pack_x2<F16>(sum[0] * f, sum[1] * f);
+        }
+        if (lane == 0 && a.lse != nullptr)
+            a.lse[static_cast<int64_t>(s.b) * a.Hkv * a.G + q_head] = L == 0.0f ? -CUDART_INF_F : M * kLn2 + logf(L);
+    };
+
     // ------------------------------------------------------------ segments
-    for (bool first = true;; first = false) {
-        if (!first) next_segment(a, seg);
+    for (;;) {
         const int hk = a.passes == 1 ? seg.hv : seg.hv / a.passes;
         const int head0 = (seg.hv - hk * a.passes) * kRows;               // first of the group's heads
         const int heads = min(kRows, a.G - head0);
-        const int64_t q_head = static_cast<int64_t>(hk) * a.G + head0;
         // the thread's heads: 8c + 2t, 8c + 2t + 1
         float m[COLS][2], mo[COLS][2], l[COLS][2], fac[COLS][2];
         float o[COLS][S::kSteps][4];
-        uint32_t qb[COLS][S::kSteps][2];
         const bool mine = seg.begin + warp < seg.end;
         if (mine) {
 #pragma unroll
             for (int c = 0; c < COLS; ++c) {
-                // queries of head 8c + g: the four dimensions of each K-step that the
-                // thread's key runs hold
-                const bool live = 8 * c + g < heads;
-                const uint16_t* src = a.q + seg.b * a.ldq + (q_head + 8 * c + g) * a.D;
-#pragma unroll
-                for (int w = 0; w < S::kSteps; ++w) {
-                    const int d = kCoded ? ((w / 4) * 4 + t) * 16 + (w % 4) * 4 : ((w / 2) * 4 + t) * 8 + (w % 2) * 4;
-                    const uint2 u = live && d < a.D ? *reinterpret_cast<const uint2*>(src + d) : make_uint2(0, 0);
-                    qb[c][w][0] = u.x;
-                    qb[c][w][1] = u.y;
-                }
                 float f = a.scale2;
                 if constexpr (kCoded) {
                     // times 2^e, so that the row's largest magnitude lies in [2^14, 2^15)
@@ -695,8 +824,15 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
         }
 
         // ------------------------------------------- the segment's sum
-        const int active = min(kWarps, seg.end - seg.begin);   // warps that had a tile
-        const bool whole = seg.begin == 0 && seg.end == seg.tiles;
+        // the next segment's queries are on their way meanwhile
+        const Segment done = seg;
+        const bool another = seg.left > kEnd;
+        if (another) {
+            next_segment(a, seg);
+            load_queries(seg);
+        }
+        const int active = min(kWarps, done.end - done.begin);   // warps that had a tile
+        const bool whole = done.begin == 0 && done.end == done.tiles;
         if (mine) {
 #pragma unroll
             for (int c = 0; c < COLS; ++c)
@@ -714,22 +850,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
         }
         // partial results: the CTA that begins an item uses its odd slot, the
         // others their even one
-        float* slot = a.slots + (2 * static_cast<int64_t>(blockIdx.x) + (seg.begin == 0 ? 1 : 0)) * slot_floats(DP, kSlotRows);
-        const int row = threadIdx.x * S::kEach / DP, d = threadIdx.x * S::kEach % DP;   // the thread's merged elements
-        auto finish = [&](int head, const float (&sum)[S::kEach], float M, float MO, float L) {
-            const float f = L == 0.0f ? 0.0f : exp2_approx(MO - M) / L;
-            if (d < a.D) {
-                uint16_t* dst = a.o + seg.b * a.ldo + (q_head + head) * a.D + d;
-                if constexpr (S::kEach == 4)
-                    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_x2<F16>(sum[0] * f, sum[1] * f), pack_x2<F16>(sum[2] * f, sum[3] * f));
-                else if constexpr (S::kEach == 2)
-                    *reinterpret_cast<uint32_t*>(dst) = pack_x2<F16>(sum[0] * f, sum[1] * f);
-                else
-                    *dst = pack_x1<F16>(sum[0] * f);
-            }
-            if (d == 0 && a.lse != nullptr)
-                a.lse[static_cast<int64_t>(seg.b) * a.Hkv * a.G + q_head + head] = L == 0.0f ? -CUDART_INF_F : M * kLn2 + logf(L);
-        };
+        float* slot = a.slots + (2 * static_cast<int64_t>(blockIdx.x) + (done.begin == 0 ? 1 : 0)) * slot_floats(DP, kSlotRows);
 #pragma unroll
         for (int c = 0; c < COLS; ++c) {
             if (mine) {
@@ -746,29 +867,28 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 }
             }
             __syncthreads();
-            const int head = row + 8 * c;
+            const int head = 8 * c + warp;   // a warp adds up one head, a lane kEach of its elements
             if (head < heads) {
-                float M = kNone, MO = kNone, L = 0.0f;
-                for (int w = 0; w < active; ++w) {
-                    M = fmaxf(M, stat[(w * kSlotRows + head) * 3]);
-                    MO = fmaxf(MO, stat[(w * kSlotRows + head) * 3 + 1]);
-                }
+                const float* sp = stat + ((lane & 7) * kSlotRows + head) * 3;
+                const bool had = lane < active;
+                const float M = warp_max(had ? sp[0] : kNone), MO = warp_max(had ? sp[1] : kNone);
+                const float L = warp_add(had ? sp[2] * exp2_approx(sp[0] - M) : 0.0f);
+                const float fw = had ? exp2_approx(sp[1] - MO) : 0.0f;
                 float sum[S::kEach];
 #pragma unroll
                 for (int i = 0; i < S::kEach; ++i) sum[i] = 0.0f;
                 for (int w = 0; w < active; ++w) {
-                    const float* sp = stat + (w * kSlotRows + head) * 3;
-                    L += sp[2] * exp2_approx(sp[0] - M);
-                    const float f = exp2_approx(sp[1] - MO);
+                    const float f = __shfl_sync(0xffffffffu, fw, w);
+                    const float* src = merge + w * 8 * DP + S::merge_at(warp, lane * S::kEach);
 #pragma unroll
-                    for (int i = 0; i < S::kEach; ++i) sum[i] += merge[w * 8 * DP + S::merge_at(row, d + i)] * f;
+                    for (int i = 0; i < S::kEach; ++i) sum[i] += src[i] * f;
                 }
                 if (whole) {
-                    finish(head, sum, M, MO, L);
+                    finish(done, head, sum, M, MO, L);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < S::kEach; ++i) slot[head * DP + d + i] = sum[i];
-                    if (d == 0) {
+                    for (int i = 0; i < S::kEach; ++i) slot[head * DP + lane * S::kEach + i] = sum[i];
+                    if (lane == 0) {
                         float* dst = slot + kSlotRows * DP + head * 3;
                         dst[0] = M;
                         dst[1] = MO;
@@ -779,50 +899,71 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
             __syncthreads();
         }
         if (!whole) {
-            // CTAs c0 .. c1 hold the item; the last to arrive adds their parts
-            const int64_t before = u1 - seg.left - (seg.end - seg.begin) - seg.begin;   // first unit of the item
-            const int c0 = static_cast<int>(((before + 1) * V - 1) / U);
-            const int c1 = static_cast<int>(((before + seg.tiles) * V - 1) / U);
+            // at most two of a CTA's segments are parts of an item: its first and its last
             if (threadIdx.x == 0) {
-                __threadfence();
-                const int32_t old = atomicAdd(a.arrived + c0, 1);
-                *last_flag = old == c1 - c0;
-                __threadfence();
+                int c0, c1;
+                parts_of(share, done, c0, c1);
+                volatile int* info = part_info + 4 * (parts & 1);
+                info[0] = done.b, info[1] = done.hv, info[2] = c0, info[3] = c1;
+                const int before = arrive(a.arrived + c0);
+                if (parts == 0) arrived0 = before;
+                else arrived1 = before;
             }
-            __syncthreads();
-            if (*last_flag) {
-                auto part = [&](int cta) {
-                    return a.slots + (2 * static_cast<int64_t>(cta) + (cta == c0 ? 1 : 0)) * slot_floats(DP, kSlotRows);
-                };
-#pragma unroll
-                for (int c = 0; c < COLS; ++c) {
-                    const int head = row + 8 * c;
-                    if (head >= heads) continue;
-                    float M = kNone, MO = kNone, L = 0.0f;
-                    for (int i = c0; i <= c1; ++i) {
-                        const float* sp = part(i) + kSlotRows * DP + head * 3;
-                        M = fmaxf(M, __ldcg(sp));
-                        MO = fmaxf(MO, __ldcg(sp + 1));
-                    }
-                    float sum[S::kEach];
-#pragma unroll
-                    for (int i = 0; i < S::kEach; ++i) sum[i] = 0.0f;
-#pragma unroll 4
-                    for (int k = c0; k <= c1; ++k) {
-                        const float* sp = part(k) + kSlotRows * DP + head * 3;
-                        const float* src = part(k) + head * DP + d;
-                        L += __ldcg(sp + 2) * exp2_approx(__ldcg(sp) - M);
-                        const float f = exp2_approx(__ldcg(sp + 1) - MO);
-#pragma unroll
-                        for (int i = 0; i < S::kEach; ++i) sum[i] += __ldcg(src + i) * f;
-                    }
-                    finish(head, sum, M, MO, L);
-                }
-                if (threadIdx.x == 0) a.arrived[c0] = 0;
-            }
-            __syncthreads();   // last_flag is free again
+            ++parts;
         }
-        if (seg.left == 0) break;
+        if (!another) break;
+    }
+
+    // the last CTA to arrive adds the parts of an item, in CTA order
+    if (threadIdx.x == 0 && parts > 0) {
+        last_flag[0] = arrived0 == part_info[3] - part_info[2];
+        last_flag[1] = arrived1 == part_info[7] - part_info[6];
+    }
+    __syncthreads();
+    for (int n = 0; n < parts; ++n) {
+        if (!last_flag[n]) continue;
+        Segment done;
+        done.b = part_info[4 * n], done.hv = part_info[4 * n + 1];
+        const int c0 = part_info[4 * n + 2], c1 = part_info[4 * n + 3];
+        const int hk = a.passes == 1 ? done.hv : done.hv / a.passes;
+        const int heads = min(kRows, a.G - (done.hv - hk * a.passes) * kRows);
+        auto part = [&](int cta) {
+            return a.slots + (2 * static_cast<int64_t>(cta) + (cta == c0 ? 1 : 0)) * slot_floats(DP, kSlotRows);
+        };
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+            const int head = 8 * c + warp;
+            if (head >= heads) continue;
+            float M = kNone, MO = kNone, L = 0.0f;
+            for (int i = c0 + lane; i <= c1; i += 32) {
+                const float* sp = part(i) + kSlotRows * DP + head * 3;
+                M = fmaxf(M, __ldcg(sp));
+                MO = fmaxf(MO, __ldcg(sp + 1));
+            }
+            M = warp_max(M);
+            MO = warp_max(MO);
+            float sum[S::kEach];
+#pragma unroll
+            for (int i = 0; i < S::kEach; ++i) sum[i] = 0.0f;
+            for (int i0 = c0; i0 <= c1; i0 += 32) {
+                float f = 0.0f;
+                if (i0 + lane <= c1) {
+                    const float* sp = part(i0 + lane) + kSlotRows * DP + head * 3;
+                    L += __ldcg(sp + 2) * exp2_approx(__ldcg(sp) - M);
+                    f = exp2_approx(__ldcg(sp + 1) - MO);
+                }
+                const int count = min(32, c1 - i0 + 1);
+#pragma unroll 8
+                for (int k = 0; k < count; ++k) {
+                    const float* src = part(i0 + k) + head * DP + lane * S::kEach;
+                    const float fk = __shfl_sync(0xffffffffu, f, k);
+#pragma unroll
+                    for (int i = 0; i < S::kEach; ++i) sum[i] += __ldcg(src + i) * fk;
+                }
+            }
+            finish(done, head, sum, M, MO, warp_add(L));
+        }
+        if (threadIdx.x == 0) a.arrived[c0] = 0;
     }
     // copies are all consumed, unless a wait ran out: let them land
     if (a.tma && *abort_flag) {
@@ -838,8 +979,8 @@ int group_rows(int64_t G) { return G > 8 ? 16 : 8; }
 
 // CTAs of a call; `most` is what the GPU holds at once.
 int grid_size(int64_t B, int64_t Hv, int64_t max_len, int64_t most) {
-    const int64_t units = B * Hv * ceil_div(max_len, kTile);
-    const int64_t ctas = ceil_div(units, kMinTiles);
+    // one CTA per kMinTiles tiles, and one more per item for what is left over
+    const int64_t ctas = B * Hv * (max_len / (kTile * kMinTiles) + 1);
     return static_cast<int>(ctas < 1 ? 1 : ctas < most ? ctas : most);
 }
 
