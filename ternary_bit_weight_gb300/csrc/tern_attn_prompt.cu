@@ -72,8 +72,8 @@ constexpr int kBarRaw = kBarEmpty + 8 * kSlots;      // [2] V tile landed that t
 constexpr int kBarSafe = kBarRaw + 8 * 2;            // [2] and is ready
 constexpr int kBarQ = kBarSafe + 8 * 2;              // [kNT]
 constexpr int kBarS = kBarQ + 8 * kNT;               // [kNT] scores ready
-constexpr int kBarP = kBarS + 8 * kNT;               // [kNT] weights ready
-constexpr int kBarO = kBarP + 8 * kNT;               // [kNT] product with V done
+constexpr int kBarP = kBarS + 8 * kNT;               // [kNT][2] halves of the weights ready
+constexpr int kBarO = kBarP + 16 * kNT;              // [kNT] product with V done
 constexpr int kBarDrain = kBarO + 8 * kNT;
 constexpr int kTmemPtr = kBarDrain + 8;
 constexpr int kAbort = kTmemPtr + 4;
@@ -208,7 +208,27 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// The non-finite halves of a word become 0 (bf16: exponent 0xFF; fp16: 0x1F).
+// Two fp32 values in one register pair, and arithmetic on both.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+    return p;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma_x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Flags of the non-finite halves of a word (bf16: exponent 0xFF; fp16: 0x1F).
 template <bool F16>
 __device__ __forceinline__ uint32_t non_finite(uint32_t w) {
     constexpr uint32_t ones = F16 ? 0x7C007C00u : 0x7F807F80u, one = F16 ? 0x04000400u : 0x00800080u;
@@ -248,7 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int i = 0; i < kNT; ++i) {
             mbar_init(cb + kBarQ + 8 * i, 1);
             mbar_init(cb + kBarS + 8 * i, 1);
-            mbar_init(cb + kBarP + 8 * i, 4);
+            mbar_init(cb + kBarP + 16 * i, 4);
+            mbar_init(cb + kBarP + 16 * i + 8, 4);
             mbar_init(cb + kBarO + 8 * i, 1);
         }
         mbar_init(cb + kBarDrain, 1);
@@ -385,16 +406,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
                 for (int i = 0; i < kNT; ++i) {
                     if (j >= e[i]) continue;
-                    if (!(ok = warp_wait(cb + kBarP + 8 * i, (j - j0) & 1, abort_flag))) break;
-                    tc_fence_after_sync();
-                    if (elect_one()) {
+                    // the weights come in halves of 64 keys: the product of the first runs
+                    // while the second is computed
+                    for (int h = 0; h < 2; ++h) {
+                        if (!(ok = warp_wait(cb + kBarP + 16 * i + 8 * h, (j - j0) & 1, abort_flag))) break;
+                        tc_fence_after_sync();
+                        if (elect_one()) {
 #pragma unroll
-                        for (int s = 0; s < kTileN / 16; ++s)   // 16 keys: 16 rows of 128 bytes
-                            umma_bf16_tmem_a(tmem + kOCol + i * DP, tmem + kSCol + i * kTileN + 8 * s, bd + s * (2048 / 16),
-                                             idesc_o, (j > j0 || s > 0) ? 1u : 0u);
-                        umma_commit(cb + kBarO + 8 * i);
+                            for (int s = 0; s < kTileN / 32; ++s) {   // 16 keys: 16 rows of 128 bytes
+                                const int k = h * (kTileN / 32) + s;
+                                umma_bf16_tmem_a(tmem + kOCol + i * DP, tmem + kSCol + i * kTileN + 8 * k, bd + k * (2048 / 16),
+                                                 idesc_o, (j > j0 || k > 0) ? 1u : 0u);
+                            }
+                            if (h == 1) umma_commit(cb + kBarO + 8 * i);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!ok) break;
                     if (j + 1 < e[i]) {
                         if (!(ok = warp_wait(cb + kBarFull + 8 * kslot, kph, abort_flag))) break;
                         tc_fence_after_sync();
@@ -454,8 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             if (!(ok = warp_wait(cb + kBarS + 8 * i, (j - j0) & 1, abort_flag))) break;
             tc_fence_after_sync();
             float s[kTileN];
-#pragma unroll
-            for (int c = 0; c < kTileN / 32; ++c) tmem_ld32_sync(ts + 32 * c, reinterpret_cast<uint32_t*>(s + 32 * c));
+            tmem_ld128_sync(ts, reinterpret_cast<uint32_t*>(s));
             if (j >= jm) {
                 const int keys = lim - j * kTileN;   // keys of the tile that the row sees
 #pragma unroll
@@ -486,24 +513,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     }
                 }
             }
-            float sum[4] = {0, 0, 0, 0};
+            const uint64_t scale_x2 = pair(scale2, scale2), minus_m = pair(-m, -m);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int h = 0; h < kTileN / 32; ++h) {
                 uint32_t p[16];
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
-                    const float x = exp2_approx(fmaf(s[32 * h + c], scale2, -m));
-                    const float y = exp2_approx(fmaf(s[32 * h + c + 1], scale2, -m));
-                    sum[(c >> 1) & 3] += x + y;
+                    float x, y;
+                    unpair(fma_x2(pair(s[32 * h + c], s[32 * h + c + 1]), scale_x2, minus_m), x, y);
+                    x = exp2_approx(x);
+                    y = exp2_approx(y);
+                    sum[(c >> 1) & 1] = add_x2(sum[(c >> 1) & 1], pair(x, y));
                     p[c >> 1] = pack_x2<F16>(x, y);
                 }
                 tmem_st_32x32b_x16(ts + 16 * h, p);
+                if (h & 1) {
+                    tmem_st_wait();
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(cb + kBarP + 16 * i + 8 * (h >> 1));
+                }
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st_wait();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(cb + kBarP + 8 * i);
+            float l0, l1;
+            unpair(add_x2(sum[0], sum[1]), l0, l1);
+            l += l0 + l1;
         }
         // --------------------------------------------------------- epilogue
         if (ok && end > j0) {
