@@ -19,17 +19,22 @@
 // tokens against the same keys: while the softmax of one runs, the tensor
 // cores multiply for the other.
 //
-// Roles (12 warps):
+// Roles (20 warps):
 //   * warp 0 issues all tcgen05.mma: scores S_i = Q_i K_j^T (both operands in
 //     shared memory) into tensor memory, and O_i += P_i V_j with P_i in tensor
 //     memory over the columns of S_i (operations of one thread run in order,
-//     so S_i of the next tile follows the product that reads P_i);
+//     so S_i of the next tile follows the product that reads P_i).  Per tile
+//     and key tile it votes once over all barriers and issues both products: a
+//     wait costs it some 170 cycles even when the barrier is complete, and the
+//     tensor pipe runs dry meanwhile;
 //   * warp 1 brings Q and the K and V tiles by TMA (128-byte swizzle);
 //   * warp 2 makes V tiles safe that hold keys some row must not see: 0 * NaN
 //     is NaN, so non-finite values there become 0 before the product, and the
 //     epilogue adds them to the rows that do see them;
-//   * warps 4-7 and 8-11, one warpgroup per tile and one thread per row:
-//     softmax, rescaling of O in tensor memory, epilogue.
+//   * warps 4-11 and 12-19, two warpgroups per tile: softmax, rescaling of O in
+//     tensor memory, epilogue.  Two threads share a row, 64 keys each: the time
+//     from scores to weights has to fit into the other tile's products, and
+//     with one thread per row (128 keys) it was 1660 cycles against their 1024.
 // Few rows against many keys: the keys are split over CTAs, which leave
 // (m, l, o) in the workspace for a second kernel that adds them in split order.
 // Every wait is bounded; a timeout raises the workspace error word.
@@ -48,22 +53,18 @@ namespace {
 
 constexpr int kMmaWarp = 0, kLoadWarp = 1, kGuardWarp = 2, kSoftWarp0 = 4;
 constexpr int kNT = 2;                        // tiles per CTA
-constexpr int kThreads = (kSoftWarp0 + 4 * kNT) * 32;
+constexpr int kThreads = (kSoftWarp0 + 8 * kNT) * 32;
 constexpr int kTileM = 128, kTileN = 128;
 constexpr int kHalf = kTileM * 128;           // 128 rows x 64 elements of 16 bits
 constexpr int kSlots = 4;                     // K and V tiles, alternating: K in 0 and 2, V in 1 and 3
 static_assert(kSlots == 4, "two V slots: as many guarded tiles in flight");
 constexpr int kSCol = 0, kOCol = kNT * kTileN;
 constexpr int kTmemCols = 512;
-constexpr int kCtrlBytes = 256;
+constexpr int kShareBytes = kNT * 2 * kTileM * 4;   // a float of every row's two threads
+constexpr int kCtrlBytes = 256 + kShareBytes;
 constexpr float kLazy = 8.0f;
 constexpr float kNone = -1.0e38f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
-
-// Registers: 168 a thread at launch; the 128 threads of warps 0-3 give up 80
-// each for the 256 of the softmax (88 * 128 + 208 * 256 = 168 * 384).
-constexpr int kRegsLaunch = 168, kRegsUtil = 88, kRegsSoft = 208;
-static_assert(kRegsUtil * 128 + kRegsSoft * 128 * kNT <= kRegsLaunch * kThreads, "register split");
 
 // control block
 constexpr int kBarFull = 0;                          // [kSlots] tile landed
@@ -72,13 +73,14 @@ constexpr int kBarRaw = kBarEmpty + 8 * kSlots;      // [2] V tile landed that t
 constexpr int kBarSafe = kBarRaw + 8 * 2;            // [2] and is ready
 constexpr int kBarQ = kBarSafe + 8 * 2;              // [kNT]
 constexpr int kBarS = kBarQ + 8 * kNT;               // [kNT] scores ready
-constexpr int kBarP = kBarS + 8 * kNT;               // [kNT][2] halves of the weights ready
-constexpr int kBarO = kBarP + 16 * kNT;              // [kNT] product with V done
+constexpr int kBarP = kBarS + 8 * kNT;               // [kNT] weights ready
+constexpr int kBarO = kBarP + 8 * kNT;               // [kNT] product with V done
 constexpr int kBarDrain = kBarO + 8 * kNT;
 constexpr int kTmemPtr = kBarDrain + 8;
 constexpr int kAbort = kTmemPtr + 4;
 constexpr int kBad = kAbort + 4;                     // a value was taken out by the guard
-static_assert(kBad + 4 <= kCtrlBytes, "control block");
+constexpr int kShare = 256;
+static_assert(kBad + 4 <= kShare, "control block");
 
 template <int DP>
 constexpr int smem_bytes() {
@@ -208,6 +210,25 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
+// Each lane with `active` set waits for its own barrier; the warp goes on when
+// all have completed.
+__device__ __forceinline__ bool vote_wait(uint32_t bar, uint32_t parity, bool active, volatile int* abort) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xffffffffu, !active || mbar_test_wait(bar, parity))) return true;
+        if ((i & 255u) == 0) {
+            if (__any_sync(0xffffffffu, *abort != 0)) return false;
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0) {
+                t0 = t;
+            } else if (__any_sync(0xffffffffu, t - t0 > kWaitTimeoutNs)) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // Two fp32 values in one register pair, and arithmetic on both.
 __device__ __forceinline__ uint64_t pair(float x, float y) {
     uint64_t p;
@@ -254,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(ctrl + kTmemPtr);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + kAbort);
     volatile int* bad_flag = reinterpret_cast<volatile int*>(ctrl + kBad);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) {
@@ -268,8 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int i = 0; i < kNT; ++i) {
             mbar_init(cb + kBarQ + 8 * i, 1);
             mbar_init(cb + kBarS + 8 * i, 1);
-            mbar_init(cb + kBarP + 16 * i, 4);
-            mbar_init(cb + kBarP + 16 * i + 8, 4);
+            mbar_init(cb + kBarP + 8 * i, 8);
             mbar_init(cb + kBarO + 8 * i, 1);
         }
         mbar_init(cb + kBarDrain, 1);
@@ -291,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = *tmem_ptr;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_ptr, 0);   // uniform, and known to be
 
     const int hk = hc / a.chunks, head0 = hk * a.G + (hc - hk * a.chunks) * a.gs;
     const int heads = min(a.gs, (hk + 1) * a.G - head0);   // of the tile's gs, those that exist
@@ -318,10 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     // two in turn, which count guarded tiles only
     const int jg = max(j0, jm);
 
-    // each side changes its registers inside its own branch: the compiler
-    // allocates by the path
     if (warp < kSoftWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsUtil));
         if (warp == kLoadWarp) {
             // ------------------------------------------------------------ loads
             if (j1 > j0) {
@@ -369,72 +386,61 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const uint32_t idesc_s = type | ((kTileN >> 3) << 17);
             const uint32_t idesc_o = type | (static_cast<uint32_t>(a.D >> 3) << 17) | kBMnMajor;
             const int steps = a.D / 16;
+            // lane 0, which is elected, tests no barrier: its tests would wait behind its
+            // own commits, that is, until its last products have completed
             auto scores = [&](int i, int n) {   // S_i = Q_i K^T, K in load n
                 const uint64_t ad = smem_desc_kmajor_sw128(sq + i * kTileBytes);
                 const uint64_t bd = smem_desc_kmajor_sw128(skv + (n % kSlots) * kTileBytes);
-                if (elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < DP / 16; ++s)
-                        if (s < steps) {
-                            const uint32_t off = (s >> 2) * (kHalf / 16) + 2 * (s & 3);
-                            umma_smem_a(tmem + kSCol + i * kTileN, ad + off, bd + off, idesc_s, s > 0);
-                        }
-                    umma_commit(cb + kBarS + 8 * i);
-                }
-                __syncwarp();
+                for (int s = 0; s < DP / 16; ++s)
+                    if (s < steps) {
+                        const uint32_t off = (s >> 2) * (kHalf / 16) + 2 * (s & 3);
+                        umma_smem_a(tmem + kSCol + i * kTileN, ad + off, bd + off, idesc_s, s > 0);
+                    }
+                umma_commit(cb + kBarS + 8 * i);
             };
             bool ok = j1 > j0;
-            for (int i = 0; i < kNT && ok; ++i) {
-                if (e[i] == j0) continue;
-                ok = warp_wait(cb + kBarQ + 8 * i, 0, abort_flag) && warp_wait(cb + kBarFull, 0, abort_flag);
-                tc_fence_after_sync();
-                if (ok) scores(i, 0);
-            }
             if (ok) {
-                if (elect_one()) umma_commit(cb + kBarEmpty);
+                const bool q = (lane == 1 && e[0] > j0) || (lane == 2 && e[kNT - 1] > j0);
+                ok = vote_wait(q ? cb + kBarQ + 8 * (lane - 1) : cb + kBarFull, 0, q || lane == 3, abort_flag);
+                tc_fence_after_sync();
+                if (ok && elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < kNT; ++i)
+                        if (e[i] > j0) scores(i, 0);
+                    umma_commit(cb + kBarEmpty);
+                }
                 __syncwarp();
             }
             for (int j = j0; j < j1 && ok; ++j) {
-                const int n = 2 * (j - j0) + 1, slot = n % kSlots;
-                const int kslot = (n + 1) % kSlots;
-                const uint32_t kph = ((n + 1) / kSlots) & 1;
+                const int n = 2 * (j - j0) + 1, slot = n % kSlots, kslot = (n + 1) % kSlots;
+                const bool next = j + 1 < j1;
                 // a guarded tile is ready when the guard says so
                 const uint32_t vbar = cb + (j >= jm ? kBarSafe + 8 * ((j - jg) & 1) : kBarFull + 8 * slot);
                 const uint32_t vph = j >= jm ? ((j - jg) >> 1) & 1 : (n / kSlots) & 1;
-                if (!(ok = warp_wait(vbar, vph, abort_flag))) break;
                 const uint64_t bd = smem_desc_mnmajor_sw128(skv + slot * kTileBytes, kHalf);
 #pragma unroll
                 for (int i = 0; i < kNT; ++i) {
                     if (j >= e[i]) continue;
-                    // the weights come in halves of 64 keys: the product of the first runs
-                    // while the second is computed
-                    for (int h = 0; h < 2; ++h) {
-                        if (!(ok = warp_wait(cb + kBarP + 16 * i + 8 * h, (j - j0) & 1, abort_flag))) break;
-                        tc_fence_after_sync();
-                        if (elect_one()) {
+                    // weights (lane 1), this V tile (2), the next K tile (3)
+                    const uint32_t bar = lane == 1 ? cb + kBarP + 8 * i : lane == 2 ? vbar : cb + kBarFull + 8 * kslot;
+                    const uint32_t par = lane == 1 ? (j - j0) & 1 : lane == 2 ? vph : ((n + 1) / kSlots) & 1;
+                    if (!(ok = vote_wait(bar, par, lane == 1 || lane == 2 || (lane == 3 && next), abort_flag))) break;
+                    tc_fence_after_sync();
+                    if (elect_one()) {
 #pragma unroll
-                            for (int s = 0; s < kTileN / 32; ++s) {   // 16 keys: 16 rows of 128 bytes
-                                const int k = h * (kTileN / 32) + s;
-                                umma_bf16_tmem_a(tmem + kOCol + i * DP, tmem + kSCol + i * kTileN + 8 * k, bd + k * (2048 / 16),
-                                                 idesc_o, (j > j0 || k > 0) ? 1u : 0u);
-                            }
-                            if (h == 1) umma_commit(cb + kBarO + 8 * i);
+                        for (int s = 0; s < kTileN / 16; ++s)   // 16 keys: 16 rows of 128 bytes
+                            umma_bf16_tmem_a(tmem + kOCol + i * DP, tmem + kSCol + i * kTileN + 8 * s, bd + s * (2048 / 16),
+                                             idesc_o, (j > j0 || s > 0) ? 1u : 0u);
+                        umma_commit(cb + kBarO + 8 * i);
+                        if (j + 1 < e[i]) scores(i, n + 1);
+                        if (i == kNT - 1 || j >= e[kNT - 1]) {   // the last tile that reads these
+                            umma_commit(cb + kBarEmpty + 8 * slot);
+                            if (next) umma_commit(cb + kBarEmpty + 8 * kslot);
                         }
-                        __syncwarp();
                     }
-                    if (!ok) break;
-                    if (j + 1 < e[i]) {
-                        if (!(ok = warp_wait(cb + kBarFull + 8 * kslot, kph, abort_flag))) break;
-                        tc_fence_after_sync();
-                        scores(i, n + 1);
-                    }
+                    __syncwarp();
                 }
-                if (!ok) break;
-                if (elect_one()) {
-                    umma_commit(cb + kBarEmpty + 8 * slot);
-                    if (j + 1 < j1) umma_commit(cb + kBarEmpty + 8 * kslot);
-                }
-                __syncwarp();
             }
             if (elect_one()) umma_commit(cb + kBarDrain);
             __syncwarp();
@@ -465,46 +471,54 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         }
     } else {
         // ---------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-        const int i = (warp - kSoftWarp0) >> 2;
+        const int i = (warp - kSoftWarp0) >> 3;
+        const int half = ((warp - kSoftWarp0) >> 2) & 1;      // of a tile's keys, and of the output's columns
         const int r = threadIdx.x & 127;                      // row = tensor-memory lane
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + kSCol + i * kTileN, to = tmem + lanes + kOCol + i * DP;
+        const uint32_t pair_bar = 1 + 4 * i + (warp & 3);     // named barrier of the two warps that share 32 rows
+        float* share = reinterpret_cast<float*>(ctrl + kShare) + i * 2 * kTileM;
         const int token = r / a.gs, head = r - token * a.gs;  // of the tile
         const bool live = token < last[i] && head < heads;
         const int t = it.t0 + i * a.tok + token;
         const int lim = live ? visible(a, it, t) : 0;
         const int end = i == 0 ? e[0] : e[kNT - 1];
         const float scale2 = a.scale2;
+        const int steps = a.D / 16, c0 = half ? (steps + 1) / 2 * 16 : 0, c1 = half ? a.D : (steps + 1) / 2 * 16;
         float m = kNone, l = 0.0f;
+        // after a timeout the rest runs through, so that the two warps keep meeting
         bool ok = true;
         for (int j = j0; j < end; ++j) {
-            if (!(ok = warp_wait(cb + kBarS + 8 * i, (j - j0) & 1, abort_flag))) break;
+            ok &= warp_wait(cb + kBarS + 8 * i, (j - j0) & 1, abort_flag);
             tc_fence_after_sync();
-            float s[kTileN];
-            tmem_ld128_sync(ts, reinterpret_cast<uint32_t*>(s));
+            float s[kTileN / 2];
+            tmem_ld64_sync(ts + half * (kTileN / 2), reinterpret_cast<uint32_t*>(s));
             if (j >= jm) {
-                const int keys = lim - j * kTileN;   // keys of the tile that the row sees
+                const int keys = lim - j * kTileN - half * (kTileN / 2);   // of the thread's, those the row sees
 #pragma unroll
-                for (int c = 0; c < kTileN; ++c)
+                for (int c = 0; c < kTileN / 2; ++c)
                     if (c >= keys) s[c] = -CUDART_INF_F;
             }
             float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int c = 4; c < kTileN; c += 8) {
+            for (int c = 4; c < kTileN / 2; c += 8) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    top[q] = c + 4 + q < kTileN ? fmaxf(fmaxf(top[q], s[c + q]), s[c + 4 + q]) : fmaxf(top[q], s[c + q]);
+                    top[q] = c + 4 + q < kTileN / 2 ? fmaxf(fmaxf(top[q], s[c + q]), s[c + 4 + q]) : fmaxf(top[q], s[c + q]);
             }
             const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale2;
-            if (__any_sync(0xffffffffu, mx > m + kLazy)) {
-                const float up = fmaxf(m, mx), f = exp2_approx(m - up);
+            // both warps have read their scores when they meet here: the weights may
+            // overwrite them
+            if (named_barrier_or(pair_bar, 64, mx > m + kLazy)) {
+                share[half * kTileM + r] = mx;
+                (void)named_barrier_or(pair_bar, 64, false);
+                const float up = fmaxf(m, fmaxf(mx, share[(half ^ 1) * kTileM + r])), f = exp2_approx(m - up);
                 m = up;
                 l *= f;
                 if (j > j0) {
-                    if (!(ok = warp_wait(cb + kBarO + 8 * i, (j - j0 - 1) & 1, abort_flag))) break;
+                    ok &= warp_wait(cb + kBarO + 8 * i, (j - j0 - 1) & 1, abort_flag);
                     tc_fence_after_sync();
-                    for (int c = 0; c < a.D; c += 16) {
+                    for (int c = c0; c < c1; c += 16) {
                         uint32_t u[16];
                         tmem_ld16_sync(to + c, u);
 #pragma unroll
@@ -516,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const uint64_t scale_x2 = pair(scale2, scale2), minus_m = pair(-m, -m);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int h = 0; h < kTileN / 32; ++h) {
+            for (int h = 0; h < kTileN / 64; ++h) {
                 uint32_t p[16];
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
@@ -527,21 +541,23 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     sum[(c >> 1) & 1] = add_x2(sum[(c >> 1) & 1], pair(x, y));
                     p[c >> 1] = pack_x2<F16>(x, y);
                 }
-                tmem_st_32x32b_x16(ts + 16 * h, p);
-                if (h & 1) {
-                    tmem_st_wait();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(cb + kBarP + 16 * i + 8 * (h >> 1));
-                }
+                tmem_st_32x32b_x16(ts + half * (kTileN / 4) + 16 * h, p);
             }
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cb + kBarP + 8 * i);
             float l0, l1;
             unpair(add_x2(sum[0], sum[1]), l0, l1);
             l += l0 + l1;
         }
         // --------------------------------------------------------- epilogue
-        if (ok && end > j0) {
-            ok = warp_wait(cb + kBarO + 8 * i, (end - j0 - 1) & 1, abort_flag);
+        (void)named_barrier_or(pair_bar, 64, false);   // the last exchange has been read
+        share[half * kTileM + r] = l;
+        (void)named_barrier_or(pair_bar, 64, false);
+        l = share[r] + share[kTileM + r];
+        if (end > j0) {
+            ok &= warp_wait(cb + kBarO + 8 * i, (end - j0 - 1) & 1, abort_flag);
             tc_fence_after_sync();
         }
         if (ok) {
@@ -551,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             const bool split_keys = a.splits > 1;
             const int64_t prow = ((static_cast<int64_t>(block) * a.HC + hc) * kNT + i) * kTileM + r;
             const float inv = split_keys ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : CUDART_NAN_F;
-            for (int c = 0; c < a.D; c += 16) {
+            for (int c = c0; c < c1; c += 16) {
                 uint32_t u[16];
                 if (end > j0) {
                     tmem_ld16_sync(to + c, u);
@@ -584,10 +600,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                                         pack_x2<F16>(x[14], x[15]));
                 }
             }
-            if (split_keys) {
-                *reinterpret_cast<float2*>(a.part_ml + (prow * a.splits + split) * 2) = make_float2(m, l);
-            } else if (live && a.lse != nullptr) {
-                a.lse[row * a.Hq + h] = l == 0.0f ? -CUDART_INF_F : m * kLn2 + logf(l);
+            if (half == 0) {
+                if (split_keys)
+                    *reinterpret_cast<float2*>(a.part_ml + (prow * a.splits + split) * 2) = make_float2(m, l);
+                else if (live && a.lse != nullptr)
+                    a.lse[row * a.Hq + h] = l == 0.0f ? -CUDART_INF_F : m * kLn2 + logf(l);
             }
         }
     }
