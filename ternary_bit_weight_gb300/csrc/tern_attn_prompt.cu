@@ -31,10 +31,11 @@
 //   * warp 2 makes V tiles safe that hold keys some row must not see: 0 * NaN
 //     is NaN, so non-finite values there become 0 before the product, and the
 //     epilogue adds them to the rows that do see them;
-//   * warps 4-11 and 12-19, two warpgroups per tile: softmax, rescaling of O in
-//     tensor memory, epilogue.  Two threads share a row, 64 keys each: the time
-//     from scores to weights has to fit into the other tile's products, and
-//     with one thread per row (128 keys) it was 1660 cycles against their 1024.
+//   * warps 4-11 and 12-19, eight per tile: softmax, rescaling of O in tensor
+//     memory, epilogue.  A warp has 16 rows, four threads sharing each (the
+//     16-lane forms of tensor-memory access): the time from scores to weights
+//     has to fit into the other tile's products, and with one thread per row it
+//     was 1660 cycles against their 1024.
 // Few rows against many keys: the keys are split over CTAs, which leave
 // (m, l, o) in the workspace for a second kernel that adds them in split order.
 // Every wait is bounded; a timeout raises the workspace error word.
@@ -60,7 +61,7 @@ constexpr int kSlots = 4;                     // K and V tiles, alternating: K i
 static_assert(kSlots == 4, "two V slots: as many guarded tiles in flight");
 constexpr int kSCol = 0, kOCol = kNT * kTileN;
 constexpr int kTmemCols = 512;
-constexpr int kShareBytes = kNT * 2 * kTileM * 4;   // a float of every row's two threads
+constexpr int kShareBytes = kNT * kTileM * 8;       // reference and sum of every row
 constexpr int kCtrlBytes = 256 + kShareBytes;
 constexpr float kLazy = 8.0f;
 constexpr float kNone = -1.0e38f;
@@ -472,101 +473,124 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     } else {
         // ---------------------------------------------------------- softmax
         const int i = (warp - kSoftWarp0) >> 3;
-        const int half = ((warp - kSoftWarp0) >> 2) & 1;      // of a tile's keys, and of the output's columns
-        const int r = threadIdx.x & 127;                      // row = tensor-memory lane
-        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + kSCol + i * kTileN, to = tmem + lanes + kOCol + i * DP;
-        const uint32_t pair_bar = 1 + 4 * i + (warp & 3);     // named barrier of the two warps that share 32 rows
-        float* share = reinterpret_cast<float*>(ctrl + kShare) + i * 2 * kTileM;
-        const int token = r / a.gs, head = r - token * a.gs;  // of the tile
-        const bool live = token < last[i] && head < heads;
-        const int t = it.t0 + i * a.tok + token;
-        const int lim = live ? visible(a, it, t) : 0;
+        const int half = ((warp - kSoftWarp0) >> 2) & 1;      // which 16 of the quarter's 32 lanes; in the epilogue, which columns
+        const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + quarter + (static_cast<uint32_t>(16 * half) << 16) + kSCol + i * kTileN;
+        const uint32_t to = tmem + quarter + kOCol + i * DP, to16 = to + (static_cast<uint32_t>(16 * half) << 16);
         const int end = i == 0 ? e[0] : e[kNT - 1];
         const float scale2 = a.scale2;
-        const int steps = a.D / 16, c0 = half ? (steps + 1) / 2 * 16 : 0, c1 = half ? a.D : (steps + 1) / 2 * 16;
-        float m = kNone, l = 0.0f;
-        // after a timeout the rest runs through, so that the two warps keep meeting
+        // the thread's rows r0 and r0 + 8: the keys they see, their references and sums
+        const int r0 = (warp & 3) * 32 + half * 16 + (lane >> 2);
+        int lim[2];
+        float m[2] = {kNone, kNone}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int token = (r0 + 8 * q) / a.gs, head = r0 + 8 * q - token * a.gs;
+            lim[q] = token < last[i] && head < heads ? visible(a, it, it.t0 + i * a.tok + token) : 0;
+        }
         bool ok = true;
         for (int j = j0; j < end; ++j) {
-            ok &= warp_wait(cb + kBarS + 8 * i, (j - j0) & 1, abort_flag);
+            if (!(ok = warp_wait(cb + kBarS + 8 * i, (j - j0) & 1, abort_flag))) break;
             tc_fence_after_sync();
-            float s[kTileN / 2];
-            tmem_ld64_sync(ts + half * (kTileN / 2), reinterpret_cast<uint32_t*>(s));
+            float s[kTileN / 2];   // register 4c + 2q + k: row q, key 8c + 2 (lane mod 4) + k
+            tmem_ld_16x256b_x16_sync(ts, reinterpret_cast<uint32_t*>(s));
             if (j >= jm) {
-                const int keys = lim - j * kTileN - half * (kTileN / 2);   // of the thread's, those the row sees
 #pragma unroll
-                for (int c = 0; c < kTileN / 2; ++c)
-                    if (c >= keys) s[c] = -CUDART_INF_F;
-            }
-            float top[4] = {s[0], s[1], s[2], s[3]};
+                for (int q = 0; q < 2; ++q) {
+                    const int keys = lim[q] - j * kTileN - 2 * (lane & 3);
 #pragma unroll
-            for (int c = 4; c < kTileN / 2; c += 8) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    top[q] = c + 4 + q < kTileN / 2 ? fmaxf(fmaxf(top[q], s[c + q]), s[c + 4 + q]) : fmaxf(top[q], s[c + q]);
-            }
-            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale2;
-            // both warps have read their scores when they meet here: the weights may
-            // overwrite them
-            if (named_barrier_or(pair_bar, 64, mx > m + kLazy)) {
-                share[half * kTileM + r] = mx;
-                (void)named_barrier_or(pair_bar, 64, false);
-                const float up = fmaxf(m, fmaxf(mx, share[(half ^ 1) * kTileM + r])), f = exp2_approx(m - up);
-                m = up;
-                l *= f;
-                if (j > j0) {
-                    ok &= warp_wait(cb + kBarO + 8 * i, (j - j0 - 1) & 1, abort_flag);
-                    tc_fence_after_sync();
-                    for (int c = c0; c < c1; c += 16) {
-                        uint32_t u[16];
-                        tmem_ld16_sync(to + c, u);
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) u[q] = __float_as_uint(__uint_as_float(u[q]) * f);
-                        tmem_st_32x32b_x16(to + c, u);
+                    for (int c = 0; c < kTileN / 8; ++c) {
+                        if (8 * c >= keys) s[4 * c + 2 * q] = -CUDART_INF_F;
+                        if (8 * c + 1 >= keys) s[4 * c + 2 * q + 1] = -CUDART_INF_F;
                     }
                 }
             }
-            const uint64_t scale_x2 = pair(scale2, scale2), minus_m = pair(-m, -m);
+            float mx[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float top[2] = {s[2 * q], s[2 * q + 1]};
+#pragma unroll
+                for (int c = 1; c < kTileN / 8; ++c) top[c & 1] = fmaxf(fmaxf(top[c & 1], s[4 * c + 2 * q]), s[4 * c + 2 * q + 1]);
+                mx[q] = fmaxf(top[0], top[1]) * scale2;
+            }
+            if (__any_sync(0xffffffffu, mx[0] > m[0] + kLazy || mx[1] > m[1] + kLazy)) {
+                float f[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float up = fmaxf(mx[q], __shfl_xor_sync(0xffffffffu, mx[q], 1));
+                    up = fmaxf(m[q], fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2)));
+                    f[q] = exp2_approx(m[q] - up);
+                    m[q] = up;
+                    l[q] *= f[q];
+                }
+                if (j > j0) {
+                    if (!(ok = warp_wait(cb + kBarO + 8 * i, (j - j0 - 1) & 1, abort_flag))) break;
+                    tc_fence_after_sync();
+                    for (int c = 0; c < a.D; c += 16) {
+                        uint32_t u[8];
+                        tmem_ld_16x256b_x2_sync(to16 + c, u);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) u[q] = __float_as_uint(__uint_as_float(u[q]) * f[(q >> 1) & 1]);
+                        tmem_st_16x256b_x2(to16 + c, u);
+                    }
+                }
+            }
+            const uint64_t scale_x2 = pair(scale2, scale2), minus_m[2] = {pair(-m[0], -m[0]), pair(-m[1], -m[1])};
             uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int h = 0; h < kTileN / 64; ++h) {
+            for (int h = 0; h < 2; ++h) {
                 uint32_t p[16];
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
+                for (int c = 0; c < 16; ++c) {   // pair c of this half: row c & 1
                     float x, y;
-                    unpair(fma_x2(pair(s[32 * h + c], s[32 * h + c + 1]), scale_x2, minus_m), x, y);
+                    unpair(fma_x2(pair(s[32 * h + 2 * c], s[32 * h + 2 * c + 1]), scale_x2, minus_m[c & 1]), x, y);
                     x = exp2_approx(x);
                     y = exp2_approx(y);
-                    sum[(c >> 1) & 1] = add_x2(sum[(c >> 1) & 1], pair(x, y));
-                    p[c >> 1] = pack_x2<F16>(x, y);
+                    sum[c & 1] = add_x2(sum[c & 1], pair(x, y));
+                    p[c] = pack_x2<F16>(x, y);
                 }
-                tmem_st_32x32b_x16(ts + half * (kTileN / 4) + 16 * h, p);
+                tmem_st_16x128b_x8(ts + 32 * h, p);
             }
             tmem_st_wait();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(cb + kBarP + 8 * i);
-            float l0, l1;
-            unpair(add_x2(sum[0], sum[1]), l0, l1);
-            l += l0 + l1;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float x, y;
+                unpair(sum[q], x, y);
+                l[q] += x + y;
+            }
         }
         // --------------------------------------------------------- epilogue
-        (void)named_barrier_or(pair_bar, 64, false);   // the last exchange has been read
-        share[half * kTileM + r] = l;
-        (void)named_barrier_or(pair_bar, 64, false);
-        l = share[r] + share[kTileM + r];
-        if (end > j0) {
-            ok &= warp_wait(cb + kBarO + 8 * i, (end - j0 - 1) & 1, abort_flag);
+        // one thread per row of the quarter, the two warps half of the columns each
+        float2* share = reinterpret_cast<float2*>(ctrl + kShare) + i * kTileM;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            l[q] += __shfl_xor_sync(0xffffffffu, l[q], 1);
+            l[q] += __shfl_xor_sync(0xffffffffu, l[q], 2);
+            if ((lane & 3) == 0) share[r0 + 8 * q] = make_float2(m[q], l[q]);
+        }
+        if (end > j0 && ok) {
+            ok = warp_wait(cb + kBarO + 8 * i, (end - j0 - 1) & 1, abort_flag);
             tc_fence_after_sync();
         }
+        // (both warps come here, whatever their waits did)
+        ok = !named_barrier_or(1 + 4 * i + (warp & 3), 64, !ok);
+        const int r = (warp & 3) * 32 + lane;
+        const int token = r / a.gs, head = r - token * a.gs;
+        const bool live = token < last[i] && head < heads;
+        const int t = it.t0 + i * a.tok + token;
+        const float m_row = share[r].x, l_row = share[r].y;
+        const int steps = a.D / 16, c0 = half ? (steps + 1) / 2 * 16 : 0, c1 = half ? a.D : (steps + 1) / 2 * 16;
         if (ok) {
             const int64_t row = it.q0 + t;
             const int h = head0 + head;
             const bool bad = *bad_flag != 0;
             const bool split_keys = a.splits > 1;
             const int64_t prow = ((static_cast<int64_t>(block) * a.HC + hc) * kNT + i) * kTileM + r;
-            const float inv = split_keys ? 1.0f : l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : CUDART_NAN_F;
+            const int seen = live ? visible(a, it, t) : 0;
+            const float inv = split_keys ? 1.0f : l_row > 0.0f ? 1.0f / l_row : l_row == 0.0f ? 0.0f : CUDART_NAN_F;
             for (int c = c0; c < c1; c += 16) {
                 uint32_t u[16];
                 if (end > j0) {
@@ -579,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
                 for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(u[q]) * inv;
                 if (bad && live) {   // values taken out by the guard
-                    for (int key = jg * kTileN; key < min(lim, j1 * kTileN); ++key) {
+                    for (int key = jg * kTileN; key < min(seen, j1 * kTileN); ++key) {
                         const uint16_t* src = a.v + (it.k0 + key) * a.ldv + static_cast<int64_t>(hk) * a.D + c;
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
@@ -602,9 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             }
             if (half == 0) {
                 if (split_keys)
-                    *reinterpret_cast<float2*>(a.part_ml + (prow * a.splits + split) * 2) = make_float2(m, l);
+                    *reinterpret_cast<float2*>(a.part_ml + (prow * a.splits + split) * 2) = make_float2(m_row, l_row);
                 else if (live && a.lse != nullptr)
-                    a.lse[row * a.Hq + h] = l == 0.0f ? -CUDART_INF_F : m * kLn2 + logf(l);
+                    a.lse[row * a.Hq + h] = l_row == 0.0f ? -CUDART_INF_F : m_row * kLn2 + logf(l_row);
             }
         }
     }
