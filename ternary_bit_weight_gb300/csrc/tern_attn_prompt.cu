@@ -52,42 +52,51 @@
 namespace tern {
 namespace {
 
-constexpr int kMmaWarp = 0, kLoadWarp = 1, kGuardWarp = 2, kSoftWarp0 = 4;
-constexpr int kNT = 2;                        // tiles per CTA
-constexpr int kThreads = (kSoftWarp0 + 8 * kNT) * 32;
 constexpr int kTileM = 128, kTileN = 128;
 constexpr int kHalf = kTileM * 128;           // 128 rows x 64 elements of 16 bits
-constexpr int kSlots = 4;                     // K and V tiles, alternating: K in 0 and 2, V in 1 and 3
-static_assert(kSlots == 4, "two V slots: as many guarded tiles in flight");
-constexpr int kSCol = 0, kOCol = kNT * kTileN;
-constexpr int kTmemCols = 512;
-constexpr int kShareBytes = kNT * kTileM * 8;       // reference and sum of every row
-constexpr int kCtrlBytes = 256 + kShareBytes;
+constexpr int kMaxNT = 2;
+
+// The two forms of the kernel: NT tiles per CTA.
+template <int NT>
+struct Form {
+    static constexpr int kMmaWarp = 0, kLoadWarp = 1;
+    static constexpr int kGuardWarp = NT == 2 ? 2 : -1;   // NT == 1: the load warp guards, too
+    static constexpr int kSoftWarp0 = NT == 2 ? 4 : 2;    // any 4 warps in a row reach all tensor-memory lanes
+    static constexpr int kThreads = (kSoftWarp0 + 8 * NT) * 32;
+    static constexpr int kCtas = NT == 2 ? 1 : 2;         // per SM
+    static constexpr int kSlots = NT == 2 ? 4 : 2;        // K and V tiles, alternating: K even, V odd
+    static constexpr int kSCol = 0, kOCol = NT * kTileN;
+    static constexpr int kTmemCols = NT == 2 ? 512 : 256;
+    static_assert(NT * (kTileN + 128) <= kTmemCols, "tensor-memory budget");
+};
+constexpr int kShareBytes = kMaxNT * kTileM * 8;       // reference and sum of every row
+constexpr int kShare = 256;
+constexpr int kCtrlBytes = kShare + kShareBytes;
 constexpr float kLazy = 8.0f;
 constexpr float kNone = -1.0e38f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 // control block
-constexpr int kBarFull = 0;                          // [kSlots] tile landed
-constexpr int kBarEmpty = kBarFull + 8 * kSlots;     // [kSlots] tile consumed
-constexpr int kBarRaw = kBarEmpty + 8 * kSlots;      // [2] V tile landed that the guard looks over
+constexpr int kMaxSlots = Form<2>::kSlots;
+constexpr int kBarFull = 0;                          // [slots] tile landed
+constexpr int kBarEmpty = kBarFull + 8 * kMaxSlots;     // [slots] tile consumed
+constexpr int kBarRaw = kBarEmpty + 8 * kMaxSlots;      // [2] V tile landed that the guard looks over
 constexpr int kBarSafe = kBarRaw + 8 * 2;            // [2] and is ready
-constexpr int kBarQ = kBarSafe + 8 * 2;              // [kNT]
-constexpr int kBarS = kBarQ + 8 * kNT;               // [kNT] scores ready
-constexpr int kBarP = kBarS + 8 * kNT;               // [kNT] weights ready
-constexpr int kBarO = kBarP + 8 * kNT;               // [kNT] product with V done
-constexpr int kBarDrain = kBarO + 8 * kNT;
+constexpr int kBarQ = kBarSafe + 8 * 2;              // [NT]
+constexpr int kBarS = kBarQ + 8 * kMaxNT;               // [NT] scores ready
+constexpr int kBarP = kBarS + 8 * kMaxNT;               // [NT] weights ready
+constexpr int kBarO = kBarP + 8 * kMaxNT;               // [NT] product with V done
+constexpr int kBarDrain = kBarO + 8 * kMaxNT;
 constexpr int kTmemPtr = kBarDrain + 8;
 constexpr int kAbort = kTmemPtr + 4;
 constexpr int kBad = kAbort + 4;                     // a value was taken out by the guard
-constexpr int kShare = 256;
 static_assert(kBad + 4 <= kShare, "control block");
 
-template <int DP>
+template <int DP, int NT>
 constexpr int smem_bytes() {
-    return 1024 + (kNT + kSlots) * (DP / 64) * kHalf + kCtrlBytes;
+    return 1024 + (NT + Form<NT>::kSlots) * (DP / 64) * kHalf + kCtrlBytes;
 }
-static_assert(smem_bytes<128>() <= 232448, "shared-memory budget");
+static_assert(smem_bytes<128, 2>() <= 232448 && smem_bytes<128, 1>() <= 115712, "shared-memory budget");
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -99,11 +108,12 @@ struct Args {
     const uint16_t* v;
     uint16_t* o;
     float* lse;
-    float* part;          // split keys: [rows][splits][D] unnormalised outputs
-    float* part_ml;       // [rows][splits][2]: reference, sum
+    float* part;          // split keys: [tile][split][D / 4][128 rows][4] unnormalised outputs
+    float* part_ml;       // [tile][split][128 rows][2]: reference, sum
     int* err;
     int64_t ldv, ldo;
     int B, Tq, Tkv, Hq, G, D;
+    int nt;               // tiles of a block
     int gs, tok, chunks;  // heads and tokens of a tile; chunks = ceil(G / gs)
     int HC;               // key/value heads x chunks
     int splits;
@@ -111,7 +121,7 @@ struct Args {
     float scale2;         // scale * log2(e)
 };
 
-// Where a block works: tokens [t0, t0 + kNT * tok) of sequence b, its rows of Q
+// Where a block works: tokens [t0, t0 + nt * tok) of sequence b, its rows of Q
 // from q0 and of K from k0.
 struct Item {
     int q0, nq, k0, nk, t0;
@@ -127,10 +137,13 @@ __device__ __forceinline__ void clamp_range(const int32_t* cu, int b, int total,
 // past the last block.
 __device__ __forceinline__ bool find_item(const Args& a, int index, int lane, Item& it) {
     int base = 0;
-    const int step = kNT * a.tok;
+    const int step = a.nt * a.tok;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
-        int q0 = 0, nq = 0;
-        if (b0 + lane < a.B) clamp_range(a.cu_q, b0 + lane, a.Tq, q0, nq);
+        int q0 = 0, nq = 0, k0 = 0, nk = 0;
+        if (b0 + lane < a.B) {
+            clamp_range(a.cu_q, b0 + lane, a.Tq, q0, nq);
+            clamp_range(a.cu_kv, b0 + lane, a.Tkv, k0, nk);
+        }
         const int blocks = (nq + step - 1) / step;
         int incl = blocks;
 #pragma unroll
@@ -145,7 +158,8 @@ __device__ __forceinline__ bool find_item(const Args& a, int index, int lane, It
             it.nq = __shfl_sync(0xffffffffu, nq, src);
             const int end = base + __shfl_sync(0xffffffffu, incl, src);
             it.t0 = (end - 1 - index) * step;
-            clamp_range(a.cu_kv, b0 + src, a.Tkv, it.k0, it.nk);
+            it.k0 = __shfl_sync(0xffffffffu, k0, src);
+            it.nk = __shfl_sync(0xffffffffu, nk, src);
             return true;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
@@ -250,11 +264,15 @@ __device__ __forceinline__ uint64_t add_x2(uint64_t a, uint64_t b) {
     return d;
 }
 
-// Flags of the non-finite halves of a word (bf16: exponent 0xFF; fp16: 0x1F).
+// acc + 0 * w on both halves: a non-finite half makes its sum NaN for good.
 template <bool F16>
-__device__ __forceinline__ uint32_t non_finite(uint32_t w) {
-    constexpr uint32_t ones = F16 ? 0x7C007C00u : 0x7F807F80u, one = F16 ? 0x04000400u : 0x00800080u;
-    return ((w & ones) + one) & 0x80008000u;   // no carry passes a half's top bit
+__device__ __forceinline__ uint32_t times_zero(uint32_t w, uint32_t acc) {
+    uint32_t d;
+    if (F16)
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(0u), "r"(acc));
+    else
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(w), "r"(0u), "r"(acc));
+    return d;
 }
 
 template <bool F16>
@@ -263,9 +281,11 @@ __device__ __forceinline__ bool value_non_finite(uint16_t u) {
     return (u & ones) == ones;
 }
 
-template <int DP, bool F16>
-__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Maps maps,
-                                                             const __grid_constant__ Args a) {
+template <int DP, bool F16, int NT>
+__global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_kernel(const __grid_constant__ Maps maps,
+                                                                                     const __grid_constant__ Args a) {
+    using F = Form<NT>;
+    constexpr int kNT = NT, kSlots = F::kSlots, kSCol = F::kSCol, kOCol = F::kOCol;
     constexpr int kHalves = DP / 64, kTileBytes = kHalves * kHalf;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -278,41 +298,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     volatile int* bad_flag = reinterpret_cast<volatile int*>(ctrl + kBad);
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(cb + kBarFull + 8 * i, 1);
-            mbar_init(cb + kBarEmpty + 8 * i, 1);
+    if (warp == F::kLoadWarp) {   // which uses them first
+        if (lane < 3) prefetch_tensormap(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v);
+        if (elect_one()) {
+            for (int i = 0; i < kSlots; ++i) {
+                mbar_init(cb + kBarFull + 8 * i, 1);
+                mbar_init(cb + kBarEmpty + 8 * i, 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(cb + kBarRaw + 8 * i, 1);
+                mbar_init(cb + kBarSafe + 8 * i, 1);
+            }
+            for (int i = 0; i < kNT; ++i) {
+                mbar_init(cb + kBarQ + 8 * i, 1);
+                mbar_init(cb + kBarS + 8 * i, 1);
+                mbar_init(cb + kBarP + 8 * i, 8);
+                mbar_init(cb + kBarO + 8 * i, 1);
+            }
+            mbar_init(cb + kBarDrain, 1);
+            *abort_flag = 0;
+            *bad_flag = 0;
+            mbar_fence_init();
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(cb + kBarRaw + 8 * i, 1);
-            mbar_init(cb + kBarSafe + 8 * i, 1);
-        }
-        for (int i = 0; i < kNT; ++i) {
-            mbar_init(cb + kBarQ + 8 * i, 1);
-            mbar_init(cb + kBarS + 8 * i, 1);
-            mbar_init(cb + kBarP + 8 * i, 8);
-            mbar_init(cb + kBarO + 8 * i, 1);
-        }
-        mbar_init(cb + kBarDrain, 1);
-        *abort_flag = 0;
-        *bad_flag = 0;
-        mbar_fence_init();
+        __syncwarp();
     }
-    if (warp == kLoadWarp && lane < 3) prefetch_tensormap(lane == 0 ? &maps.q : lane == 1 ? &maps.k : &maps.v);
     grid_launch_dependents();
     grid_dependency_wait();
     Item it;
     const int hc = blockIdx.x % a.HC, rest = blockIdx.x / a.HC;
     const int split = rest % a.splits, block = rest / a.splits;
     if (!find_item(a, block, lane, it)) return;   // the whole CTA
-    if (warp == 0) {
-        tmem_alloc(smem_u32(tmem_ptr), kTmemCols);
-        tmem_relinquish();
-    }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_ptr, 0);   // uniform, and known to be
 
     const int hk = hc / a.chunks, head0 = hk * a.G + (hc - hk * a.chunks) * a.gs;
     const int heads = min(a.gs, (hk + 1) * a.G - head0);   // of the tile's gs, those that exist
@@ -339,34 +354,96 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     // two in turn, which count guarded tiles only
     const int jg = max(j0, jm);
 
-    if (warp < kSoftWarp0) {
-        if (warp == kLoadWarp) {
+    // K or V tile n of the loads (K and V of each key tile in turn).
+    auto load_tile = [&](int n) {
+        const int slot = n % kSlots, j = j0 + n / 2;
+        const uint32_t bar = cb + ((n & 1) && j >= jm ? kBarRaw + 8 * ((j - jg) & 1) : kBarFull + 8 * slot);
+        if (elect_one()) {
+            mbar_arrive_expect_tx(bar, kTileBytes);
+            for (int h = 0; h < kHalves; ++h)
+                tma_load_3d(skv + slot * kTileBytes + h * kHalf, n & 1 ? &maps.v : &maps.k, 64 * h, hk, it.k0 + j * kTileN, bar);
+        }
+        __syncwarp();
+    };
+    // Make guarded V tile j safe (one warp): keys from `seen` on are hidden from some
+    // row, those from nk on from all.
+    const int seen = visible(a, it, it.t0);
+    auto guard = [&](int j) {
+        const int slot = (2 * (j - j0) + 1) % kSlots, bar = 8 * ((j - jg) & 1);
+        if (!warp_wait(cb + kBarRaw + bar, ((j - jg) >> 1) & 1, abort_flag)) return false;
+        const int lo = max(0, seen - j * kTileN), hi = min(kTileN, it.nk - j * kTileN);
+        uint8_t* tile = smem + (kNT + slot) * kTileBytes + lane * 16;   // a row's 128 bytes are 8 lanes'
+        uint32_t acc[4] = {0, 0, 0, 0};
+        const uint32_t* first = reinterpret_cast<const uint32_t*>(tile);
+        for (int h = 0; h < kHalves; ++h) {
+#pragma unroll 8
+            for (int row = lo & ~3; row < hi; row += 4) {
+                const uint4 u = *reinterpret_cast<const uint4*>(first + (h * kHalf + row * 128) / 4);
+                acc[0] = times_zero<F16>(u.x, acc[0]);
+                acc[1] = times_zero<F16>(u.y, acc[1]);
+                acc[2] = times_zero<F16>(u.z, acc[2]);
+                acc[3] = times_zero<F16>(u.w, acc[3]);
+            }
+        }
+        const uint32_t any = acc[0] | acc[1] | acc[2] | acc[3];
+        bool wrote = false;
+        if (__any_sync(0xffffffffu, (any & 0x7FFF7FFFu) != 0)) {
+            wrote = true;
+            uint16_t* value = reinterpret_cast<uint16_t*>(tile);
+            for (int h = 0; h < kHalves; ++h)
+                for (int row = lo & ~3; row < hi; row += 4)
+                    for (int q = 0; q < 8; ++q)
+                        if (row + (lane >> 3) >= lo && value_non_finite<F16>(value[(h * kHalf + row * 128) / 2 + q]))
+                            value[(h * kHalf + row * 128) / 2 + q] = 0;
+            if (lane == 0) *bad_flag = 1;
+        }
+        if (hi < kTileN) {
+            wrote = true;
+            for (int h = 0; h < kHalves; ++h)
+                for (int row = hi & ~3; row < kTileN; row += 4)
+                    if (row + (lane >> 3) >= hi) *reinterpret_cast<uint4*>(tile + h * kHalf + row * 128) = make_uint4(0, 0, 0, 0);
+        }
+        if (wrote) fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cb + kBarSafe + bar);
+        return true;
+    };
+
+    // the first loads, then what the others need
+    if (warp == F::kLoadWarp && j1 > j0) {
+        if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < kNT; ++i) {
+                if (e[i] == j0) continue;
+                mbar_arrive_expect_tx(cb + kBarQ + 8 * i, kHalves * a.gs * a.tok * 128);
+                for (int h = 0; h < kHalves; ++h)
+                    tma_load_3d(sq + i * kTileBytes + h * kHalf, &maps.q, 64 * h, head0, it.q0 + it.t0 + i * a.tok,
+                                cb + kBarQ + 8 * i);
+            }
+        }
+        __syncwarp();
+        for (int n = 0; n < min(kSlots, 2 * (j1 - j0)); ++n) load_tile(n);
+    }
+    if (warp == F::kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_ptr), F::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_ptr, 0);   // uniform, and known to be
+
+    if (warp < F::kSoftWarp0) {
+        if (warp == F::kLoadWarp) {
             // ------------------------------------------------------------ loads
             if (j1 > j0) {
-                if (elect_one()) {
-#pragma unroll
-                    for (int i = 0; i < kNT; ++i) {
-                        if (e[i] == j0) continue;
-                        mbar_arrive_expect_tx(cb + kBarQ + 8 * i, kHalves * a.gs * a.tok * 128);
-                        for (int h = 0; h < kHalves; ++h)
-                            tma_load_3d(sq + i * kTileBytes + h * kHalf, &maps.q, 64 * h, head0, it.q0 + it.t0 + i * a.tok,
-                                        cb + kBarQ + 8 * i);
-                    }
-                }
-                __syncwarp();
                 bool ok = true;
-                for (int n = 0; n < 2 * (j1 - j0) && ok; ++n) {   // K and V of each tile in turn
-                    const int slot = n % kSlots, round = n / kSlots;
-                    if (round > 0 && !(ok = warp_wait(cb + kBarEmpty + 8 * slot, (round - 1) & 1, abort_flag))) break;
-                    const int j = j0 + n / 2;
-                    const uint32_t bar = cb + ((n & 1) && j >= jm ? kBarRaw + 8 * ((j - jg) & 1) : kBarFull + 8 * slot);
-                    if (elect_one()) {
-                        mbar_arrive_expect_tx(bar, kTileBytes);
-                        for (int h = 0; h < kHalves; ++h)
-                            tma_load_3d(skv + slot * kTileBytes + h * kHalf, n & 1 ? &maps.v : &maps.k, 64 * h, hk,
-                                        it.k0 + j * kTileN, bar);
+                for (int n = 0; n < 2 * (j1 - j0) && ok; ++n) {
+                    if (n >= kSlots) {
+                        if (!(ok = warp_wait(cb + kBarEmpty + 8 * (n % kSlots), (n / kSlots - 1) & 1, abort_flag))) break;
+                        load_tile(n);
                     }
-                    __syncwarp();
+                    if (F::kGuardWarp < 0 && (n & 1) && j0 + n / 2 >= jg) ok = guard(j0 + n / 2);
                 }
                 if (*abort_flag) {   // copies in flight must land before the CTA ends
                     volatile int no_abort = 0;
@@ -381,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
                     for (int i = 0; i < kNT; ++i) (void)warp_wait(cb + kBarQ + 8 * i, 0, &no_abort);
                 }
             }
-        } else if (warp == kMmaWarp) {
+        } else if (warp == F::kMmaWarp) {
             // -------------------------------------------------------------- MMA
             const uint32_t type = F16 ? idesc_fp16_f32(128, 0) : idesc_bf16_f32(128, 0);
             const uint32_t idesc_s = type | ((kTileN >> 3) << 17);
@@ -402,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             };
             bool ok = j1 > j0;
             if (ok) {
-                const bool q = (lane == 1 && e[0] > j0) || (lane == 2 && e[kNT - 1] > j0);
+                const bool q = (lane == 1 && e[0] > j0) || (NT == 2 && lane == 2 && e[kNT - 1] > j0);
                 ok = vote_wait(q ? cb + kBarQ + 8 * (lane - 1) : cb + kBarFull, 0, q || lane == 3, abort_flag);
                 tc_fence_after_sync();
                 if (ok && elect_one()) {
@@ -447,33 +524,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             __syncwarp();
             volatile int no_abort = 0;
             (void)warp_wait(cb + kBarDrain, 0, &no_abort);
-        } else if (warp == kGuardWarp) {
-            // ------------------------------------------------------------ guard
-            for (int j = jg; j < j1; ++j) {
-                const int slot = (2 * (j - j0) + 1) % kSlots, bar = 8 * ((j - jg) & 1);
-                if (!warp_wait(cb + kBarRaw + bar, ((j - jg) >> 1) & 1, abort_flag)) break;
-                uint4* tile = reinterpret_cast<uint4*>(smem + (kNT + slot) * kTileBytes);
-                uint32_t any = 0;
-#pragma unroll 8
-                for (int i = lane; i < kTileBytes / 16; i += 32) {
-                    const uint4 u = tile[i];
-                    any |= non_finite<F16>(u.x) | non_finite<F16>(u.y) | non_finite<F16>(u.z) | non_finite<F16>(u.w);
-                }
-                if (__any_sync(0xffffffffu, any != 0)) {
-                    uint16_t* value = reinterpret_cast<uint16_t*>(tile);
-                    for (int i = lane; i < kTileBytes / 2; i += 32)
-                        if (value_non_finite<F16>(value[i])) value[i] = 0;
-                    if (lane == 0) *bad_flag = 1;
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(cb + kBarSafe + bar);
-            }
+        } else if (warp == F::kGuardWarp) {
+            for (int j = jg; j < j1; ++j)
+                if (!guard(j)) break;
         }
     } else {
         // ---------------------------------------------------------- softmax
-        const int i = (warp - kSoftWarp0) >> 3;
-        const int half = ((warp - kSoftWarp0) >> 2) & 1;      // which 16 of the quarter's 32 lanes; in the epilogue, which columns
+        const int i = (warp - F::kSoftWarp0) >> 3;
+        const int half = ((warp - F::kSoftWarp0) >> 2) & 1;      // which 16 of the quarter's 32 lanes; in the epilogue, which columns
         const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + quarter + (static_cast<uint32_t>(16 * half) << 16) + kSCol + i * kTileN;
         const uint32_t to = tmem + quarter + kOCol + i * DP, to16 = to + (static_cast<uint32_t>(16 * half) << 16);
@@ -582,53 +640,71 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const bool live = token < last[i] && head < heads;
         const int t = it.t0 + i * a.tok + token;
         const float m_row = share[r].x, l_row = share[r].y;
-        const int steps = a.D / 16, c0 = half ? (steps + 1) / 2 * 16 : 0, c1 = half ? a.D : (steps + 1) / 2 * 16;
+        const int middle = (a.D + 63) / 64 * 32, c0 = half ? middle : 0, c1 = half ? a.D : middle;   // columns, by 32
         if (ok) {
-            const int64_t row = it.q0 + t;
-            const int h = head0 + head;
             const bool bad = *bad_flag != 0;
             const bool split_keys = a.splits > 1;
-            const int64_t prow = ((static_cast<int64_t>(block) * a.HC + hc) * kNT + i) * kTileM + r;
-            const int seen = live ? visible(a, it, t) : 0;
+            const int64_t part = ((static_cast<int64_t>(block) * a.HC + hc) * kNT + i) * a.splits + split;
+            const int lim_row = live ? visible(a, it, t) : 0;
             const float inv = split_keys ? 1.0f : l_row > 0.0f ? 1.0f / l_row : l_row == 0.0f ? 0.0f : CUDART_NAN_F;
-            for (int c = c0; c < c1; c += 16) {
-                uint32_t u[16];
+            uint8_t* stage = smem + i * kTileBytes;   // over the queries, whose products are done
+            for (int c = c0; c < c1; c += 32) {   // (columns from D on are loaded, too, and dropped)
+                float x[32];
                 if (end > j0) {
-                    tmem_ld16_sync(to + c, u);
+                    tmem_ld32_sync(to + c, reinterpret_cast<uint32_t*>(x));
                 } else {
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) u[q] = 0;
+                    for (int q = 0; q < 32; ++q) x[q] = 0.0f;
                 }
-                float x[16];
 #pragma unroll
-                for (int q = 0; q < 16; ++q) x[q] = __uint_as_float(u[q]) * inv;
+                for (int q = 0; q < 32; ++q) x[q] *= inv;
                 if (bad && live) {   // values taken out by the guard
-                    for (int key = jg * kTileN; key < min(seen, j1 * kTileN); ++key) {
+                    for (int key = max(seen, j0 * kTileN); key < min(lim_row, j1 * kTileN); ++key) {
                         const uint16_t* src = a.v + (it.k0 + key) * a.ldv + static_cast<int64_t>(hk) * a.D + c;
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            const uint32_t w = src[q];
+                        for (int q = 0; q < 32; ++q) {
+                            const uint32_t w = c + q < a.D ? src[q] : 0;
                             if (value_non_finite<F16>(static_cast<uint16_t>(w))) x[q] += unpack_x2<F16>(w).x;
                         }
                     }
                 }
-                if (split_keys) {
-                    float4* dst = reinterpret_cast<float4*>(a.part + (prow * a.splits + split) * a.D + c);
+                if (split_keys) {   // [4 columns][row], so that a warp's rows lie together
+                    float4* dst = reinterpret_cast<float4*>(a.part) + (part * (a.D / 4) + c / 4) * kTileM + r;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) dst[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-                } else if (live) {
-                    uint4* dst = reinterpret_cast<uint4*>(a.o + row * a.ldo + static_cast<int64_t>(h) * a.D + c);
-                    dst[0] = make_uint4(pack_x2<F16>(x[0], x[1]), pack_x2<F16>(x[2], x[3]), pack_x2<F16>(x[4], x[5]),
-                                        pack_x2<F16>(x[6], x[7]));
-                    dst[1] = make_uint4(pack_x2<F16>(x[8], x[9]), pack_x2<F16>(x[10], x[11]), pack_x2<F16>(x[12], x[13]),
-                                        pack_x2<F16>(x[14], x[15]));
+                    for (int q = 0; q < 8; ++q)
+                        if (c + 4 * q < a.D)
+                            dst[q * kTileM] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                } else {
+                    // 16-byte runs spread over the banks by the row
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4*>(stage + r * (DP * 2) + (((c / 8 + q) ^ (r & 7)) << 4)) =
+                            make_uint4(pack_x2<F16>(x[8 * q], x[8 * q + 1]), pack_x2<F16>(x[8 * q + 2], x[8 * q + 3]),
+                                       pack_x2<F16>(x[8 * q + 4], x[8 * q + 5]), pack_x2<F16>(x[8 * q + 6], x[8 * q + 7]));
                 }
             }
+            const int64_t row = it.q0 + t;
             if (half == 0) {
                 if (split_keys)
-                    *reinterpret_cast<float2*>(a.part_ml + (prow * a.splits + split) * 2) = make_float2(m_row, l_row);
+                    reinterpret_cast<float2*>(a.part_ml)[part * kTileM + r] = make_float2(m_row, l_row);
                 else if (live && a.lse != nullptr)
-                    a.lse[row * a.Hq + h] = l_row == 0.0f ? -CUDART_INF_F : m_row * kLn2 + logf(l_row);
+                    a.lse[row * a.Hq + head0 + head] = l_row == 0.0f ? -CUDART_INF_F : m_row * kLn2 + logf(l_row);
+            }
+            if (!split_keys) {
+                // whole rows to memory, 16 of the quarter's 32 by each warp: a thread per
+                // row would touch 32 lines with every store
+                (void)named_barrier_or(1 + 4 * i + (warp & 3), 64, false);
+                constexpr int kRuns = DP / 8, kAtOnce = 32 / kRuns;
+                const int64_t at = row * a.ldo + static_cast<int64_t>(head0 + head) * a.D;
+                const uint32_t live_rows = __ballot_sync(0xffffffffu, live);
+                const int run = lane % kRuns;
+#pragma unroll
+                for (int q = 0; q < 16 / kAtOnce; ++q) {
+                    const int rq = 16 * half + q * kAtOnce + lane / kRuns;   // of the quarter's rows
+                    const int64_t dst = __shfl_sync(0xffffffffu, at, rq);
+                    const uint4 u = *reinterpret_cast<const uint4*>(stage + ((warp & 3) * 32 + rq) * (DP * 2) + ((run ^ (rq & 7)) << 4));
+                    if (((live_rows >> rq) & 1u) && run * 8 < a.D) *reinterpret_cast<uint4*>(a.o + dst + run * 8) = u;
+                }
             }
         }
     }
@@ -639,52 +715,48 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     if (*abort_flag && threadIdx.x == 0) atomicOr(a.err, 1);
     if (warp == 0) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc(tmem, F::kTmemCols);
     }
 }
 
-// Sum of the splits' partial results, one warp per row, in split order.
-constexpr int kCombineWarps = 8, kCombineRows = 32;
+// Sum of the splits' partial results in split order: a thread per row and 8
+// columns, the rows of a warp one after the other as they were written.
+constexpr int kCombineThreads = 128;
 template <bool F16>
-__global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const Args a) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Args a) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kParts = kNT * kTileM / kCombineRows;
-    const int64_t item = blockIdx.x / kParts;
-    const int r0 = (blockIdx.x % kParts) * kCombineRows;
+    const int r = threadIdx.x, runs = a.D / 8;
+    const int64_t tile = blockIdx.x / runs, item = tile / a.nt;
+    const int run = static_cast<int>(blockIdx.x % runs), i = static_cast<int>(tile % a.nt);
     const int hc = static_cast<int>(item % a.HC), block = static_cast<int>(item / a.HC);
     Item it;
-    if (!find_item(a, block, lane, it)) return;
+    if (!find_item(a, block, threadIdx.x & 31, it)) return;
     const int hk = hc / a.chunks, head0 = hk * a.G + (hc - hk * a.chunks) * a.gs;
-    const int heads = min(a.gs, (hk + 1) * a.G - head0);
-    for (int r = r0 + warp; r < r0 + kCombineRows; r += kCombineWarps) {
-        const int i = r / kTileM, rr = r % kTileM, token = rr / a.gs, head = rr - token * a.gs;
-        const int t = it.t0 + i * a.tok + token;
-        if (token >= a.tok || t >= it.nq || head >= heads) continue;
-        const int64_t prow = item * kNT * kTileM + r;
-        const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + prow * a.splits;
-        float M = kNone, L = 0.0f;
-        for (int s = 0; s < a.splits; ++s) M = fmaxf(M, ml[s].x);
-        float4 sum = make_float4(0, 0, 0, 0);
-        const int d = lane * 4;
-        for (int s = 0; s < a.splits; ++s) {
-            const float f = exp2_approx(ml[s].x - M);
-            L += ml[s].y * f;
-            if (d < a.D) {
-                const float4 u = *reinterpret_cast<const float4*>(a.part + (prow * a.splits + s) * a.D + d);
-                // a split that the row sees nothing of adds nothing
-                if (ml[s].y != 0.0f) sum.x += u.x * f, sum.y += u.y * f, sum.z += u.z * f, sum.w += u.w * f;
-            }
+    const int token = r / a.gs, head = r - token * a.gs, t = it.t0 + i * a.tok + token;
+    if (token >= a.tok || t >= it.nq || head >= min(a.gs, (hk + 1) * a.G - head0)) return;
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + tile * a.splits * kTileM + r;
+    const float4* part = reinterpret_cast<const float4*>(a.part) + (tile * a.splits * (a.D / 4) + 2 * run) * kTileM + r;
+    float M = kNone, L = 0.0f;
+    for (int s = 0; s < a.splits; ++s) M = fmaxf(M, ml[s * kTileM].x);
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int s = 0; s < a.splits; ++s) {
+        const float2 x = ml[s * kTileM];
+        const float4 u = part[static_cast<int64_t>(s) * (a.D / 4) * kTileM];
+        const float4 v = part[(static_cast<int64_t>(s) * (a.D / 4) + 1) * kTileM];
+        const float f = exp2_approx(x.x - M);
+        L += x.y * f;
+        if (x.y != 0.0f) {   // a split that the row sees nothing of adds nothing
+            sum[0] += u.x * f, sum[1] += u.y * f, sum[2] += u.z * f, sum[3] += u.w * f;
+            sum[4] += v.x * f, sum[5] += v.y * f, sum[6] += v.z * f, sum[7] += v.w * f;
         }
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-        const int64_t row = it.q0 + t;
-        const int h = head0 + head;
-        if (d < a.D)
-            *reinterpret_cast<uint2*>(a.o + row * a.ldo + static_cast<int64_t>(h) * a.D + d) =
-                make_uint2(pack_x2<F16>(sum.x * inv, sum.y * inv), pack_x2<F16>(sum.z * inv, sum.w * inv));
-        if (lane == 0 && a.lse != nullptr) a.lse[row * a.Hq + h] = L == 0.0f ? -CUDART_INF_F : M * kLn2 + logf(L);
     }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const int64_t row = it.q0 + t;
+    *reinterpret_cast<uint4*>(a.o + row * a.ldo + static_cast<int64_t>(head0 + head) * a.D + 8 * run) =
+        make_uint4(pack_x2<F16>(sum[0] * inv, sum[1] * inv), pack_x2<F16>(sum[2] * inv, sum[3] * inv),
+                   pack_x2<F16>(sum[4] * inv, sum[5] * inv), pack_x2<F16>(sum[6] * inv, sum[7] * inv));
+    if (run == 0 && a.lse != nullptr) a.lse[row * a.Hq + head0 + head] = L == 0.0f ? -CUDART_INF_F : M * kLn2 + logf(L);
 }
 
 // ---------------------------------------------------------------- host
@@ -704,7 +776,7 @@ bool encode_heads(CUtensorMap* map, bool f16, const uint16_t* p, int64_t rows, i
 }
 
 struct Plan {
-    int gs, tok, chunks, HC, splits;
+    int nt, gs, tok, chunks, HC, splits;
     int64_t blocks;   // token blocks, at most
     size_t off_part, off_ml, ws_bytes;
 };
@@ -724,14 +796,21 @@ Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, in
     }
     p.chunks = static_cast<int>(ceil_div(G, p.gs));
     p.HC = static_cast<int>(Hkv) * p.chunks;
-    p.blocks = Tq / (kNT * p.tok) + B;
+    // One tile per CTA and two CTAs per SM, where the second tile of a block would
+    // be empty or the work per CTA is short, so that one CTA's start and end run
+    // beside the other's products (27B-class heads, us, one tile / two: 32 queries
+    // of up to 48 tokens 8.1 / 13.1; one prompt of 512 10.5 / 12.3; 32 prompts of
+    // 512 182 / 194).  Two tiles against the same keys otherwise, which read K and
+    // V half as often (16 prompts of 2048 282 / 246; 4096 tokens 145 / 134).
+    p.nt = avg_q <= p.tok || avg_k < 6 * kTileN ? 1 : 2;
+    p.blocks = Tq / (p.nt * p.tok) + B;
     if (p.blocks > Tq) p.blocks = Tq;
-    // split the keys when the blocks fill less than half of the SMs, a split
+    // split the keys when the blocks fill less than half of the places, a split
     // keeping at least four key tiles
-    const int64_t items = B * ceil_div(avg_q, kNT * p.tok) * p.HC;
+    const int64_t items = B * ceil_div(avg_q, p.nt * p.tok) * p.HC, places = static_cast<int64_t>(sm_count) * (p.nt == 1 ? 2 : 1);
     int64_t splits = 1;
-    if (2 * items <= sm_count) {
-        splits = sm_count / items;
+    if (2 * items <= places) {
+        splits = places / items;
         const int64_t most = avg_k / (4 * kTileN);
         if (splits > most) splits = most;
         if (splits < 1) splits = 1;
@@ -740,7 +819,7 @@ Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, in
     size_t off = kWorkspaceErrBytes;
     p.off_part = p.off_ml = off;
     if (splits > 1) {
-        const int64_t rows = p.blocks * p.HC * kNT * kTileM * splits;
+        const int64_t rows = p.blocks * p.HC * p.nt * kTileM * splits;
         off += static_cast<size_t>(rows * D) * sizeof(float);
         p.off_ml = off;
         off += static_cast<size_t>(rows) * 2 * sizeof(float);
@@ -749,16 +828,21 @@ Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, in
     return p;
 }
 
+template <int DP, bool F16, int NT>
+cudaError_t launch_form(const Maps& maps, const Args& a, int64_t grid, cudaStream_t stream) {
+    static const cudaError_t limit =
+        cudaFuncSetAttribute(prompt_kernel<DP, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP, NT>());
+    if (limit != cudaSuccess) return limit;
+    return launch_after(prompt_kernel<DP, F16, NT>, dim3(static_cast<unsigned>(grid)), Form<NT>::kThreads,
+                        smem_bytes<DP, NT>(), stream, maps, a);
+}
+
 template <int DP, bool F16>
 cudaError_t launch_tiles(const Maps& maps, const Args& a, int64_t grid, cudaStream_t stream) {
-    static const cudaError_t limit =
-        cudaFuncSetAttribute(prompt_kernel<DP, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP>());
-    if (limit != cudaSuccess) return limit;
-    cudaError_t e = launch_after(prompt_kernel<DP, F16>, dim3(static_cast<unsigned>(grid)), kThreads, smem_bytes<DP>(),
-                                 stream, maps, a);
+    const cudaError_t e = a.nt == 1 ? launch_form<DP, F16, 1>(maps, a, grid, stream) : launch_form<DP, F16, 2>(maps, a, grid, stream);
     if (e != cudaSuccess || a.splits == 1) return e;
-    const int64_t combine = grid / a.splits * (kNT * kTileM / kCombineRows);
-    return launch_after(combine_kernel<F16>, dim3(static_cast<unsigned>(combine)), kCombineWarps * 32, 0, stream, a);
+    const int64_t combine = grid / a.splits * a.nt * (a.D / 8);
+    return launch_after(combine_kernel<F16>, dim3(static_cast<unsigned>(combine)), kCombineThreads, 0, stream, a);
 }
 
 }  // namespace
@@ -800,6 +884,7 @@ cudaError_t launch_prompt(bool x_f16, const PromptArgs& pa, void* ws, int sm_cou
     a.Hq = pa.Hq;
     a.G = pa.Hq / pa.Hkv;
     a.D = pa.D;
+    a.nt = p.nt;
     a.gs = p.gs;
     a.tok = p.tok;
     a.chunks = p.chunks;
