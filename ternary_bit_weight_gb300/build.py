@@ -1,8 +1,9 @@
 """Build libtern.so in-tree with nvcc for sm_103a (GB300).
 
 Each ``csrc/*.cu`` file is compiled separately and in parallel, then linked
-into ``_build/libtern.so`` against the shared CUDA runtime.  Rebuilds only
-when a source or header is newer than the library.
+into ``_build/libtern.so`` against the shared CUDA runtime; ``csrc/tern_python.c``
+becomes ``_build/_tern_python.so``, the argument marshalling of the calls made
+for single tokens.  Rebuilds only when a source or header is newer.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libtern.so")
+PY_SRC = os.path.join(CSRC, "tern_python.c")
+PY_LIB = os.path.join(BUILD, "_tern_python.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-Wall",
@@ -40,11 +44,11 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(PY_LIB):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(PY_LIB))
     deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
-        + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
+        + glob.glob(os.path.join(INCLUDE, "*.h")) + [PY_SRC, __file__]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -77,6 +81,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if res.returncode != 0:
         raise RuntimeError(f"link of libtern.so failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, PY_SRC,
+           "-o", PY_LIB + f".tmp{os.getpid()}", "-L", BUILD, "-l:libtern.so", "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"gcc failed for tern_python.c:\n{res.stdout}\n{res.stderr}")
+    os.replace(PY_LIB + f".tmp{os.getpid()}", PY_LIB)
     return LIB
 
 

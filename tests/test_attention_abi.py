@@ -154,3 +154,28 @@ def test_binding_raises_with_the_status():
         tb.tern_rope(0, 0, 4, 100, 0, None, None, 1.0, 1, FAKE, 100, FAKE, 100, stream=0)
     assert e.value.status == SHAPE
     assert "TERN_ERR_SHAPE" in str(e.value)
+
+
+def test_binding_converts_arguments():
+    """Pointers may be None, addresses or tensors; what is neither is refused before the library is called."""
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(64, dtype=torch.bfloat16)
+
+    def status(q):
+        try:
+            tb.tern_rope(0, 0, 4, 16, 16, FAKE, FAKE, 1.0, 1, q, 8, FAKE, 16, stream=0)   # ldq < Hq * D
+        except tb.TernError as e:
+            return e.status
+
+    assert status(None) == NULL
+    assert status(FAKE) == SHAPE
+    assert status(x) == SHAPE
+    for bad in ("x", 1.5):
+        with pytest.raises((TypeError, AttributeError)):
+            status(bad)
+    with pytest.raises(TypeError):
+        tb.tern_rope(0, 0, 4, 16, 1.5, FAKE, FAKE, 1.0, 1, FAKE, 16, FAKE, 16, stream=0)
+    with pytest.raises(OverflowError):
+        tb.tern_rope(1 << 40, 0, 4, 16, 16, FAKE, FAKE, 1.0, 1, FAKE, 16, FAKE, 16, stream=0)
+    with pytest.raises(TypeError):
+        tb.library() and tb._native.tern_rope(0, 0)
