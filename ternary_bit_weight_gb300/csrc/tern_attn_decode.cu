@@ -154,6 +154,24 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
+// N (2 or 4) floats at once.
+template <int N>
+struct __align__(4 * N) Floats {
+    float v[N];
+};
+template <int N>
+__device__ __forceinline__ Floats<N> load_l2(const float* p) {
+    Floats<N> x;
+    if constexpr (N == 4) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(p));
+        x.v[0] = u.x, x.v[1] = u.y, x.v[2] = u.z, x.v[3] = u.w;
+    } else {
+        const float2 u = __ldcg(reinterpret_cast<const float2*>(p));
+        x.v[0] = u.x, x.v[1] = u.y;
+    }
+    return x;
+}
+
 template <int BYTES>
 __device__ __forceinline__ void copy_async_or_zero(uint32_t dst, const void* src, bool there) {
     const int n = there ? BYTES : 0;   // the rest is filled with zeros
@@ -202,9 +220,9 @@ __device__ __forceinline__ int arrive(int32_t* counter) {
 }
 
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-    return x;
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ float warp_add(float x) {
 #pragma unroll
@@ -276,11 +294,12 @@ __device__ __forceinline__ int64_t warp_sum(int64_t n) {
     return lo + (hi << 24);
 }
 
-__device__ __forceinline__ Share share_of(const Args& a, int lane) {
+// `mine` is the length of the lane's first sequence (0 where there is none).
+__device__ __forceinline__ Share share_of(const Args& a, int lane, int mine) {
     int64_t tiles = 0;
     uint32_t some = 0;
     for (int b = lane; b < a.B; b += 32) {
-        const int n = tiles_of(length_of(a, b));
+        const int n = tiles_of(b == lane ? mine : length_of(a, b));
         tiles += n;
         some += n > 0;
     }
@@ -300,7 +319,7 @@ __device__ __forceinline__ Share share_of(const Args& a, int lane) {
             s.whole = static_cast<int>(q);
             int64_t ctas = 0;
             for (int b = lane; b < a.B; b += 32)
-                ctas += (static_cast<uint32_t>(tiles_of(length_of(a, b))) + s.whole - 1) / static_cast<uint32_t>(s.whole);
+                ctas += (static_cast<uint32_t>(tiles_of(b == lane ? mine : length_of(a, b))) + s.whole - 1) / static_cast<uint32_t>(s.whole);
             s.ctas = warp_sum(ctas) * a.Hv;
         }
     }
@@ -323,13 +342,13 @@ __device__ __forceinline__ void next_segment(const Args& a, Segment& s) {
 }
 
 // The CTA's first segment (one warp); begin == end: it has none.
-__device__ __forceinline__ Segment first_segment(const Args& a, const Share& share, int64_t cta, int lane) {
+__device__ __forceinline__ Segment first_segment(const Args& a, const Share& share, int64_t cta, int lane, int mine) {
     Segment s;
     const int64_t u0 = share.whole ? cta : quotient(share.weight * cta, share.ctas);
     const int64_t u1 = share.whole ? cta + 1 : quotient(share.weight * (cta + 1), share.ctas);
     int64_t base = 0;
     for (int b0 = 0;; b0 += 32) {
-        const int len = b0 + lane < a.B ? length_of(a, b0 + lane) : 0;
+        const int len = b0 == 0 ? mine : b0 + lane < a.B ? length_of(a, b0 + lane) : 0;
         const uint32_t tiles = tiles_of(len);
         // CTAs, or weight, of an item: below 2^28, of a sequence's Hv items below 2^40
         const uint32_t each = tiles == 0 ? 0 : share.whole ? (tiles + share.whole - 1) / static_cast<uint32_t>(share.whole) : tiles + kEnd;
@@ -415,6 +434,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
     grid_launch_dependents();
     grid_dependency_wait();
 
+    const int mine0 = lane < a.B ? length_of(a, lane) : 0;   // the lane's first sequence
     // sequences of length zero see nothing
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (length_of(a, b) != 0) continue;
@@ -426,9 +446,9 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 a.lse[static_cast<int64_t>(b) * a.Hkv * a.G + h] = -CUDART_INF_F;
     }
 
-    const Share share = share_of(a, lane);
+    const Share share = share_of(a, lane, mine0);
     if (blockIdx.x >= share.ctas) return;
-    Segment seg = first_segment(a, share, blockIdx.x, lane);
+    Segment seg = first_segment(a, share, blockIdx.x, lane, mine0);
     if (seg.begin == seg.end) return;
 
     // ---------------------------------------------------- loads of a warp
@@ -879,15 +899,18 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 for (int i = 0; i < S::kEach; ++i) sum[i] = 0.0f;
                 for (int w = 0; w < active; ++w) {
                     const float f = __shfl_sync(0xffffffffu, fw, w);
-                    const float* src = merge + w * 8 * DP + S::merge_at(warp, lane * S::kEach);
+                    const Floats<S::kEach> x =
+                        *reinterpret_cast<const Floats<S::kEach>*>(merge + w * 8 * DP + S::merge_at(warp, lane * S::kEach));
 #pragma unroll
-                    for (int i = 0; i < S::kEach; ++i) sum[i] += src[i] * f;
+                    for (int i = 0; i < S::kEach; ++i) sum[i] += x.v[i] * f;
                 }
                 if (whole) {
                     finish(done, head, sum, M, MO, L);
                 } else {
+                    Floats<S::kEach> x;
 #pragma unroll
-                    for (int i = 0; i < S::kEach; ++i) slot[head * DP + lane * S::kEach + i] = sum[i];
+                    for (int i = 0; i < S::kEach; ++i) x.v[i] = sum[i];
+                    *reinterpret_cast<Floats<S::kEach>*>(slot + head * DP + lane * S::kEach) = x;
                     if (lane == 0) {
                         float* dst = slot + kSlotRows * DP + head * 3;
                         dst[0] = M;
@@ -935,30 +958,27 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
             const int head = 8 * c + warp;
             if (head >= heads) continue;
             float M = kNone, MO = kNone, L = 0.0f;
-            for (int i = c0 + lane; i <= c1; i += 32) {
-                const float* sp = part(i) + kSlotRows * DP + head * 3;
-                M = fmaxf(M, __ldcg(sp));
-                MO = fmaxf(MO, __ldcg(sp + 1));
-            }
-            M = warp_max(M);
-            MO = warp_max(MO);
             float sum[S::kEach];
 #pragma unroll
             for (int i = 0; i < S::kEach; ++i) sum[i] = 0.0f;
-            for (int i0 = c0; i0 <= c1; i0 += 32) {
-                float f = 0.0f;
-                if (i0 + lane <= c1) {
-                    const float* sp = part(i0 + lane) + kSlotRows * DP + head * 3;
-                    L += __ldcg(sp + 2) * exp2_approx(__ldcg(sp) - M);
-                    f = exp2_approx(__ldcg(sp + 1) - MO);
-                }
+            for (int i0 = c0; i0 <= c1; i0 += 32) {   // a lane has one part's statistics
                 const int count = min(32, c1 - i0 + 1);
-#pragma unroll 8
+                const float* sp = part(i0 + min(lane, count - 1)) + kSlotRows * DP + head * 3;
+                const bool had = lane < count;
+                const float mi = had ? __ldcg(sp) : kNone, moi = had ? __ldcg(sp + 1) : kNone, li = had ? __ldcg(sp + 2) : 0.0f;
+                const float up = fmaxf(M, warp_max(mi)), upo = fmaxf(MO, warp_max(moi));
+                const float keep = exp2_approx(MO - upo), f = exp2_approx(moi - upo);
+                L = L * exp2_approx(M - up) + li * exp2_approx(mi - up);
+                M = up;
+                MO = upo;
+#pragma unroll
+                for (int i = 0; i < S::kEach; ++i) sum[i] *= keep;
+#pragma unroll 4
                 for (int k = 0; k < count; ++k) {
-                    const float* src = part(i0 + k) + head * DP + lane * S::kEach;
+                    const Floats<S::kEach> x = load_l2<S::kEach>(part(i0 + k) + head * DP + lane * S::kEach);
                     const float fk = __shfl_sync(0xffffffffu, f, k);
 #pragma unroll
-                    for (int i = 0; i < S::kEach; ++i) sum[i] += __ldcg(src + i) * fk;
+                    for (int i = 0; i < S::kEach; ++i) sum[i] += x.v[i] * fk;
                 }
             }
             finish(done, head, sum, M, MO, warp_add(L));
