@@ -82,6 +82,7 @@ struct Args {
     int Hkv, passes, Hv;   // Hv = Hkv * passes: (key/value head, 16 of its query heads)
     int shift;
     int tma;               // tiles come by TMA (else a copy per lane)
+    int narrow;            // all of the work's weight x CTAs is below 2^31
     float scale2;          // scale * log2(e)
 };
 
@@ -283,46 +284,53 @@ __device__ __forceinline__ int length_of(const Args& a, int b) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-// Quotients of what nearly always fits 32 bits (a 64-bit division takes
-// several hundred cycles of the start, which single sequences feel).
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-    return ((x | y) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
-}
-__device__ __forceinline__ int64_t warp_sum(int64_t n) {
-    const int64_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(n) & 0xFFFFFFu);
-    const int64_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(n >> 24));   // n is below 2^51
-    return lo + (hi << 24);
+// The arithmetic of the start is done in T: 32 bits where the host has seen that
+// the largest product fits (64-bit divisions and their code made the start of a
+// short call 1 us longer), else 64 bits.
+template <typename T>
+__device__ __forceinline__ T warp_sum(T n) {
+    if constexpr (sizeof(T) == 4) {
+        return __reduce_add_sync(0xffffffffu, n);
+    } else {
+        const int64_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(n) & 0xFFFFFFu);
+        const int64_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(n >> 24));   // n is below 2^51
+        return lo + (hi << 24);
+    }
 }
 
 // `mine` is the length of the lane's first sequence (0 where there is none).
+template <typename T>
 __device__ __forceinline__ Share share_of(const Args& a, int lane, int mine) {
-    int64_t tiles = 0;
+    T tiles = 0;
     uint32_t some = 0;
     for (int b = lane; b < a.B; b += 32) {
         const int n = tiles_of(b == lane ? mine : length_of(a, b));
         tiles += n;
         some += n > 0;
     }
-    tiles = warp_sum(tiles) * a.Hv;
-    const int64_t items = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, some)) * a.Hv;
-    const int64_t grid = gridDim.x;
+    tiles = warp_sum<T>(tiles) * a.Hv;
+    const T items = static_cast<T>(__reduce_add_sync(0xffffffffu, some)) * a.Hv;
+    const T grid = gridDim.x;
     Share s;
     s.whole = 0;
-    s.weight = tiles + kEnd * items;
-    s.ctas = tiles == 0 ? 0 : max(static_cast<int64_t>(1), min(grid, max(items, s.weight / (kMinTiles + kEnd))));
+    const T weight = tiles + kEnd * items;
+    s.weight = weight;
+    T ctas = tiles == 0 ? T(0) : max(T(1), min(grid, max(items, weight / (kMinTiles + kEnd))));
     if (tiles > 0 && items < grid) {
         // an item's parts add up one after the other: n tiles are split no finer
         // than where a tile less per warp costs as much as the parts it adds
-        const int64_t even = static_cast<int64_t>(sqrtf(kPart * static_cast<float>(tiles) / static_cast<float>(items)));
-        const int64_t q = max(max(static_cast<int64_t>(kMinTiles), even), quotient(tiles + grid - items - 1, grid - items));
-        if (q + kEnd <= quotient(s.weight, s.ctas) + 2 * kEnd && q <= INT32_MAX) {
+        const T even = static_cast<T>(sqrtf(kPart * __fdividef(static_cast<float>(tiles), static_cast<float>(items))));
+        const T q = max(max(T(kMinTiles), even), (tiles + grid - items - 1) / (grid - items));
+        // q + kEnd <= weight / ctas + 2 kEnd
+        if ((q > kEnd ? (q - kEnd) * ctas : T(0)) <= weight && q <= T(INT32_MAX)) {
             s.whole = static_cast<int>(q);
-            int64_t ctas = 0;
+            T parts = 0;
             for (int b = lane; b < a.B; b += 32)
-                ctas += (static_cast<uint32_t>(tiles_of(b == lane ? mine : length_of(a, b))) + s.whole - 1) / static_cast<uint32_t>(s.whole);
-            s.ctas = warp_sum(ctas) * a.Hv;
+                parts += (static_cast<uint32_t>(tiles_of(b == lane ? mine : length_of(a, b))) + s.whole - 1) / static_cast<uint32_t>(s.whole);
+            ctas = warp_sum<T>(parts) * a.Hv;
         }
     }
+    s.ctas = ctas;
     return s;
 }
 
@@ -342,20 +350,22 @@ __device__ __forceinline__ void next_segment(const Args& a, Segment& s) {
 }
 
 // The CTA's first segment (one warp); begin == end: it has none.
-__device__ __forceinline__ Segment first_segment(const Args& a, const Share& share, int64_t cta, int lane, int mine) {
+template <typename T>
+__device__ __forceinline__ Segment first_segment(const Args& a, const Share& share, int lane, int mine) {
     Segment s;
-    const int64_t u0 = share.whole ? cta : quotient(share.weight * cta, share.ctas);
-    const int64_t u1 = share.whole ? cta + 1 : quotient(share.weight * (cta + 1), share.ctas);
-    int64_t base = 0;
+    const T cta = blockIdx.x, weight = static_cast<T>(share.weight), ctas = static_cast<T>(share.ctas);
+    const T u0 = share.whole ? cta : weight * cta / ctas;
+    const T u1 = share.whole ? cta + 1 : weight * (cta + 1) / ctas;
+    T base = 0;
     for (int b0 = 0;; b0 += 32) {
         const int len = b0 == 0 ? mine : b0 + lane < a.B ? length_of(a, b0 + lane) : 0;
         const uint32_t tiles = tiles_of(len);
-        // CTAs, or weight, of an item: below 2^28, of a sequence's Hv items below 2^40
+        // CTAs, or weight, of an item: below 2^28
         const uint32_t each = tiles == 0 ? 0 : share.whole ? (tiles + share.whole - 1) / static_cast<uint32_t>(share.whole) : tiles + kEnd;
-        int64_t incl = static_cast<int64_t>(each) * a.Hv;
+        T incl = static_cast<T>(each) * a.Hv;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t up = __shfl_up_sync(0xffffffffu, incl, d);
+            const T up = __shfl_up_sync(0xffffffffu, incl, d);
             if (lane >= d) incl += up;
         }
         const uint32_t past = __ballot_sync(0xffffffffu, base + incl > u0);
@@ -364,21 +374,21 @@ __device__ __forceinline__ Segment first_segment(const Args& a, const Share& sha
             s.b = b0 + src;
             s.len = __shfl_sync(0xffffffffu, len, src);
             s.tiles = tiles_of(s.len);
-            const int64_t n = __shfl_sync(0xffffffffu, each, src);
-            const int64_t in = u0 - base - (__shfl_sync(0xffffffffu, incl, src) - n * a.Hv);
-            s.hv = static_cast<int>(quotient(in, n));
-            const int64_t at = in - s.hv * n;
+            const T n = __shfl_sync(0xffffffffu, each, src);
+            const T in = u0 - base - (__shfl_sync(0xffffffffu, incl, src) - n * a.Hv);
+            s.hv = static_cast<int>(in / n);
+            const int at = static_cast<int>(in - s.hv * n);
             if (share.whole) {
                 const int per = static_cast<int>((s.tiles + static_cast<uint32_t>(n) - 1) / static_cast<uint32_t>(n));
                 s.start = cta - at;
-                s.begin = static_cast<int>(at) * per;
+                s.begin = at * per;
                 s.end = min(s.tiles, s.begin + per);
                 s.left = 0;
             } else {
-                const int64_t upto = min(n, at + (u1 - u0));
+                const int upto = static_cast<int>(min(n, at + (u1 - u0)));
                 s.start = u0 - at;
-                s.begin = static_cast<int>(max(static_cast<int64_t>(0), at - kEnd));
-                s.end = static_cast<int>(max(static_cast<int64_t>(s.begin), upto - kEnd));
+                s.begin = max(0, at - kEnd);
+                s.end = max(s.begin, upto - kEnd);
                 s.left = (u1 - u0) - (upto - at);
                 if (s.begin == s.end && s.left > kEnd) next_segment(a, s);
             }
@@ -388,17 +398,33 @@ __device__ __forceinline__ Segment first_segment(const Args& a, const Share& sha
     }
 }
 
+// Share and first segment of the CTA; false: it has none.
+template <typename T>
+__device__ __forceinline__ bool start(const Args& a, int lane, int mine, Share& share, Segment& s) {
+    share = share_of<T>(a, lane, mine);
+    if (blockIdx.x >= share.ctas) return false;
+    s = first_segment<T>(a, share, lane, mine);
+    return s.begin != s.end;
+}
+__device__ __noinline__ bool start_wide(const Args& a, int lane, int mine, Share& share, Segment& s) {
+    return start<int64_t>(a, lane, mine, share, s);
+}
+
 // CTAs that have a part of the segment's item.
+template <typename T>
 __device__ __forceinline__ void parts_of(const Share& share, const Segment& s, int& c0, int& c1) {
     if (share.whole) {
         c0 = static_cast<int>(s.start);
         c1 = c0 + static_cast<int>((static_cast<uint32_t>(s.tiles) + share.whole - 1) / static_cast<uint32_t>(share.whole)) - 1;
     } else {
         // the CTA that has weight unit u of the total W is the last c with W c / C <= u
-        const int64_t u = s.start + kEnd;
-        c0 = static_cast<int>(quotient((u + 1) * share.ctas - 1, share.weight));
-        c1 = static_cast<int>(quotient((u + s.tiles) * share.ctas - 1, share.weight));
+        const T u = static_cast<T>(s.start) + kEnd, weight = static_cast<T>(share.weight), ctas = static_cast<T>(share.ctas);
+        c0 = static_cast<int>(((u + 1) * ctas - 1) / weight);
+        c1 = static_cast<int>(((u + s.tiles) * ctas - 1) / weight);
     }
+}
+__device__ __noinline__ void parts_of_wide(const Share& share, const Segment& s, int& c0, int& c1) {
+    parts_of<int64_t>(share, s, c0, c1);
 }
 
 template <int DP, int KV, bool F16, int COLS>
@@ -446,10 +472,9 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 a.lse[static_cast<int64_t>(b) * a.Hkv * a.G + h] = -CUDART_INF_F;
     }
 
-    const Share share = share_of(a, lane, mine0);
-    if (blockIdx.x >= share.ctas) return;
-    Segment seg = first_segment(a, share, blockIdx.x, lane, mine0);
-    if (seg.begin == seg.end) return;
+    Share share;
+    Segment seg;
+    if (!(a.narrow ? start<uint32_t>(a, lane, mine0, share, seg) : start_wide(a, lane, mine0, share, seg))) return;
 
     // ---------------------------------------------------- loads of a warp
     // Page ids are looked up for a batch of up to 32 of the warp's tiles in one
@@ -925,7 +950,8 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
             // at most two of a CTA's segments are parts of an item: its first and its last
             if (threadIdx.x == 0) {
                 int c0, c1;
-                parts_of(share, done, c0, c1);
+                if (a.narrow) parts_of<uint32_t>(share, done, c0, c1);
+                else parts_of_wide(share, done, c0, c1);
                 volatile int* info = part_info + 4 * (parts & 1);
                 info[0] = done.b, info[1] = done.hv, info[2] = c0, info[3] = c1;
                 const int before = arrive(a.arrived + c0);
@@ -1008,6 +1034,7 @@ template <int DP, int KV, bool F16, int COLS>
 cudaError_t launch(Args& a, const DecodeArgs& d, int sm_count, cudaStream_t stream) {
     using S = Shape<DP, KV, COLS>;
     const int grid = grid_size(d.B, a.Hv, a.capacity, static_cast<int64_t>(sm_count) * S::kCtas);
+    a.narrow = static_cast<double>(d.B) * a.Hv * static_cast<double>(a.capacity / kTile + 1 + kEnd) * (grid + 1) < 2147483648.0;
     Maps maps;
     memset(&maps, 0, sizeof(maps));
     // pages of a tile and more, whose (page, head) count fits a coordinate
