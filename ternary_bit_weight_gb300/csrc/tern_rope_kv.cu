@@ -87,6 +87,28 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
                       pack_x2<F16>(x[6], x[7]));
 }
 
+// Largest magnitude of a head's values, 16 of them in each of its LANES lanes; a
+// NaN among them stays.  Magnitudes are compared two by two as 16-bit values.
+template <bool F16>
+__device__ __forceinline__ uint32_t max_x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if (F16)
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+template <int LANES, bool F16>
+__device__ __forceinline__ float head_max(const uint4& ua, const uint4& ub) {
+    const uint32_t sign = 0x7FFF7FFFu;
+    uint32_t m = max_x2<F16>(max_x2<F16>(max_x2<F16>(ua.x & sign, ua.y & sign), max_x2<F16>(ua.z & sign, ua.w & sign)),
+                             max_x2<F16>(max_x2<F16>(ub.x & sign, ub.y & sign), max_x2<F16>(ub.z & sign, ub.w & sign)));
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d >>= 1) m = max_x2<F16>(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float2 f = unpack_x2<F16>(m);
+    return f.x != f.x ? f.x : f.y != f.y ? f.y : fmaxf(f.x, f.y);
+}
+
 // 8 codes of x * inv as two words.
 template <int KV>
 __device__ __forceinline__ uint2 encode8(const float* x, float inv) {
@@ -216,21 +238,13 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const TokenArgs a)
                 }
             } else {
                 // codes from the values rounded to 16 bits, as a separate write sees them
-                float x[16], m = 0.0f;
-                bool finite = true;
-                unpack8<F16>(ua, x);
-                unpack8<F16>(ub, x + 8);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    m = fmaxf(m, fabsf(x[i]));
-                    finite = finite && fabsf(x[i]) <= FLT_MAX;
-                }
-                if (!finite) m = __int_as_float(0x7f800000);   // marks the whole head
-#pragma unroll
-                for (int d = LANES / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                const float m = head_max<LANES, F16>(ua, ub);   // NaN or infinite with any such value
                 if (store) {
                     const float top = KV == kKvE4m3 ? 448.0f : 127.0f;
-                    const bool bad = m > FLT_MAX;
+                    const bool bad = !(m <= FLT_MAX);
+                    float x[16];
+                    unpack8<F16>(ua, x);
+                    unpack8<F16>(ub, x + 8);
                     // m below top / FLT_MAX: the largest finite inverse keeps codes within the range
                     const float inv = m > 0.0f && !bad ? fminf(__fdiv_rn(top, m), FLT_MAX) : 0.0f;
                     if (bad) {
