@@ -796,13 +796,16 @@ Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, in
     }
     p.chunks = static_cast<int>(ceil_div(G, p.gs));
     p.HC = static_cast<int>(Hkv) * p.chunks;
-    // One tile per CTA and two CTAs per SM, where the second tile of a block would
-    // be empty or the work per CTA is short, so that one CTA's start and end run
-    // beside the other's products (27B-class heads, us, one tile / two: 32 queries
-    // of up to 48 tokens 8.1 / 13.1; one prompt of 512 10.5 / 12.3; 32 prompts of
-    // 512 182 / 194).  Two tiles against the same keys otherwise, which read K and
-    // V half as often (16 prompts of 2048 282 / 246; 4096 tokens 145 / 134).
-    p.nt = avg_q <= p.tok || avg_k < 6 * kTileN ? 1 : 2;
+    // One tile per CTA and two CTAs per SM where the second tile of a block would be
+    // empty, where blocks are very short, so that one CTA's start and end run beside
+    // the other's products, and where short blocks fit the GPU at once and their
+    // latency counts.  Two tiles against the same keys otherwise, which read K and V
+    // half as often.  27B-class heads, us, one tile / two: 32 queries of up to 48
+    // tokens 8.1 / 13.1; 200 prompts of 64 142 / 177; one prompt of 512 10.5 / 12.3;
+    // 24 documents of up to 1023 57 / 54; 16 prompts of 2048 282 / 246; 4096 tokens
+    // 145 / 134; 256 new against 16384 93 / 74.
+    const int64_t single = B * ceil_div(avg_q, p.tok) * p.HC;
+    p.nt = avg_q <= p.tok || avg_k < 2 * kTileN || (avg_k < 6 * kTileN && single <= 2 * sm_count) ? 1 : 2;
     p.blocks = Tq / (p.nt * p.tok) + B;
     if (p.blocks > Tq) p.blocks = Tq;
     // split the keys when the blocks fill less than half of the places, a split

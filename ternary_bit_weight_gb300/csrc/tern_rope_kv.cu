@@ -18,9 +18,12 @@
 // lane.  m is a butterfly over the task's lanes.  A warp serves one token, or
 // a part of its heads when tokens are few: its lanes compute the token's angles
 // once, keep them in registers for all heads, and walk the heads with two
-// loads ahead.  No barrier and no shared memory: with one CTA per token and
-// the angles in shared memory, CTAs stood at barriers and start-up for most of
-// their life (8191 tokens of 48 heads: 42 us, 4.8 TB/s).
+// loads ahead (one where it quantises, too, which at 72 registers leaves 28 warps
+// on an SM: 8191 tokens rotated, stored as int8 and read back 58 -> 52 us).  A
+// CTA is one warp, so that warps come and go one by one.  No barrier and no
+// shared memory: with one CTA per token and the angles in shared memory, CTAs
+// stood at barriers and start-up for most of their life (8191 tokens of 48 heads:
+// 42 us, 4.8 TB/s, against 34 us, 5.9 TB/s).
 
 #include <cuda_fp8.h>
 #include <float.h>
@@ -32,7 +35,7 @@
 namespace tern {
 namespace {
 
-constexpr int kTokenThreads = 128;
+constexpr int kTokenThreads = 32;
 constexpr int kTokenWarps = 8;     // per SM, at least, before a token's heads stay in one warp
 constexpr int kReadThreads = 256;
 
@@ -131,12 +134,15 @@ __device__ __forceinline__ uint2 encode8(const float* x, float inv) {
     return make_uint2(w[0], w[1]);
 }
 
+__host__ __device__ constexpr bool coded(int kv) { return kv == kKvE4m3 || kv == kKvI8; }
+
 // One warp per token and part of its heads: rotate queries and keys, and
 // (KV != kKvNone) store keys and values in the cache.
 template <int LANES, bool F16, int KV>
-__global__ void __launch_bounds__(kTokenThreads) token_kernel(const TokenArgs a) {
+__global__ void __launch_bounds__(kTokenThreads, coded(KV) ? 28 : 0) token_kernel(const TokenArgs a) {
     constexpr int kSub = 32 / LANES;      // heads at a time
     constexpr int kOwn = 8 / kSub;        // pairs whose angle a lane computes
+    constexpr int kAhead = coded(KV) ? 1 : 2;   // tasks loaded ahead
     grid_launch_dependents();
     grid_dependency_wait();
     const int64_t w = (int64_t)blockIdx.x * (kTokenThreads / 32) + (threadIdx.x >> 5);
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const TokenArgs a)
     int h = first + sub;
     uint4 ua, ub, na, nb;
     load(h, ua, ub);
-    load(h + kSub, na, nb);
+    if (kAhead == 2) load(h + kSub, na, nb);
     int64_t slot = -1;
     if (KV != kKvNone) {
         slot = a.slots[t];
@@ -196,7 +202,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const TokenArgs a)
     for (int h0 = first; h0 < tasks; h0 += kSub, h += kSub) {
         const bool mine = h < tasks && live;
         uint4 la, lb;
-        load(h + 2 * kSub, la, lb);
+        load(h + kAhead * kSub, la, lb);
         const bool is_v = h >= a.Hq + a.Hk;
         if (turned && !is_v) {
             float x[16], y[16];
@@ -258,8 +264,12 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(const TokenArgs a)
                 }
             }
         }
-        ua = na, ub = nb;
-        na = la, nb = lb;
+        if (kAhead == 2) {
+            ua = na, ub = nb;
+            na = la, nb = lb;
+        } else {
+            ua = la, ub = lb;
+        }
     }
 }
 
