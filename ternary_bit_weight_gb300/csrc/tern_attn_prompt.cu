@@ -719,16 +719,17 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
     }
 }
 
-// Sum of the splits' partial results in split order: a thread per row and 8
-// columns, the rows of a warp one after the other as they were written.
-constexpr int kCombineThreads = 128;
+// Sum of the splits' partial results in split order: `parts` CTAs per tile, a
+// thread per row, 8 columns at a time, the rows of a warp one after the other as
+// they were written.
+constexpr int kCombineThreads = kTileM;
 template <bool F16>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Args a) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Args a, int parts) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int r = threadIdx.x, runs = a.D / 8;
-    const int64_t tile = blockIdx.x / runs, item = tile / a.nt;
-    const int run = static_cast<int>(blockIdx.x % runs), i = static_cast<int>(tile % a.nt);
+    const int r = threadIdx.x;
+    const int64_t tile = blockIdx.x / parts, item = tile / a.nt;
+    const int i = static_cast<int>(tile % a.nt);
     const int hc = static_cast<int>(item % a.HC), block = static_cast<int>(item / a.HC);
     Item it;
     if (!find_item(a, block, threadIdx.x & 31, it)) return;
@@ -736,27 +737,31 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Args a) 
     const int token = r / a.gs, head = r - token * a.gs, t = it.t0 + i * a.tok + token;
     if (token >= a.tok || t >= it.nq || head >= min(a.gs, (hk + 1) * a.G - head0)) return;
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + tile * a.splits * kTileM + r;
-    const float4* part = reinterpret_cast<const float4*>(a.part) + (tile * a.splits * (a.D / 4) + 2 * run) * kTileM + r;
     float M = kNone, L = 0.0f;
     for (int s = 0; s < a.splits; ++s) M = fmaxf(M, ml[s * kTileM].x);
-    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int s = 0; s < a.splits; ++s) {
-        const float2 x = ml[s * kTileM];
-        const float4 u = part[static_cast<int64_t>(s) * (a.D / 4) * kTileM];
-        const float4 v = part[(static_cast<int64_t>(s) * (a.D / 4) + 1) * kTileM];
-        const float f = exp2_approx(x.x - M);
-        L += x.y * f;
-        if (x.y != 0.0f) {   // a split that the row sees nothing of adds nothing
-            sum[0] += u.x * f, sum[1] += u.y * f, sum[2] += u.z * f, sum[3] += u.w * f;
-            sum[4] += v.x * f, sum[5] += v.y * f, sum[6] += v.z * f, sum[7] += v.w * f;
-        }
-    }
+    for (int s = 0; s < a.splits; ++s) L += ml[s * kTileM].y * exp2_approx(ml[s * kTileM].x - M);
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     const int64_t row = it.q0 + t;
-    *reinterpret_cast<uint4*>(a.o + row * a.ldo + static_cast<int64_t>(head0 + head) * a.D + 8 * run) =
-        make_uint4(pack_x2<F16>(sum[0] * inv, sum[1] * inv), pack_x2<F16>(sum[2] * inv, sum[3] * inv),
-                   pack_x2<F16>(sum[4] * inv, sum[5] * inv), pack_x2<F16>(sum[6] * inv, sum[7] * inv));
-    if (run == 0 && a.lse != nullptr) a.lse[row * a.Hq + head0 + head] = L == 0.0f ? -CUDART_INF_F : M * kLn2 + logf(L);
+    const int h = head0 + head;
+    for (int run = blockIdx.x % parts; run < a.D / 8; run += parts) {
+        const float4* part = reinterpret_cast<const float4*>(a.part) + (tile * a.splits * (a.D / 4) + 2 * run) * kTileM + r;
+        float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+        for (int s = 0; s < a.splits; ++s) {
+            const float2 x = ml[s * kTileM];
+            const float4 u = part[static_cast<int64_t>(s) * (a.D / 4) * kTileM];
+            const float4 v = part[(static_cast<int64_t>(s) * (a.D / 4) + 1) * kTileM];
+            const float f = exp2_approx(x.x - M);
+            if (x.y != 0.0f) {   // a split that the row sees nothing of adds nothing
+                sum[0] += u.x * f, sum[1] += u.y * f, sum[2] += u.z * f, sum[3] += u.w * f;
+                sum[4] += v.x * f, sum[5] += v.y * f, sum[6] += v.z * f, sum[7] += v.w * f;
+            }
+        }
+        *reinterpret_cast<uint4*>(a.o + row * a.ldo + static_cast<int64_t>(h) * a.D + 8 * run) =
+            make_uint4(pack_x2<F16>(sum[0] * inv, sum[1] * inv), pack_x2<F16>(sum[2] * inv, sum[3] * inv),
+                       pack_x2<F16>(sum[4] * inv, sum[5] * inv), pack_x2<F16>(sum[6] * inv, sum[7] * inv));
+        if (run == 0 && a.lse != nullptr) a.lse[row * a.Hq + h] = L == 0.0f ? -CUDART_INF_F : M * kLn2 + logf(L);
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -774,6 +779,8 @@ bool encode_heads(CUtensorMap* map, bool f16, const uint16_t* p, int64_t rows, i
                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+constexpr int64_t kMostPartial = 96 << 20;   // bytes of partial results: they stay in L2
 
 struct Plan {
     int nt, gs, tok, chunks, HC, splits;
@@ -808,15 +815,27 @@ Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, in
     p.nt = avg_q <= p.tok || avg_k < 2 * kTileN || (avg_k < 6 * kTileN && single <= 2 * sm_count) ? 1 : 2;
     p.blocks = Tq / (p.nt * p.tok) + B;
     if (p.blocks > Tq) p.blocks = Tq;
-    // split the keys when the blocks fill less than half of the places, a split
-    // keeping at least four key tiles
+    // Split the keys where that costs less by this estimate (us): waves of blocks,
+    // each a key tile at a time and 4.5 beside them; partial results written and
+    // read at 8 TB/s, and a second launch.  A split keeps at least four key tiles.
+    // From four waves on blocks of unequal length fill the GPU by themselves.
+    // 27B-class heads, us, split / not: 256 new tokens against 16384 74 / 198, 512
+    // 142 / 183, 1024 274 / 347, 2048 480 / 508; 8 x 128 against 4128 116 / 121.
     const int64_t items = B * ceil_div(avg_q, p.nt * p.tok) * p.HC, places = static_cast<int64_t>(sm_count) * (p.nt == 1 ? 2 : 1);
+    const double tiles = static_cast<double>(avg_k) / kTileN, step = p.nt == 1 ? 1.25 : 1.45;
     int64_t splits = 1;
-    if (2 * items <= places) {
-        splits = places / items;
-        const int64_t most = avg_k / (4 * kTileN);
-        if (splits > most) splits = most;
-        if (splits < 1) splits = 1;
+    if (items < 4 * places) {
+        double least = 0.0;
+        for (int64_t s = 1; s <= 32 && (s == 1 || 4 * s <= tiles); ++s) {
+            if (s > 1 && items * s * p.nt * kTileM * D * 4 > kMostPartial) break;
+            const double waves = static_cast<double>(ceil_div(items * s, places));
+            const double joined = s == 1 ? 0.0 : 3.0 + static_cast<double>(items * s * p.nt * kTileM * D) * 8.0 / 8.0e6;
+            const double cost = waves * (step * tiles / static_cast<double>(s) + 4.5) + joined;
+            if (s == 1 || cost < least) {
+                least = cost;
+                splits = s;
+            }
+        }
     }
     p.splits = static_cast<int>(splits);
     size_t off = kWorkspaceErrBytes;
@@ -844,8 +863,10 @@ template <int DP, bool F16>
 cudaError_t launch_tiles(const Maps& maps, const Args& a, int64_t grid, cudaStream_t stream) {
     const cudaError_t e = a.nt == 1 ? launch_form<DP, F16, 1>(maps, a, grid, stream) : launch_form<DP, F16, 2>(maps, a, grid, stream);
     if (e != cudaSuccess || a.splits == 1) return e;
-    const int64_t combine = grid / a.splits * a.nt * (a.D / 8);
-    return launch_after(combine_kernel<F16>, dim3(static_cast<unsigned>(combine)), kCombineThreads, 0, stream, a);
+    // one CTA per 8 columns, fewer where the tiles alone are many
+    const int64_t tiles = grid / a.splits * a.nt;
+    const int parts = tiles * (a.D / 8) <= 4096 ? a.D / 8 : 4;
+    return launch_after(combine_kernel<F16>, dim3(static_cast<unsigned>(tiles * parts)), kCombineThreads, 0, stream, a, parts);
 }
 
 }  // namespace
