@@ -333,13 +333,20 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
     const int heads = min(a.gs, (hk + 1) * a.G - head0);   // of the tile's gs, those that exist
     // key tiles: tile i works on [j0, e[i])
     int e[kNT], last[kNT];   // last: tokens of tile i
-    int most = 0;
+    // Key tile of which tile i sees at most half: products, softmax and guard take
+    // that half only.  (us, with / without: 32 queries of up to 48 tokens 7.6 / 8.0, 200
+    // prompts of 64 135 / 144.  With two tiles per CTA the branches cost the long
+    // prompts 7 %, so only with one.)
+    int shorter[kNT];
+    int most = 0, keys_most = 0;
 #pragma unroll
     for (int i = 0; i < kNT; ++i) {
         last[i] = min(a.tok, it.nq - it.t0 - i * a.tok);
         const int keys = last[i] > 0 ? visible(a, it, it.t0 + i * a.tok + last[i] - 1) : 0;
         e[i] = (keys + kTileN - 1) / kTileN;
+        shorter[i] = NT == 1 && e[i] * kTileN - keys >= kTileN / 2 ? e[i] - 1 : -1;
         most = max(most, e[i]);
+        keys_most = max(keys_most, keys);
     }
     int j0 = 0, j1 = most;
     if (a.splits > 1) {
@@ -397,10 +404,11 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
                             value[(h * kHalf + row * 128) / 2 + q] = 0;
             if (lane == 0) *bad_flag = 1;
         }
-        if (hi < kTileN) {
+        const int used = NT == 1 && keys_most - j * kTileN <= kTileN / 2 ? kTileN / 2 : kTileN;   // rows that the product takes
+        if (hi < used) {
             wrote = true;
             for (int h = 0; h < kHalves; ++h)
-                for (int row = hi & ~3; row < kTileN; row += 4)
+                for (int row = hi & ~3; row < used; row += 4)
                     if (row + (lane >> 3) >= hi) *reinterpret_cast<uint4*>(tile + h * kHalf + row * 128) = make_uint4(0, 0, 0, 0);
         }
         if (wrote) fence_proxy_async_smem();
@@ -461,19 +469,20 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
         } else if (warp == F::kMmaWarp) {
             // -------------------------------------------------------------- MMA
             const uint32_t type = F16 ? idesc_fp16_f32(128, 0) : idesc_bf16_f32(128, 0);
-            const uint32_t idesc_s = type | ((kTileN >> 3) << 17);
+            const uint32_t idesc_s = type | ((kTileN >> 3) << 17), idesc_half = type | ((kTileN >> 4) << 17);
             const uint32_t idesc_o = type | (static_cast<uint32_t>(a.D >> 3) << 17) | kBMnMajor;
             const int steps = a.D / 16;
             // lane 0, which is elected, tests no barrier: its tests would wait behind its
             // own commits, that is, until its last products have completed
             auto scores = [&](int i, int n) {   // S_i = Q_i K^T, K in load n
+                const uint32_t idesc = NT == 1 && j0 + n / 2 == shorter[i] ? idesc_half : idesc_s;
                 const uint64_t ad = smem_desc_kmajor_sw128(sq + i * kTileBytes);
                 const uint64_t bd = smem_desc_kmajor_sw128(skv + (n % kSlots) * kTileBytes);
 #pragma unroll
                 for (int s = 0; s < DP / 16; ++s)
                     if (s < steps) {
                         const uint32_t off = (s >> 2) * (kHalf / 16) + 2 * (s & 3);
-                        umma_smem_a(tmem + kSCol + i * kTileN, ad + off, bd + off, idesc_s, s > 0);
+                        umma_smem_a(tmem + kSCol + i * kTileN, ad + off, bd + off, idesc, s > 0);
                     }
                 umma_commit(cb + kBarS + 8 * i);
             };
@@ -507,9 +516,11 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
                     tc_fence_after_sync();
                     if (elect_one()) {
 #pragma unroll
-                        for (int s = 0; s < kTileN / 16; ++s)   // 16 keys: 16 rows of 128 bytes
+                        for (int s = 0; s < kTileN / 16; ++s) {   // 16 keys: 16 rows of 128 bytes
+                            if (NT == 1 && s == kTileN / 32 && j == shorter[i]) break;
                             umma_bf16_tmem_a(tmem + kOCol + i * DP, tmem + kSCol + i * kTileN + 8 * s, bd + s * (2048 / 16),
                                              idesc_o, (j > j0 || s > 0) ? 1u : 0u);
+                        }
                         umma_commit(cb + kBarO + 8 * i);
                         if (j + 1 < e[i]) scores(i, n + 1);
                         if (i == kNT - 1 || j >= e[kNT - 1]) {   // the last tile that reads these
@@ -535,7 +546,7 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
         const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + quarter + (static_cast<uint32_t>(16 * half) << 16) + kSCol + i * kTileN;
         const uint32_t to = tmem + quarter + kOCol + i * DP, to16 = to + (static_cast<uint32_t>(16 * half) << 16);
-        const int end = i == 0 ? e[0] : e[kNT - 1];
+        const int end = i == 0 ? e[0] : e[kNT - 1], half_tile = i == 0 ? shorter[0] : shorter[kNT - 1];
         const float scale2 = a.scale2;
         // the thread's rows r0 and r0 + 8: the keys they see, their references and sums
         const int r0 = (warp & 3) * 32 + half * 16 + (lane >> 2);
@@ -597,6 +608,7 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
             uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                if (NT == 1 && h == 1 && j == half_tile) break;   // (its scores are from before, masked)
                 uint32_t p[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c) {   // pair c of this half: row c & 1
@@ -808,7 +820,7 @@ Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, in
     // the other's products, and where short blocks fit the GPU at once and their
     // latency counts.  Two tiles against the same keys otherwise, which read K and V
     // half as often.  27B-class heads, us, one tile / two: 32 queries of up to 48
-    // tokens 8.1 / 13.1; 200 prompts of 64 142 / 177; one prompt of 512 10.5 / 12.3;
+    // tokens 7.6 / 13.1; 200 prompts of 64 135 / 177; one prompt of 512 10.5 / 12.3;
     // 24 documents of up to 1023 57 / 54; 16 prompts of 2048 282 / 246; 4096 tokens
     // 145 / 134; 256 new against 16384 93 / 74.
     const int64_t single = B * ceil_div(avg_q, p.tok) * p.HC;

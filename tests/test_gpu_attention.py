@@ -153,6 +153,21 @@ def test_prompt_non_finite_values_reach_only_rows_that_see_them(n, at, bad):
     assert torch.equal(O3[:at], O2[:at])
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("keys", [63, 64, 65, 127, 128, 129, 191, 192, 193])
+def test_prompt_ends_around_half_a_tile(keys, causal):
+    """Few queries against a last tile that is full, half full and one beside it;
+    the rows behind the sequence's keys are not finite."""
+    H, G, D = 4, 2, 128
+    nq, nk = [min(keys, 33), keys, 1], [keys, keys, keys]
+    Q = heads(70 + keys, sum(nq), H, D, "bf16")
+    K, V = heads(80 + keys, sum(nk) + 200, G, D, "bf16"), heads(90 + keys, sum(nk) + 200, G, D, "bf16")
+    K[sum(nk):] = float("nan")
+    V[sum(nk):] = float("inf")
+    O, L = run_prompt(Q, K, V, nq, nk, H, G, D, "bf16", causal, D ** -0.5)
+    check_prompt(Q, K, V, O, L, nq, nk, H, G, D, "bf16", causal, D ** -0.5)
+
+
 def test_prompt_offsets_are_clamped():
     """Offsets outside the buffers are read as the nearest end, decreasing ones as an empty sequence."""
     Hq, Hkv, D, t, n = 2, 1, 64, "bf16", 150
