@@ -15,6 +15,9 @@
 //
 // What bounds it: the bytes of the cache, read once (the G query heads of a
 // key/value head are rows of the same products).
+// Measured, 40 / 8 heads of 128: 128 sequences of 8192 over int8 codes 338 us
+// (6.6 TB/s), two of 32768 in fp16 51.5 us (5.2 TB/s), 32 of up to 8192 over e4m3
+// codes 40.5 us, one of 701 8.6 us, of which some 8 us are launch, start and join.
 //
 // Work.  An item is one (sequence, key/value head); its tiles of 16 keys are
 // dealt to the CTAs in one of two ways (see Share), a segment being the part of
