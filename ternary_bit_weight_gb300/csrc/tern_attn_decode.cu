@@ -16,11 +16,11 @@
 // What bounds it: the bytes of the cache, read once (the G query heads of a
 // key/value head are rows of the same products).
 // Measured, 40 / 8 heads of 128: 128 sequences of 8192 over int8 codes 338 us
-// (6.6 TB/s), two of 32768 in fp16 51.5 us (5.2 TB/s), 32 of up to 8192 over e4m3
-// codes 40.5 us, one of 701 8.6 us, of which some 8 us are launch, start and join.
+// (6.6 TB/s), two of 32768 in fp16 48.4 us (5.5 TB/s), 32 of up to 8192 over e4m3
+// codes 37.6 us, one of 701 8.1 us, of which some 8 us are launch, start and join.
 //
 // Work.  An item is one (sequence, key/value head); its tiles of 16 keys are
-// dealt to the CTAs in one of two ways (see Share), a segment being the part of
+// dealt to the CTAs in one of three ways (see Share), a segment being the part of
 // an item that a CTA has.  Within a segment the warps take the tiles in turn;
 // at its end their (m, l, o) meet in shared memory.  An item inside one CTA is
 // then finished; otherwise the CTAs leave partial results in the workspace and
@@ -61,7 +61,9 @@ constexpr int kTile = 16;              // keys per unit
 constexpr int kRows = 16;              // query heads per pass over the keys
 constexpr int kMinTiles = 8;           // of a CTA, one per warp
 constexpr int kEnd = 8;                // what ending a segment costs, in tiles
+constexpr int kJoin = 24;              // what a second segment and the joining of parts cost, in tiles
 constexpr float kPart = 2.4f;          // what adding a part costs, against an eighth of a tile
+constexpr int kFirst = 4;              // parts that a join loads before it knows their statistics
 constexpr float kLazy = 8.0f;          // how far a score may pass the reference
 constexpr float kNone = -1.0e38f;      // reference before any key
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
@@ -81,6 +83,7 @@ struct Args {
     float* slots;          // [2 * grid] partial results
     int64_t ldq, ldo, max_pages, num_pages;
     int64_t capacity;      // max_pages * page_size
+    float slack;           // see share_of
     int B, D, G;           // G query heads share a key/value head
     int Hkv, passes, Hv;   // Hv = Hkv * passes: (key/value head, 16 of its query heads)
     int shift;
@@ -110,6 +113,8 @@ struct Shape {
     // two CTAs of 8 warps and 128 registers on an SM, so that one streams while
     // the other ends a segment.  The rest needs the registers, or the ring, of one.
     static constexpr int kCtas = KV != kKvX16 && COLS == 1 ? 2 : 1;
+    // SMs take tiles from L2 so much faster than all of them get them from memory
+    static constexpr float kSlack = KV == kKvX16 ? 1.6f : KV == kKvE4m3 ? 1.2f : 1.05f;
     static constexpr int kWarps = 8;
     static constexpr int kSmemMax = kCtas == 2 ? 115712 : 232448;
     static constexpr int kThreads = kWarps * 32;
@@ -265,6 +270,7 @@ struct Segment {
     int begin, end;
     int64_t start;       // dealing by weight: where the item starts
     int64_t left;        // and what is left of the CTA's part after it
+    int64_t item;        // dealing whole items: what each takes of `left` (else 0)
 };
 
 // How the tiles are dealt to the CTAs.
@@ -273,13 +279,21 @@ struct Segment {
 //     CTA, so unequal lengths load the SMs equally.  The first kEnd of an item
 //     stand for no tile: a cut that falls there splits no item.
 //   * whole == q: an item of n tiles goes to ceil(n / q) CTAs of its own, one
-//     segment each.  Fewer segments and partial results than by weight, less
-//     equal loads: taken when its largest load, with the segments' ends, is the
-//     smaller one (few sequences).
+//     segment each.
+//   * several == k: a CTA has k items, whole.
+// The last two have fewer segments and partial results than by weight, and less
+// equal loads.  Where the loads are within `slack` of equal, and kJoin, they are
+// faster, because the memory is what is busy, not every SM: bf16 cache of 18 sequences of 4064 (144
+// items for 152 CTAs) 50.0 us against 55 by weight, 32 of 2272 (two items each) 51
+// against 55; e4m3 codes of 30 of 3000 (240 for 304) 36.9 against 40.9, int8 of 32
+// of 512 11.5 against 16.4.  (int8 codes of 128 of 8192 in fours, 1.19 times the
+// equal load, 367 against 338: there the SMs are as busy as the memory.)
 struct Share {
-    int whole;
+    int whole, several;
     int64_t weight;      // by weight: of all items
     int64_t ctas;        // that have a part
+    int64_t items;
+    uint32_t ctas0;      // dealing a CTA or more to an item: CTAs of an item of the lane's first sequence
 };
 
 __device__ __forceinline__ int length_of(const Args& a, int b) {
@@ -305,35 +319,60 @@ __device__ __forceinline__ T warp_sum(T n) {
 template <typename T>
 __device__ __forceinline__ Share share_of(const Args& a, int lane, int mine) {
     T tiles = 0;
-    uint32_t some = 0;
+    uint32_t some = 0, most = 0;
     for (int b = lane; b < a.B; b += 32) {
-        const int n = tiles_of(b == lane ? mine : length_of(a, b));
+        const uint32_t n = tiles_of(b == lane ? mine : length_of(a, b));
         tiles += n;
         some += n > 0;
+        most = max(most, n);
     }
     tiles = warp_sum<T>(tiles) * a.Hv;
     const T items = static_cast<T>(__reduce_add_sync(0xffffffffu, some)) * a.Hv;
     const T grid = gridDim.x;
     Share s;
-    s.whole = 0;
+    s.whole = s.several = 0;
+    s.ctas0 = 0;
     const T weight = tiles + kEnd * items;
     s.weight = weight;
     T ctas = tiles == 0 ? T(0) : max(T(1), min(grid, max(items, weight / (kMinTiles + kEnd))));
-    if (tiles > 0 && items < grid) {
+    // the weight that a CTA may have when items are not cut by weight
+    const float bound = a.slack * __fdividef(static_cast<float>(weight), static_cast<float>(ctas)) + kJoin;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (items >= grid) {
+        const T k = (items + grid - 1) / grid;
+        if (static_cast<float>(k) * static_cast<float>(most + kEnd) <= bound && k <= T(INT32_MAX)) {
+            s.several = static_cast<int>(k);
+            ctas = (items + k - 1) / k;
+        }
+    } else if (tiles > 0) {
         // an item's parts add up one after the other: n tiles are split no finer
         // than where a tile less per warp costs as much as the parts it adds
         const T even = static_cast<T>(sqrtf(kPart * __fdividef(static_cast<float>(tiles), static_cast<float>(items))));
         const T q = max(max(T(kMinTiles), even), (tiles + grid - items - 1) / (grid - items));
-        // q + kEnd <= weight / ctas + 2 kEnd
-        if ((q > kEnd ? (q - kEnd) * ctas : T(0)) <= weight && q <= T(INT32_MAX)) {
-            s.whole = static_cast<int>(q);
+        if (most <= q) {   // a CTA per item
+            if (static_cast<float>(most + kEnd) <= bound) {
+                s.whole = static_cast<int>(most);
+                s.ctas0 = mine > 0;
+                ctas = items;
+            }
+        } else {   // so q is below 2^31
             T parts = 0;
-            for (int b = lane; b < a.B; b += 32)
-                parts += (static_cast<uint32_t>(tiles_of(b == lane ? mine : length_of(a, b))) + s.whole - 1) / static_cast<uint32_t>(s.whole);
-            ctas = warp_sum<T>(parts) * a.Hv;
+            float load = 0.0f;   // the largest of a CTA
+            for (int b = lane; b < a.B; b += 32) {
+                const uint32_t n = tiles_of(b == lane ? mine : length_of(a, b));
+                const uint32_t some = (n + static_cast<uint32_t>(q) - 1) / static_cast<uint32_t>(q);
+                parts += some;
+                if (b == lane) s.ctas0 = some;
+                if (some > 0) load = fmaxf(load, __fdividef(static_cast<float>(n), static_cast<float>(some)));
+            }
+            if (warp_max(load) + kEnd <= bound) {
+                s.whole = static_cast<int>(q);
+                ctas = warp_sum<T>(parts) * a.Hv;
+            }
         }
     }
     s.ctas = ctas;
+    s.items = items;
     return s;
 }
 
@@ -349,7 +388,7 @@ __device__ __forceinline__ void next_segment(const Args& a, Segment& s) {
     }
     s.begin = 0;
     s.end = static_cast<int>(min(static_cast<int64_t>(s.tiles), s.left - kEnd));
-    s.left -= s.end + kEnd;
+    s.left -= s.item ? s.item : s.end + kEnd;
 }
 
 // The CTA's first segment (one warp); begin == end: it has none.
@@ -357,14 +396,17 @@ template <typename T>
 __device__ __forceinline__ Segment first_segment(const Args& a, const Share& share, int lane, int mine) {
     Segment s;
     const T cta = blockIdx.x, weight = static_cast<T>(share.weight), ctas = static_cast<T>(share.ctas);
-    const T u0 = share.whole ? cta : weight * cta / ctas;
-    const T u1 = share.whole ? cta + 1 : weight * (cta + 1) / ctas;
+    const T k = share.several;
+    const T u0 = share.whole ? cta : k ? cta * k : weight * cta / ctas;
+    const T u1 = share.whole || k ? u0 + 1 : weight * (cta + 1) / ctas;
+    s.item = 0;
     T base = 0;
     for (int b0 = 0;; b0 += 32) {
         const int len = b0 == 0 ? mine : b0 + lane < a.B ? length_of(a, b0 + lane) : 0;
         const uint32_t tiles = tiles_of(len);
-        // CTAs, or weight, of an item: below 2^28
-        const uint32_t each = tiles == 0 ? 0 : share.whole ? (tiles + share.whole - 1) / static_cast<uint32_t>(share.whole) : tiles + kEnd;
+        // CTAs, number (1) or weight of an item: below 2^28
+        const uint32_t each = tiles == 0 ? 0 : k ? 1
+                              : share.whole ? b0 == 0 ? share.ctas0 : (tiles + share.whole - 1) / static_cast<uint32_t>(share.whole) : tiles + kEnd;
         T incl = static_cast<T>(each) * a.Hv;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -379,7 +421,7 @@ __device__ __forceinline__ Segment first_segment(const Args& a, const Share& sha
             s.tiles = tiles_of(s.len);
             const T n = __shfl_sync(0xffffffffu, each, src);
             const T in = u0 - base - (__shfl_sync(0xffffffffu, incl, src) - n * a.Hv);
-            s.hv = static_cast<int>(in / n);
+            s.hv = static_cast<int>(n == 1 ? in : in / n);
             const int at = static_cast<int>(in - s.hv * n);
             if (share.whole) {
                 const int per = static_cast<int>((s.tiles + static_cast<uint32_t>(n) - 1) / static_cast<uint32_t>(n));
@@ -387,6 +429,12 @@ __device__ __forceinline__ Segment first_segment(const Args& a, const Share& sha
                 s.begin = at * per;
                 s.end = min(s.tiles, s.begin + per);
                 s.left = 0;
+            } else if (k) {
+                s.item = int64_t(1) << 32;   // more than an item weighs
+                s.start = 0;
+                s.begin = 0;
+                s.end = s.tiles;
+                s.left = (min(k, static_cast<T>(share.items) - u0) - 1) * s.item;
             } else {
                 const int upto = static_cast<int>(min(n, at + (u1 - u0)));
                 s.start = u0 - at;
@@ -600,9 +648,10 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
     };
     load_queries(seg);
     // partial results left so far (in part_info: b, hv, first and last CTA of the
-    // item) and how many CTAs had arrived before: looked at when the CTA's tiles
-    // are done
-    int parts = 0, arrived0 = 0, arrived1 = 0;
+    // item).  The CTA arrives for them when its tiles are done: in mid-stream the
+    // arrival waits for stores that queue with the loads of the SM, and its warp
+    // fell 6 us behind.
+    int parts = 0;
 
     // a warp stores the finished sums of one head
     auto finish = [&](const Segment& s, int head, const float (&sum)[S::kEach], float M, float MO, float L) {
@@ -957,9 +1006,6 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 else parts_of_wide(share, done, c0, c1);
                 volatile int* info = part_info + 4 * (parts & 1);
                 info[0] = done.b, info[1] = done.hv, info[2] = c0, info[3] = c1;
-                const int before = arrive(a.arrived + c0);
-                if (parts == 0) arrived0 = before;
-                else arrived1 = before;
             }
             ++parts;
         }
@@ -967,9 +1013,9 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
     }
 
     // the last CTA to arrive adds the parts of an item, in CTA order
-    if (threadIdx.x == 0 && parts > 0) {
-        last_flag[0] = arrived0 == part_info[3] - part_info[2];
-        last_flag[1] = arrived1 == part_info[7] - part_info[6];
+    if (lane == 0 && warp < parts) {   // warp 0, which has just written it, takes the last part
+        const int n = parts - 1 - warp;
+        last_flag[n] = arrive(a.arrived + part_info[4 * n + 2]) == part_info[4 * n + 3] - part_info[4 * n + 2];
     }
     __syncthreads();
     for (int n = 0; n < parts; ++n) {
@@ -992,6 +1038,11 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
             for (int i = 0; i < S::kEach; ++i) sum[i] = 0.0f;
             for (int i0 = c0; i0 <= c1; i0 += 32) {   // a lane has one part's statistics
                 const int count = min(32, c1 - i0 + 1);
+                // the first parts are on their way with the statistics
+                Floats<S::kEach> x0[kFirst];
+#pragma unroll
+                for (int k = 0; k < kFirst; ++k)
+                    x0[k] = load_l2<S::kEach>(part(i0 + min(k, count - 1)) + head * DP + lane * S::kEach);
                 const float* sp = part(i0 + min(lane, count - 1)) + kSlotRows * DP + head * 3;
                 const bool had = lane < count;
                 const float mi = had ? __ldcg(sp) : kNone, moi = had ? __ldcg(sp + 1) : kNone, li = had ? __ldcg(sp + 2) : 0.0f;
@@ -1002,8 +1053,15 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 MO = upo;
 #pragma unroll
                 for (int i = 0; i < S::kEach; ++i) sum[i] *= keep;
+#pragma unroll
+                for (int k = 0; k < kFirst; ++k) {
+                    const float fk = k < count ? __shfl_sync(0xffffffffu, f, k) : 0.0f;
+#pragma unroll
+                    for (int i = 0; i < S::kEach; ++i)
+                        if (k < count) sum[i] += x0[k].v[i] * fk;
+                }
 #pragma unroll 4
-                for (int k = 0; k < count; ++k) {
+                for (int k = kFirst; k < count; ++k) {
                     const Floats<S::kEach> x = load_l2<S::kEach>(part(i0 + k) + head * DP + lane * S::kEach);
                     const float fk = __shfl_sync(0xffffffffu, f, k);
 #pragma unroll
@@ -1037,6 +1095,7 @@ template <int DP, int KV, bool F16, int COLS>
 cudaError_t launch(Args& a, const DecodeArgs& d, int sm_count, cudaStream_t stream) {
     using S = Shape<DP, KV, COLS>;
     const int grid = grid_size(d.B, a.Hv, a.capacity, static_cast<int64_t>(sm_count) * S::kCtas);
+    a.slack = S::kSlack;
     a.narrow = static_cast<double>(d.B) * a.Hv * static_cast<double>(a.capacity / kTile + 1 + kEnd) * (grid + 1) < 2147483648.0;
     Maps maps;
     memset(&maps, 0, sizeof(maps));

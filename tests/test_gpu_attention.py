@@ -318,6 +318,32 @@ def test_decode_scales(scale, kind):
     check_decode(Q, O, L, lens, Hq, Hkv, D, kind, t, scale, plain)
 
 
+# Batches whose work is dealt to the SMs in each way: several whole items per CTA,
+# some CTAs short of one, with empty sequences between them; an item or part of one
+# per CTA; unequal lengths cut by weight, with more items than CTAs and with fewer.
+BATCHES = [
+    [33] * 50,
+    [40, 0, 33, 37, 0, 0, 48] * 11 + [0, 35],
+    [200] * 18,
+    [180, 200, 190, 0] * 10,
+    [1700] + [20, 50, 5] * 20,
+    [2500, 3, 40, 700, 0, 90],
+]
+
+
+@pytest.mark.parametrize("kind", ["x16", "e4m3", "i8"])
+@pytest.mark.parametrize("batch", range(len(BATCHES)))
+def test_decode_batches(batch, kind):
+    lens, Hq, Hkv, D = BATCHES[batch], 16, 8, 128
+    Q = heads(131, len(lens), Hq, D, "bf16", 8)
+    pages, cache, table, plain = make_cache(lens, Hkv, 16, D, kind, "bf16", 132)
+    scale = 1.0 / math.sqrt(D)
+    ws = workspace(tb.tern_attn_decode_workspace_bytes(len(lens), Hq, Hkv, D, table.shape[1] * 16))
+    for _ in range(2):   # the second call finds the workspace as the first left it
+        O, L = run_decode(Q, lens, Hq, Hkv, D, 16, kind, "bf16", scale, pages, cache, table, ws=ws)
+    check_decode(Q, O, L, lens, Hq, Hkv, D, kind, "bf16", scale, plain)
+
+
 @pytest.mark.parametrize("kind", ["e4m3", "i8"])
 @pytest.mark.parametrize("size", [2.0 ** -60, 2.0 ** 40])
 def test_decode_factors_of_any_size(size, kind):
