@@ -450,7 +450,7 @@ tern_status tern_rope_freqs(int64_t rot_dim, double base, int scaling, double fa
  *   d_Q, d_Qo  device [T, ldq] in, [T, ldqo] out, Hq heads; d_Qo may be d_Q
  *              with ldqo == ldq
  *   d_K, d_Ko  likewise with Hk heads; Hk == 0: none (the pointers are unused)
- *   rot_dim    a multiple of 16, 0 <= rot_dim <= D
+ *   rot_dim    a multiple of 16, 0 <= rot_dim <= D, or D / 2
  * T == 0 is a no-op. */
 tern_status tern_rope(int x_type, int layout, int64_t T, int64_t D, int64_t rot_dim, const int32_t* d_pos,
                       const float* d_inv_freq, float amplitude, int64_t Hq, const void* d_Q, int64_t ldq,

@@ -40,7 +40,7 @@ tern_status check_rows(const void* p, int64_t ld, int64_t H, int64_t D) {
 
 tern_status check_rotation(int layout, int64_t rot_dim, int64_t D) {
     if (layout != TERN_ROPE_HALF && layout != TERN_ROPE_INTERLEAVED) return TERN_ERR_SHAPE;
-    if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0) return TERN_ERR_SHAPE;
+    if (rot_dim < 0 || rot_dim > D || (rot_dim % 16 != 0 && 2 * rot_dim != D)) return TERN_ERR_SHAPE;
     return TERN_OK;
 }
 

@@ -136,9 +136,39 @@ __device__ __forceinline__ uint2 encode8(const float* x, float inv) {
 
 __host__ __device__ constexpr bool coded(int kv) { return kv == kKvE4m3 || kv == kKvI8; }
 
+// A lane's run of 8 elements: 16 bytes at `at`, or (SPLIT) 8 there and 8 at `at2`;
+// likewise 8 codes.
+template <bool SPLIT>
+__device__ __forceinline__ uint4 load_run(const uint16_t* p, int at, int at2) {
+    if constexpr (!SPLIT) return *reinterpret_cast<const uint4*>(p + at);
+    const uint2 a = *reinterpret_cast<const uint2*>(p + at), b = *reinterpret_cast<const uint2*>(p + at2);
+    return make_uint4(a.x, a.y, b.x, b.y);
+}
+template <bool SPLIT>
+__device__ __forceinline__ void store_run(uint16_t* p, int at, int at2, const uint4& u) {
+    if constexpr (!SPLIT) {
+        *reinterpret_cast<uint4*>(p + at) = u;
+    } else {
+        *reinterpret_cast<uint2*>(p + at) = make_uint2(u.x, u.y);
+        *reinterpret_cast<uint2*>(p + at2) = make_uint2(u.z, u.w);
+    }
+}
+template <bool SPLIT>
+__device__ __forceinline__ void store_codes(uint8_t* p, int at, int at2, const uint2& u) {
+    if constexpr (!SPLIT) {
+        *reinterpret_cast<uint2*>(p + at) = u;
+    } else {
+        *reinterpret_cast<uint32_t*>(p + at) = u.x;
+        *reinterpret_cast<uint32_t*>(p + at2) = u.y;
+    }
+}
+
 // One warp per token and part of its heads: rotate queries and keys, and
-// (KV != kKvNone) store keys and values in the cache.
-template <int LANES, bool F16, int KV>
+// (KV != kKvNone) store keys and values in the cache.  SPLIT: rot is an odd
+// multiple of 8, so that one lane has four pairs that turn and four that do not,
+// and runs are of 4 elements (8191 tokens, 48 heads of 80, half of each turned 28.5
+// us, all of each 27.2).
+template <int LANES, bool F16, int KV, bool SPLIT>
 __global__ void __launch_bounds__(kTokenThreads, coded(KV) ? 28 : 0) token_kernel(const TokenArgs a) {
     constexpr int kSub = 32 / LANES;      // heads at a time
     constexpr int kOwn = 8 / kSub;        // pairs whose angle a lane computes
@@ -153,11 +183,18 @@ __global__ void __launch_bounds__(kTokenThreads, coded(KV) ? 28 : 0) token_kerne
     const int tasks = min(a.Hq + a.Hk + a.Hv, first + a.per);
     const bool live = lane * 16 < a.D;
     const bool turned = live && lane * 16 < a.rot;
-    // the lane's two runs of 8 elements
-    int ea = lane * 16, eb = ea + 8;
+    const bool turned2 = SPLIT ? lane * 16 + 8 < a.rot : turned;   // pairs 4-7 of the lane
+    // the lane's two runs of 8 elements (SPLIT: of 4 and 4)
+    int ea = lane * 16, eb = ea + 8, ea2 = ea + 4, eb2 = eb + 4;
     if (!a.interleaved && turned) {
         ea = lane * 8;
         eb = a.rot / 2 + lane * 8;
+        ea2 = ea + 4;
+        eb2 = eb + 4;
+        if (SPLIT && !turned2) {
+            ea2 = lane * 16 + 8;
+            eb2 = ea2 + 4;
+        }
     }
     const uint16_t* qrow = a.q + t * a.ldq;
     const uint16_t* krow = a.k + t * a.ldk - (int64_t)a.Hq * a.D;
@@ -166,8 +203,8 @@ __global__ void __launch_bounds__(kTokenThreads, coded(KV) ? 28 : 0) token_kerne
         ua = ub = make_uint4(0, 0, 0, 0);
         if (h < tasks && live) {
             const uint16_t* src = (h < a.Hq ? qrow : h < a.Hq + a.Hk ? krow : vrow) + (int64_t)h * a.D;
-            ua = *reinterpret_cast<const uint4*>(src + ea);
-            ub = *reinterpret_cast<const uint4*>(src + eb);
+            ua = load_run<SPLIT>(src, ea, ea2);
+            ub = load_run<SPLIT>(src, eb, eb2);
         }
     };
     int h = first + sub;
@@ -188,8 +225,10 @@ __global__ void __launch_bounds__(kTokenThreads, coded(KV) ? 28 : 0) token_kerne
         const int32_t p = a.pos[t];
         float2 own[kOwn];
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i)
-            own[i] = turned ? cos_sin(p, a.inv_freq[lane * 8 + sub * kOwn + i], a.amplitude) : make_float2(0.0f, 0.0f);
+        for (int i = 0; i < kOwn; ++i) {
+            const int pair = lane * 8 + sub * kOwn + i;
+            own[i] = (SPLIT ? 2 * pair < a.rot : turned) ? cos_sin(p, a.inv_freq[pair], a.amplitude) : make_float2(0.0f, 0.0f);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             cs[i].x = __shfl_sync(0xffffffffu, own[i % kOwn].x, (i / kOwn) * LANES + lane);
@@ -213,12 +252,13 @@ __global__ void __launch_bounds__(kTokenThreads, coded(KV) ? 28 : 0) token_kerne
                 // pair i of the lane: (x[i], x[8 + i]) or (x[2i], x[2i + 1])
                 const float p0 = a.interleaved ? x[2 * i] : x[i], p1 = a.interleaved ? x[2 * i + 1] : x[8 + i];
                 const float r0 = p0 * cs[i].x - p1 * cs[i].y, r1 = p1 * cs[i].x + p0 * cs[i].y;
+                const bool turn = !SPLIT || i < 4 || turned2;
                 if (a.interleaved) {
-                    y[2 * i] = r0;
-                    y[2 * i + 1] = r1;
+                    y[2 * i] = turn ? r0 : p0;
+                    y[2 * i + 1] = turn ? r1 : p1;
                 } else {
-                    y[i] = r0;
-                    y[8 + i] = r1;
+                    y[i] = turn ? r0 : p0;
+                    y[8 + i] = turn ? r1 : p1;
                 }
             }
             ua = pack8<F16>(y);
@@ -227,8 +267,8 @@ __global__ void __launch_bounds__(kTokenThreads, coded(KV) ? 28 : 0) token_kerne
         if (KV == kKvNone || h < a.Hq) {
             if (mine) {
                 uint16_t* dst = h < a.Hq ? a.qo + t * a.ldqo + h * a.D : a.ko + t * a.ldko + (h - a.Hq) * a.D;
-                *reinterpret_cast<uint4*>(dst + ea) = ua;
-                *reinterpret_cast<uint4*>(dst + eb) = ub;
+                store_run<SPLIT>(dst, ea, ea2, ua);
+                store_run<SPLIT>(dst, eb, eb2, ub);
             }
         }
         if (KV != kKvNone && h0 + kSub > a.Hq) {   // some of the warp's tasks go to the cache
@@ -239,8 +279,8 @@ __global__ void __launch_bounds__(kTokenThreads, coded(KV) ? 28 : 0) token_kerne
             if (KV == kKvX16) {
                 if (store) {
                     uint16_t* dst = reinterpret_cast<uint16_t*>(cache) + cell * a.D;
-                    *reinterpret_cast<uint4*>(dst + ea) = ua;
-                    *reinterpret_cast<uint4*>(dst + eb) = ub;
+                    store_run<SPLIT>(dst, ea, ea2, ua);
+                    store_run<SPLIT>(dst, eb, eb2, ub);
                 }
             } else {
                 // codes from the values rounded to 16 bits, as a separate write sees them
@@ -258,8 +298,8 @@ __global__ void __launch_bounds__(kTokenThreads, coded(KV) ? 28 : 0) token_kerne
                         for (int i = 0; i < 16; ++i) x[i] = 0.0f;
                     }
                     uint8_t* dst = cache + cell * a.D;
-                    *reinterpret_cast<uint2*>(dst + ea) = encode8<KV>(x, inv);
-                    *reinterpret_cast<uint2*>(dst + eb) = encode8<KV>(x + 8, inv);
+                    store_codes<SPLIT>(dst, ea, ea2, encode8<KV>(x, inv));
+                    store_codes<SPLIT>(dst, eb, eb2, encode8<KV>(x + 8, inv));
                     if (lane == 0) (is_v ? a.vscale : a.kscale)[cell] = bad ? __int_as_float(0x7fc00000) : __fdiv_rn(m, top);
                 }
             }
@@ -356,8 +396,8 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a)
     }
 }
 
-template <int LANES, bool F16>
-cudaError_t launch_token(int kv, TokenArgs a, int64_t T, cudaStream_t stream) {
+template <int LANES, bool F16, bool SPLIT>
+cudaError_t launch_runs(int kv, TokenArgs a, int64_t T, cudaStream_t stream) {
     constexpr int kSub = 32 / LANES;
     const int64_t tasks = a.Hq + a.Hk + a.Hv, steps = ceil_div(tasks, kSub);
     // a warp walks all heads of a token, unless the tokens are too few to fill the SMs
@@ -369,11 +409,16 @@ cudaError_t launch_token(int kv, TokenArgs a, int64_t T, cudaStream_t stream) {
     a.parts = static_cast<int>(ceil_div(tasks, a.per));
     const dim3 grid(static_cast<unsigned>(ceil_div(T * a.parts, kTokenThreads / 32)));
     if constexpr (LANES == 8) {
-        if (kv == kKvX16) return launch_after(token_kernel<8, F16, kKvX16>, grid, kTokenThreads, 0, stream, a);
-        if (kv == kKvE4m3) return launch_after(token_kernel<8, F16, kKvE4m3>, grid, kTokenThreads, 0, stream, a);
-        if (kv == kKvI8) return launch_after(token_kernel<8, F16, kKvI8>, grid, kTokenThreads, 0, stream, a);
+        if (kv == kKvX16) return launch_after(token_kernel<8, F16, kKvX16, SPLIT>, grid, kTokenThreads, 0, stream, a);
+        if (kv == kKvE4m3) return launch_after(token_kernel<8, F16, kKvE4m3, SPLIT>, grid, kTokenThreads, 0, stream, a);
+        if (kv == kKvI8) return launch_after(token_kernel<8, F16, kKvI8, SPLIT>, grid, kTokenThreads, 0, stream, a);
     }
-    return launch_after(token_kernel<LANES, F16, kKvNone>, grid, kTokenThreads, 0, stream, a);
+    return launch_after(token_kernel<LANES, F16, kKvNone, SPLIT>, grid, kTokenThreads, 0, stream, a);
+}
+
+template <int LANES, bool F16>
+cudaError_t launch_token(int kv, const TokenArgs& a, int64_t T, cudaStream_t stream) {
+    return a.rot % 16 == 0 ? launch_runs<LANES, F16, false>(kv, a, T, stream) : launch_runs<LANES, F16, true>(kv, a, T, stream);
 }
 
 TokenArgs token_args(const RopeArgs& r) {

@@ -232,6 +232,21 @@ def test_rope_kv_write_is_the_two_calls(T, Hq, Hkv, D, rot, t, layout, kind):
     assert not math.isnan(float(Qa.float().sum()))
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("T,Hq,Hk,D,t", [(5, 16, 8, 80, "bf16"), (33, 3, 2, 48, "f16"), (3, 2, 1, 16, "bf16"),
+                                         (4, 5, 3, 112, "bf16"), (3, 7, 2, 144, "f16"), (2, 3, 1, 240, "bf16")])
+def test_rope_of_half_a_head(T, Hq, Hk, D, t, layout):
+    """rot_dim an odd multiple of 8."""
+    test_rope(T, Hq, Hk, D, D // 2, t, layout)
+
+
+@pytest.mark.parametrize("kind", ["x16", "e4m3", "i8"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("T,Hq,Hkv,D,t", [(6, 8, 8, 80, "bf16"), (30, 6, 3, 48, "f16"), (3, 2, 1, 112, "bf16")])
+def test_rope_kv_write_of_half_a_head(T, Hq, Hkv, D, t, layout, kind):
+    test_rope_kv_write_is_the_two_calls(T, Hq, Hkv, D, D // 2, t, layout, kind)
+
+
 def test_other_stream():
     """The calls run on the stream they are given."""
     T, H, D = 64, 8, 128
