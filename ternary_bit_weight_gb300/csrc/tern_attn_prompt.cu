@@ -20,7 +20,7 @@
 // cores multiply for the other.  For short sequences a CTA has one tile (10 warps,
 // the load warp is the guard, too) and two CTAs share an SM (see plan_prompt).
 // Measured, 40 / 8 heads of 128, causal, bf16: 8192 tokens 450-490 us (1.40-1.53
-// PFLOP/s, with the power limit), 4096 134 us, 512 11 us, 64 5.6 us.
+// PFLOP/s, with the power limit), 4096 134 us, 512 11 us, 32 prompts of 128 39 us.
 //
 // Roles (two tiles, 20 warps):
 //   * warp 0 issues all tcgen05.mma: scores S_i = Q_i K_j^T (both operands in
@@ -93,7 +93,8 @@ constexpr int kBarDrain = kBarO + 8 * kMaxNT;
 constexpr int kTmemPtr = kBarDrain + 8;
 constexpr int kAbort = kTmemPtr + 4;
 constexpr int kBad = kAbort + 4;                     // a value was taken out by the guard
-static_assert(kBad + 4 <= kShare, "control block");
+constexpr int kItem = kBad + 4;                      // an Item
+static_assert(kItem + 20 <= kShare, "control block");
 
 template <int DP, int NT>
 constexpr int smem_bytes() {
@@ -137,18 +138,24 @@ __device__ __forceinline__ void clamp_range(const int32_t* cu, int b, int total,
 
 // Block `index` of the sequences' token blocks in order; the blocks of a
 // sequence run from its end, whose causal rows see most keys.  One warp; false
-// past the last block.
+// past the last block.  A lane counts the blocks of RUN sequences, whose offsets
+// it loads together.
+template <int RUN>
 __device__ __forceinline__ bool find_item(const Args& a, int index, int lane, Item& it) {
     int base = 0;
     const int step = a.nt * a.tok;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        int q0 = 0, nq = 0, k0 = 0, nk = 0;
-        if (b0 + lane < a.B) {
-            clamp_range(a.cu_q, b0 + lane, a.Tq, q0, nq);
-            clamp_range(a.cu_kv, b0 + lane, a.Tkv, k0, nk);
+    for (int b0 = 0; b0 < a.B; b0 += 32 * RUN) {
+        const int first = b0 + lane * RUN;
+        int q0[RUN], nq[RUN], k0 = 0, nk = 0, mine = 0;
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+            q0[i] = nq[i] = 0;
+            if (first + i < a.B) clamp_range(a.cu_q, first + i, a.Tq, q0[i], nq[i]);
         }
-        const int blocks = (nq + step - 1) / step;
-        int incl = blocks;
+        if (RUN == 1 && first < a.B) clamp_range(a.cu_kv, first, a.Tkv, k0, nk);
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) mine += static_cast<uint32_t>(nq[i] + step - 1) / static_cast<uint32_t>(step);
+        int incl = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int up = __shfl_up_sync(0xffffffffu, incl, d);
@@ -157,10 +164,20 @@ __device__ __forceinline__ bool find_item(const Args& a, int index, int lane, It
         const uint32_t past = __ballot_sync(0xffffffffu, base + incl > index);
         if (past != 0) {
             const int src = __ffs(past) - 1;
-            it.q0 = __shfl_sync(0xffffffffu, q0, src);
-            it.nq = __shfl_sync(0xffffffffu, nq, src);
-            const int end = base + __shfl_sync(0xffffffffu, incl, src);
-            it.t0 = (end - 1 - index) * step;
+            // the lane that has it finds the sequence of its run
+            int end = base + incl - mine, b = first, q = q0[0], n = nq[0];
+#pragma unroll
+            for (int i = 0; i < RUN; ++i)
+                if (end <= index) {
+                    b = first + i;
+                    q = q0[i];
+                    n = nq[i];
+                    end += static_cast<uint32_t>(n + step - 1) / static_cast<uint32_t>(step);
+                }
+            it.q0 = __shfl_sync(0xffffffffu, q, src);
+            it.nq = __shfl_sync(0xffffffffu, n, src);
+            it.t0 = (__shfl_sync(0xffffffffu, end, src) - 1 - index) * step;
+            if (RUN > 1) clamp_range(a.cu_kv, __shfl_sync(0xffffffffu, b, src), a.Tkv, k0, nk);
             it.k0 = __shfl_sync(0xffffffffu, k0, src);
             it.nk = __shfl_sync(0xffffffffu, nk, src);
             return true;
@@ -325,20 +342,45 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
         }
         __syncwarp();
     }
+    const uint32_t rest = blockIdx.x / static_cast<uint32_t>(a.HC);
+    const int hc = blockIdx.x - rest * a.HC;
+    const int block = a.splits == 1 ? rest : rest / static_cast<uint32_t>(a.splits);
+    const int split = rest - block * a.splits;
     grid_launch_dependents();
     grid_dependency_wait();
-    Item it;
-    const int hc = blockIdx.x % a.HC, rest = blockIdx.x / a.HC;
-    const int split = rest % a.splits, block = rest / a.splits;
-    if (!find_item(a, block, lane, it)) return;   // the whole CTA
+    Item it = {};
+    if constexpr (NT == 1) {
+        // One warp finds the item, the others get it with the barrier: short blocks
+        // are many, and ten warps' loads of the same offsets held one another up (32
+        // queries of up to 48 tokens 6.9 us instead of 7.6, 200 prompts of 64 117 instead
+        // of 135).  With two tiles the loads are earlier when nobody waits for a barrier.
+        int* found = reinterpret_cast<int*>(ctrl + kItem);
+        if (warp == F::kLoadWarp) {
+            if (!(a.B <= 64 ? find_item<1>(a, block, lane, it) : find_item<4>(a, block, lane, it))) it.nq = 0;
+            if (lane == 0) found[0] = it.q0, found[1] = it.nq, found[2] = it.k0, found[3] = it.nk, found[4] = it.t0;
+        } else if (warp == F::kMmaWarp) {
+            tmem_alloc(smem_u32(tmem_ptr), F::kTmemCols);
+            tmem_relinquish();
+        }
+        tc_fence_before_sync();
+        __syncthreads();
+        tc_fence_after_sync();
+        it.q0 = found[0], it.nq = found[1], it.k0 = found[2], it.nk = found[3], it.t0 = found[4];
+        if (it.nq == 0) {   // past the last block
+            if (warp == F::kMmaWarp) tmem_dealloc(*tmem_ptr, F::kTmemCols);
+            return;
+        }
+    } else {
+        if (!find_item<1>(a, block, lane, it)) return;   // the whole CTA
+    }
 
     const int hk = hc / a.chunks, head0 = hk * a.G + (hc - hk * a.chunks) * a.gs;
     const int heads = min(a.gs, (hk + 1) * a.G - head0);   // of the tile's gs, those that exist
     // key tiles: tile i works on [j0, e[i])
     int e[kNT], last[kNT];   // last: tokens of tile i
     // Key tile of which tile i sees at most half: products, softmax and guard take
-    // that half only.  (us, with / without: 32 queries of up to 48 tokens 7.6 / 8.0, 200
-    // prompts of 64 135 / 144.  With two tiles per CTA the branches cost the long
+    // that half only.  (32 queries of up to 48 tokens 0.4 us less of 8.0, 200 prompts
+    // of 64 9 of 144.  With two tiles per CTA the branches cost the long
     // prompts 7 %, so only with one.)
     int shorter[kNT];
     int most = 0, keys_most = 0;
@@ -352,9 +394,9 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
         keys_most = max(keys_most, keys);
     }
     int j0 = 0, j1 = most;
-    if (a.splits > 1) {
-        j0 = static_cast<int>(static_cast<int64_t>(most) * split / a.splits);
-        j1 = static_cast<int>(static_cast<int64_t>(most) * (split + 1) / a.splits);
+    if (a.splits > 1) {   // most < 2^24, splits <= 32
+        j0 = static_cast<uint32_t>(most) * split / static_cast<uint32_t>(a.splits);
+        j1 = static_cast<uint32_t>(most) * (split + 1) / static_cast<uint32_t>(a.splits);
     }
 #pragma unroll
     for (int i = 0; i < kNT; ++i) e[i] = max(j0, min(e[i], j1));
@@ -420,7 +462,7 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
         return true;
     };
 
-    // the first loads, then what the others need
+    // the first loads
     if (warp == F::kLoadWarp && j1 > j0) {
         if (elect_one()) {
 #pragma unroll
@@ -435,13 +477,15 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
         __syncwarp();
         for (int n = 0; n < min(kSlots, 2 * (j1 - j0)); ++n) load_tile(n);
     }
-    if (warp == F::kMmaWarp) {
-        tmem_alloc(smem_u32(tmem_ptr), F::kTmemCols);
-        tmem_relinquish();
+    if constexpr (NT == 2) {
+        if (warp == F::kMmaWarp) {
+            tmem_alloc(smem_u32(tmem_ptr), F::kTmemCols);
+            tmem_relinquish();
+        }
+        tc_fence_before_sync();
+        __syncthreads();
+        tc_fence_after_sync();
     }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_ptr, 0);   // uniform, and known to be
 
     if (warp < F::kSoftWarp0) {
@@ -747,7 +791,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const Args a, 
     const int i = static_cast<int>(tile % a.nt);
     const int hc = static_cast<int>(item % a.HC), block = static_cast<int>(item / a.HC);
     Item it;
-    if (!find_item(a, block, threadIdx.x & 31, it)) return;
+    if (!find_item<1>(a, block, threadIdx.x & 31, it)) return;
     const int hk = hc / a.chunks, head0 = hk * a.G + (hc - hk * a.chunks) * a.gs;
     const int token = r / a.gs, head = r - token * a.gs, t = it.t0 + i * a.tok + token;
     if (token >= a.tok || t >= it.nq || head >= min(a.gs, (hk + 1) * a.G - head0)) return;
@@ -803,7 +847,7 @@ struct Plan {
     size_t off_part, off_ml, ws_bytes;
 };
 
-Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, int64_t D, int sm_count) {
+Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, int64_t D, bool causal, int sm_count) {
     Plan p = {};
     const int64_t G = Hq / Hkv, avg_q = ceil_div(Tq, B), avg_k = Tkv / B;
     // fewest tiles for sequences of the average length; of equals, the most heads
@@ -819,15 +863,16 @@ Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, in
     p.chunks = static_cast<int>(ceil_div(G, p.gs));
     p.HC = static_cast<int>(Hkv) * p.chunks;
     // One tile per CTA and two CTAs per SM where the second tile of a block would be
-    // empty, where blocks are very short, so that one CTA's start and end run beside
+    // empty, where a tile sees few keys, so that one CTA's start and end run beside
     // the other's products, and where short blocks fit the GPU at once and their
     // latency counts.  Two tiles against the same keys otherwise, which read K and V
-    // half as often.  27B-class heads, us, one tile / two: 32 queries of up to 48
-    // tokens 7.6 / 13.1; 200 prompts of 64 135 / 177; one prompt of 512 10.5 / 12.3;
-    // 24 documents of up to 1023 57 / 54; 16 prompts of 2048 282 / 246; 4096 tokens
-    // 145 / 134; 256 new against 16384 93 / 74.
+    // half as often.  27B-class heads, us, one tile / two: 32 prompts of 128 39 / 61,
+    // 64 of 256 155 / 190, 16 of 512 89 / 98, 16 of 768 154 / 158, 16 of 1024 236 / 235;
+    // 24 documents of up to 1023, not causal, 57 / 54; 8 of 256 new tokens after 1000
+    // 64 / 62; one prompt of 512 10.9 / 12.2, of 1500 32 / 27.
     const int64_t single = B * ceil_div(avg_q, p.tok) * p.HC;
-    p.nt = avg_q <= p.tok || avg_k < 2 * kTileN || (avg_k < 6 * kTileN && single <= 2 * sm_count) ? 1 : 2;
+    const int64_t seen = causal ? avg_k - avg_q / 2 : avg_k;   // keys of a row, on average
+    p.nt = avg_q <= p.tok || 2 * seen < 5 * kTileN || (avg_k < 6 * kTileN && single <= 2 * sm_count) ? 1 : 2;
     p.blocks = Tq / (p.nt * p.tok) + B;
     if (p.blocks > Tq) p.blocks = Tq;
     // Split the keys where that costs less by this estimate (us): waves of blocks,
@@ -887,11 +932,13 @@ cudaError_t launch_tiles(const Maps& maps, const Args& a, int64_t grid, cudaStre
 }  // namespace
 
 size_t prompt_ws_bytes(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, int64_t D, int sm_count) {
-    return plan_prompt(B, Tq, Tkv, Hq, Hkv, D, sm_count < 1 ? 1 : sm_count).ws_bytes;
+    const int sms = sm_count < 1 ? 1 : sm_count;
+    const size_t all = plan_prompt(B, Tq, Tkv, Hq, Hkv, D, false, sms).ws_bytes, causal = plan_prompt(B, Tq, Tkv, Hq, Hkv, D, true, sms).ws_bytes;
+    return all > causal ? all : causal;
 }
 
 cudaError_t launch_prompt(bool x_f16, const PromptArgs& pa, void* ws, int sm_count, cudaStream_t stream) {
-    const Plan p = plan_prompt(pa.B, pa.Tq, pa.Tkv, pa.Hq, pa.Hkv, pa.D, sm_count);
+    const Plan p = plan_prompt(pa.B, pa.Tq, pa.Tkv, pa.Hq, pa.Hkv, pa.D, pa.causal, sm_count);
     const int64_t grid = p.blocks * p.HC * p.splits;
     if (grid > INT32_MAX / 8) return cudaErrorInvalidValue;
     if (encode_tiled_fn() == nullptr) return cudaErrorNotSupported;
