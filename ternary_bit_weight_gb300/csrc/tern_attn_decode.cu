@@ -16,8 +16,8 @@
 // What bounds it: the bytes of the cache, read once (the G query heads of a
 // key/value head are rows of the same products).
 // Measured, 40 / 8 heads of 128: 128 sequences of 8192 over int8 codes 338 us
-// (6.6 TB/s), two of 32768 in fp16 48.4 us (5.5 TB/s), 32 of up to 8192 over e4m3
-// codes 37.6 us, one of 701 8.1 us, of which some 8 us are launch, start and join.
+// (6.6 TB/s), two of 32768 in fp16 49.1 us (5.5 TB/s), 32 of up to 8192 over e4m3
+// codes 39.0 us, one of 701 8.6 us, of which some 8 us are launch, start and join.
 //
 // Work.  An item is one (sequence, key/value head); its tiles of 16 keys are
 // dealt to the CTAs in one of three ways (see Share), a segment being the part of
