@@ -10,11 +10,12 @@
 // factor m / top, both divisions and the product IEEE fp32, so that any other
 // implementation of the rule gets the same codes.
 //
-// Layout of the work: a head is one task of LANES lanes (8 for D <= 128, 16
-// above), a lane owning two runs of 8 elements (16 bytes each).  In the half
-// layout the two runs are the partners of one another (elements 8j.. and
-// rot/2 + 8j..), in the interleaved layout they are neighbours; either way
-// lane j needs the angles of pairs 8j .. 8j+7 and a rotation stays inside a
+// Layout of the work: a head is one task of LANES lanes (4 for D <= 64, 8
+// for D <= 128, 16 above; with 8 lanes for 48 heads of 64, half of them idle, 8191
+// tokens took 23 us instead of 14), a lane owning two runs of 8 elements (16
+// bytes each).  In the half layout the two runs are the partners of one another
+// (elements 8j.. and rot/2 + 8j..), in the interleaved layout they are
+// neighbours; either way lane j needs the angles of pairs 8j .. 8j+7 and a rotation stays inside a
 // lane.  m is a butterfly over the task's lanes.  A warp serves one token, or
 // a part of its heads when tokens are few: its lanes compute the token's angles
 // once, keep them in registers for all heads, and walk the heads with two
@@ -352,21 +353,21 @@ __device__ __forceinline__ void decode16(const uint4& u, float factor, uint4& lo
     hi = pack8<F16>(x + 8);
 }
 
-// Eight lanes per (token, head).  A lane has two runs of 8 elements, one in each
+// Eight lanes (four for D <= 64) per (token, head).  A lane has two runs of 8 elements, one in each
 // half of the head, so that the lanes' stores of 16 bytes follow one another.  What
 // bounds it: latency while the codes are in L2, DRAM beyond.  (8191 tokens of int8
 // codes just written, 50 MB read and written, us: 7.0; 10.0 with two neighbouring
 // runs, whose stores have half of every 32-byte sector each.  The passes above keep
 // neighbours: bound by DRAM they gain nothing, and the start costs 1 us more.)
-template <bool F16, int KV>
+template <int LANES, bool F16, int KV>
 __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const ReadArgs a) {
     grid_launch_dependents();
     grid_dependency_wait();
-    const int lane = threadIdx.x & 7;
+    const int lane = threadIdx.x % LANES;
     const int ea = lane * 8, eb = a.D / 2 + ea;
     if (eb >= a.D) return;
-    const int64_t tasks = a.T * a.Hkv, step = (int64_t)gridDim.x * (kReadThreads / 8);
-    for (int64_t i = (int64_t)blockIdx.x * (kReadThreads / 8) + (threadIdx.x >> 3); i < tasks; i += step) {
+    const int64_t tasks = a.T * a.Hkv, step = (int64_t)gridDim.x * (kReadThreads / LANES);
+    for (int64_t i = (int64_t)blockIdx.x * (kReadThreads / LANES) + threadIdx.x / LANES; i < tasks; i += step) {
         const int64_t t = ((i | a.Hkv) >> 32) == 0 ? static_cast<uint32_t>(i) / static_cast<uint32_t>(a.Hkv) : i / a.Hkv;
         const int g = static_cast<int>(i - t * a.Hkv);
         const int64_t slot = a.slots[t];
@@ -408,10 +409,10 @@ cudaError_t launch_runs(int kv, TokenArgs a, int64_t T, cudaStream_t stream) {
     a.per = static_cast<int>(ceil_div(steps, parts)) * kSub;
     a.parts = static_cast<int>(ceil_div(tasks, a.per));
     const dim3 grid(static_cast<unsigned>(ceil_div(T * a.parts, kTokenThreads / 32)));
-    if constexpr (LANES == 8) {
-        if (kv == kKvX16) return launch_after(token_kernel<8, F16, kKvX16, SPLIT>, grid, kTokenThreads, 0, stream, a);
-        if (kv == kKvE4m3) return launch_after(token_kernel<8, F16, kKvE4m3, SPLIT>, grid, kTokenThreads, 0, stream, a);
-        if (kv == kKvI8) return launch_after(token_kernel<8, F16, kKvI8, SPLIT>, grid, kTokenThreads, 0, stream, a);
+    if constexpr (LANES <= 8) {
+        if (kv == kKvX16) return launch_after(token_kernel<LANES, F16, kKvX16, SPLIT>, grid, kTokenThreads, 0, stream, a);
+        if (kv == kKvE4m3) return launch_after(token_kernel<LANES, F16, kKvE4m3, SPLIT>, grid, kTokenThreads, 0, stream, a);
+        if (kv == kKvI8) return launch_after(token_kernel<LANES, F16, kKvI8, SPLIT>, grid, kTokenThreads, 0, stream, a);
     }
     return launch_after(token_kernel<LANES, F16, kKvNone, SPLIT>, grid, kTokenThreads, 0, stream, a);
 }
@@ -446,6 +447,8 @@ TokenArgs token_args(const RopeArgs& r) {
 
 cudaError_t launch_rope(bool x_f16, int64_t T, const RopeArgs& r, cudaStream_t stream) {
     const TokenArgs a = token_args(r);
+    if (r.D <= 64)
+        return x_f16 ? launch_token<4, true>(kKvNone, a, T, stream) : launch_token<4, false>(kKvNone, a, T, stream);
     if (r.D <= 128)
         return x_f16 ? launch_token<8, true>(kKvNone, a, T, stream) : launch_token<8, false>(kKvNone, a, T, stream);
     return x_f16 ? launch_token<16, true>(kKvNone, a, T, stream) : launch_token<16, false>(kKvNone, a, T, stream);
@@ -465,16 +468,22 @@ cudaError_t launch_kv_write(bool x_f16, int64_t T, const RopeArgs& r, const uint
     a.kscale = const_cast<float*>(c.kscale);
     a.vscale = const_cast<float*>(c.vscale);
     a.err = err;
+    if (r.D <= 64) return x_f16 ? launch_token<4, true>(c.kv, a, T, stream) : launch_token<4, false>(c.kv, a, T, stream);
     return x_f16 ? launch_token<8, true>(c.kv, a, T, stream) : launch_token<8, false>(c.kv, a, T, stream);
+}
+
+template <int LANES, bool F16>
+static cudaError_t launch_read_by(const ReadArgs& a, int kv, cudaStream_t stream) {
+    const int64_t blocks = ceil_div(a.T * a.Hkv, kReadThreads / LANES);
+    const dim3 grid(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30)));
+    if (kv == kKvX16) return launch_after(kv_read_kernel<LANES, F16, kKvX16>, grid, kReadThreads, 0, stream, a);
+    if (kv == kKvE4m3) return launch_after(kv_read_kernel<LANES, F16, kKvE4m3>, grid, kReadThreads, 0, stream, a);
+    return launch_after(kv_read_kernel<LANES, F16, kKvI8>, grid, kReadThreads, 0, stream, a);
 }
 
 template <bool F16>
 static cudaError_t launch_read(const ReadArgs& a, int kv, cudaStream_t stream) {
-    const int64_t blocks = ceil_div(a.T * a.Hkv, kReadThreads / 8);
-    const dim3 grid(static_cast<unsigned>(blocks < (1 << 30) ? blocks : (1 << 30)));
-    if (kv == kKvX16) return launch_after(kv_read_kernel<F16, kKvX16>, grid, kReadThreads, 0, stream, a);
-    if (kv == kKvE4m3) return launch_after(kv_read_kernel<F16, kKvE4m3>, grid, kReadThreads, 0, stream, a);
-    return launch_after(kv_read_kernel<F16, kKvI8>, grid, kReadThreads, 0, stream, a);
+    return a.D <= 64 ? launch_read_by<4, F16>(a, kv, stream) : launch_read_by<8, F16>(a, kv, stream);
 }
 
 cudaError_t launch_kv_read(bool x_f16, int64_t T, int Hkv, int D, const int64_t* slots, const KvCache& c, uint16_t* k,
