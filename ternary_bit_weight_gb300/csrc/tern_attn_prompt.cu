@@ -602,7 +602,11 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int token = (r0 + 8 * q) / a.gs, head = r0 + 8 * q - token * a.gs;
-            lim[q] = token < last[i] && head < heads ? visible(a, it, it.t0 + i * a.tok + token) : 0;
+            const bool live = token < last[i] && head < heads;
+            lim[q] = live ? visible(a, it, it.t0 + i * a.tok + token) : 0;
+            // a row that does not exist (its queries are whatever shared memory held)
+            // never asks for a new reference, so the others' do not depend on it
+            if (!live) m[q] = CUDART_INF_F;
         }
         bool ok = true;
         for (int j = j0; j < end; ++j) {
