@@ -170,7 +170,9 @@ tern_status tern_unrepack(const void* d_tiled, int64_t N, int64_t K, uint8_t* d_
  *   d_ws     device workspace of ws_bytes >= tern_workspace_bytes(M, N, K),
  *            256-byte aligned.  It must be zero-filled before its first
  *            use; every completed call leaves its counters at zero again,
- *            so one workspace can serve a sequence of calls on one stream.
+ *            so one workspace can serve any sequence of calls on one stream:
+ *            of the linear layers and of attention, of any shapes that it is
+ *            large enough for.
  *            Calls that may overlap in time need separate workspaces.  Its
  *            first 32-bit word is an error word: the kernel sets it non-zero
  *            (and returns early, leaving Y incomplete) only if a pipeline
@@ -207,10 +209,10 @@ tern_status tern_linear_multi(const uint16_t* d_X, int64_t ldx, const void* d_ti
  * allocator.  The source pages have no counterpart: this is a library
  * convenience.  Arguments and results are those of tern_linear; instead of a
  * caller workspace the call uses a scratch array built into the library
- * (16 MiB per device, held by every GPU that loads the library until the
- * process exits).  It allocates nothing.
- *   - Problems whose tern_workspace_bytes(M, N, K) exceeds 16 MiB return
- *     TERN_ERR_SIZE before anything is enqueued.
+ * (16 MiB + 4 KiB per device, held by every GPU that loads the library until
+ * the process exits).  It allocates nothing.
+ *   - Problems whose tern_workspace_bytes(M, N, K) exceeds 16 MiB + 4 KiB
+ *     return TERN_ERR_SIZE before anything is enqueued.
  *   - The first call on a device (with that device current) looks up the
  *     array's device address and may load the library's GPU code; make that
  *     first call before any stream capture.
@@ -511,7 +513,8 @@ tern_status tern_kv_read(int x_type, int kv_type, int64_t T, int64_t Hkv, int64_
  * are rounded to x_type for their product with V and O is rounded once.
  *   d_O    device [Tq, ldo] of x_type; rows of no sequence are not written
  *   d_lse  optional device fp32 [Tq, Hq]
- *   d_ws   as tern_linear's, of tern_attn_prompt_workspace_bytes
+ *   d_ws   as tern_linear's (and may be the same one), of
+ *          tern_attn_prompt_workspace_bytes
  * Offsets outside [0, Tq] / [0, Tkv] are read as the nearest end, a sequence
  * whose offsets decrease as empty. */
 size_t tern_attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, int64_t D);

@@ -1141,15 +1141,14 @@ cudaError_t launch_kind(int kv, Args& a, const DecodeArgs& d, int sm_count, cuda
 
 constexpr int64_t kMostCtas = 2;   // per SM, any form: the workspace does not depend on the form
 
-int64_t arrived_bytes(int grid) { return round_up(static_cast<int64_t>(grid) * 4, 256); }
+static_assert(kMostCtas <= kCountersPerSm, "an arrival counter per CTA");
 
 }  // namespace
 
 size_t decode_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, int sm_count) {
     const int64_t G = Hq / Hkv;
     const int grid = grid_size(B, Hkv * ceil_div(G, kRows), max_len, kMostCtas * (sm_count < 1 ? 1 : sm_count));
-    return kWorkspaceErrBytes + static_cast<size_t>(arrived_bytes(grid)) +
-           static_cast<size_t>(2 * grid) * slot_floats(D > 64 ? 128 : 64, group_rows(G)) * sizeof(float);
+    return workspace_data(sm_count) + static_cast<size_t>(2 * grid) * slot_floats(D > 64 ? 128 : 64, group_rows(G)) * sizeof(float);
 }
 
 cudaError_t launch_decode(bool x_f16, const DecodeArgs& d, void* ws, int sm_count, cudaStream_t stream) {
@@ -1176,11 +1175,10 @@ cudaError_t launch_decode(bool x_f16, const DecodeArgs& d, void* ws, int sm_coun
     a.passes = static_cast<int>(ceil_div(a.G, kRows));
     a.Hv = a.Hkv * a.passes;
     a.scale2 = d.scale * kLog2e;
-    const int grid = grid_size(d.B, a.Hv, a.capacity, kMostCtas * sm_count);
-    uint8_t* w = static_cast<uint8_t*>(ws) + kWorkspaceErrBytes;
-    a.err = static_cast<int*>(ws);
-    a.arrived = reinterpret_cast<int32_t*>(w);
-    a.slots = reinterpret_cast<float*>(w + arrived_bytes(grid));
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    a.err = reinterpret_cast<int*>(w);
+    a.arrived = reinterpret_cast<int32_t*>(w + kWorkspaceErrBytes);
+    a.slots = reinterpret_cast<float*>(w + workspace_data(sm_count));
     if (d.D > 64) return x_f16 ? launch_kind<128, true>(d.cache.kv, a, d, sm_count, stream) : launch_kind<128, false>(d.cache.kv, a, d, sm_count, stream);
     return x_f16 ? launch_kind<64, true>(d.cache.kv, a, d, sm_count, stream) : launch_kind<64, false>(d.cache.kv, a, d, sm_count, stream);
 }

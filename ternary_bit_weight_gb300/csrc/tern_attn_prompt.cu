@@ -905,6 +905,7 @@ Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, in
     size_t off = kWorkspaceErrBytes;
     p.off_part = p.off_ml = off;
     if (splits > 1) {
+        p.off_part = off = workspace_data(sm_count);
         const int64_t rows = p.blocks * p.HC * p.nt * kTileM * splits;
         off += static_cast<size_t>(rows * D) * sizeof(float);
         p.off_ml = off;

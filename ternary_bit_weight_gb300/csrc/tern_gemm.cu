@@ -1023,9 +1023,9 @@ GemmPlan plan_gemm(int64_t M, const int64_t* N, const int64_t* K, int P, int sm_
         p.items += tiles[q] * p.KS[q];
     }
     p.grid = p.items < sm_count ? p.items : sm_count;
-    // workspace: error word, then per problem: X16 [M][K] fp16 | 2^-c per
-    // token | split partials
-    size_t off = kWorkspaceErrBytes;
+    // workspace: error word and counters, then per problem: X16 [M][K] fp16 |
+    // 2^-c per token | split partials
+    size_t off = workspace_data(sm_count);
     for (int q = 0; q < P; ++q) {
         p.off_x16[q] = off;
         off += round_up(M * K[q] * 2, 1024);

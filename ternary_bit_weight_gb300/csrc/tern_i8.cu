@@ -290,13 +290,14 @@ I8Plan plan_i8(int64_t M, int64_t N, int64_t K, int sm_count) {
     if (ks > p.G) ks = p.G;
     if (ks < 1) ks = 1;
     p.KS = ks;
-    p.ws_bytes = kWorkspaceErrBytes + (p.KS > 1 ? static_cast<size_t>(p.KS * M * N) * sizeof(float) : 0);
+    p.off_partial = workspace_data(sm_count);
+    p.ws_bytes = p.KS > 1 ? p.off_partial + static_cast<size_t>(p.KS * M * N) * sizeof(float) : kWorkspaceErrBytes;
     return p;
 }
 
 cudaError_t launch_i8(const int8_t* xq, const float* a, const uint8_t* tiled, int64_t M, int64_t N,
                       const OutputSplit& out, void* ws, const I8Plan& plan, cudaStream_t stream) {
-    float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kWorkspaceErrBytes);
+    float* partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + plan.off_partial);
     const uint8_t* codes = tiled;
     const uint16_t* scales = reinterpret_cast<const uint16_t*>(tiled + plan.R * plan.G * kUnitCodeBytes);
     dim3 grid(static_cast<unsigned>(plan.R), static_cast<unsigned>(plan.KS));

@@ -70,12 +70,12 @@ struct StreamPlan {
     bool one;              // M == 1: activation rows resident in shared memory
     int64_t x_smem;        // shared memory for them (the largest set one CTA needs)
     int64_t U;             // units of all problems
-    int64_t tiles;         // 128-row tiles of all problems
-    int64_t V;             // workers
+    int64_t V;             // workers, at most one per SM
     int64_t grid;          // CTAs
     int stages;            // shared-memory ring depth
     size_t smem;           // dynamic shared memory per CTA
-    size_t ws_bytes;       // workspace: error word, tile counters, partial slots
+    size_t off_slots;      // workspace: error word, counters, partial slots
+    size_t ws_bytes;
 };
 
 
@@ -128,7 +128,7 @@ cudaError_t launch_gemm(const StreamProblem* probs, int P, bool x_f16, bool s8, 
 // order, one CTA per (row tile, K split).
 struct I8Plan {
     int64_t R, G, KS;
-    size_t ws_bytes;
+    size_t off_partial, ws_bytes;
 };
 size_t i8_xq_bytes(int64_t M, int64_t K);
 I8Plan plan_i8(int64_t M, int64_t N, int64_t K, int sm_count);
@@ -217,7 +217,16 @@ struct DecodeArgs {
 size_t decode_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, int sm_count);
 cudaError_t launch_decode(bool x_f16, const DecodeArgs& a, void* ws, int sm_count, cudaStream_t stream);
 
-// Size of the error word + padding at the start of every linear workspace.
+// Every workspace begins with the error word (padded), and behind it the
+// counters of arrivals, which are zero between calls: 4 per SM for the
+// streaming kernel (a worker's row quarters), 2 for single-token attention (a
+// CTA's items).  Data of any kind starts behind both, at a place that depends on
+// the device alone, so what one call leaves there is no other call's counter.
 constexpr size_t kWorkspaceErrBytes = 256;
+constexpr int64_t kCountersPerSm = 4;
+inline size_t workspace_data(int sm_count) {
+    const int64_t bytes = (sm_count > 0 ? sm_count : 152) * kCountersPerSm * int64_t(sizeof(int32_t));
+    return kWorkspaceErrBytes + static_cast<size_t>((bytes + 255) / 256 * 256);
+}
 
 }  // namespace tern

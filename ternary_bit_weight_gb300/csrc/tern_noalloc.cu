@@ -27,7 +27,7 @@
 
 namespace {
 
-constexpr size_t kScratchBytes = size_t(16) << 20;   // 16 MiB per device
+constexpr size_t kScratchBytes = (size_t(16) << 20) + 4096;   // per device: 16 MiB of data behind error word and counters
 constexpr int kMaxDevices = 64;
 
 __device__ __align__(256) uint8_t g_scratch[kScratchBytes];

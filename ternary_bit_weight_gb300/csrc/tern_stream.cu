@@ -143,7 +143,6 @@ struct StreamProb {
     const uint8_t* scales;     // per unit: 128 FP16 scales, or (s8) 128 int8 scales
     const uint16_t* x;         // M == 1: the activation row
     int64_t u_begin;           // its first unit in the launch's unit sequence
-    int64_t tile0;             // its first tile in the launch's tile counters
     int64_t N;
     int32_t R;                 // 128-row tiles
     int32_t G;                 // groups per row
@@ -162,7 +161,7 @@ struct StreamArgs {
     int64_t U;                 // units of all problems
     int64_t V;                 // workers = CTAs
     int* err;                  // workspace error word
-    int* counters;             // [tiles of all problems][4 row quarters]
+    int* counters;             // [V][4 row quarters]
     float* slots;              // [2V][NCOL][128]
     StreamProb prob[kMaxGroup];
 };
@@ -218,7 +217,8 @@ __device__ __forceinline__ void flush_tile(const StreamArgs& a, int64_t v, int p
     const int64_t t0 = pr.u_begin + b * pr.G;   // the tile's first unit in the sequence
     const int64_t w_first = owner_worker(t0, a.U, a.V);
     const int64_t w_last = owner_worker(t0 + pr.G - 1, a.U, a.V);
-    int* counter = a.counters + (pr.tile0 + b) * 4 + quad;
+    // a worker begins one shared tile at most (its last), so that worker names it
+    int* counter = a.counters + w_first * 4 + quad;
     int last = 0;
     if (lane == 0) {
         __threadfence();   // publish the warp's slot writes (ordered by the warp barrier)
@@ -792,12 +792,7 @@ StreamPlan plan_stream(int64_t M, const int64_t* N, const int64_t* K, int P, int
     StreamPlan p = {};
     if (sm_count <= 0) sm_count = 152;
     p.U = 0;
-    p.tiles = 0;
-    for (int i = 0; i < P; ++i) {
-        const int64_t R = ceil_div(N[i], kTileRows);
-        p.U += R * (K[i] / kGroup);
-        p.tiles += R;
-    }
+    for (int i = 0; i < P; ++i) p.U += ceil_div(N[i], kTileRows) * (K[i] / kGroup);
     p.V = p.U < sm_count ? p.U : sm_count;   // one worker per CTA, one CTA per SM
     p.grid = p.V;
     // M == 1 keeps the activation rows of each CTA's problems in shared
@@ -823,8 +818,8 @@ StreamPlan plan_stream(int64_t M, const int64_t* N, const int64_t* K, int P, int
     p.stages = static_cast<int>(stages);
     p.smem = static_cast<size_t>(1024 + p.x_smem + stages * stage_bytes + kCtrlBytes);
     const int64_t ncol = p.one ? SCfg<true>::NCOL : SCfg<false>::NCOL;
-    const size_t counters = static_cast<size_t>(round_up(p.tiles * 4 * 4, 256));
-    p.ws_bytes = kWorkspaceErrBytes + counters + static_cast<size_t>(2 * p.V * kTileRows * ncol) * sizeof(float);
+    p.off_slots = workspace_data(sm_count);
+    p.ws_bytes = p.off_slots + static_cast<size_t>(2 * p.V * kTileRows * ncol) * sizeof(float);
     return p;
 }
 
@@ -841,7 +836,7 @@ cudaError_t launch_stream(const StreamProblem* probs, int P, bool x_f16, bool s8
     a.x_smem = static_cast<uint32_t>(plan.x_smem);
     a.U = plan.U;
     a.V = plan.V;
-    int64_t u = 0, tile = 0;
+    int64_t u = 0;
     for (int p = 0; p < P; ++p) {
         StreamProb& pr = a.prob[p];
         const int64_t R = ceil_div(probs[p].N, kTileRows), G = probs[p].K / kGroup;
@@ -849,13 +844,11 @@ cudaError_t launch_stream(const StreamProblem* probs, int P, bool x_f16, bool s8
         pr.scales = probs[p].tiled + R * G * kUnitCodeBytes;
         pr.x = probs[p].x;
         pr.u_begin = u;
-        pr.tile0 = tile;
         pr.N = probs[p].N;
         pr.R = static_cast<int32_t>(R);
         pr.G = static_cast<int32_t>(G);
         pr.out = probs[p].out;
         u += R * G;
-        tile += R;
     }
     if (s8) {
         const int64_t U0 = a.prob[0].R * (int64_t)a.prob[0].G;
@@ -864,7 +857,7 @@ cudaError_t launch_stream(const StreamProblem* probs, int P, bool x_f16, bool s8
     uint8_t* w = static_cast<uint8_t*>(ws);
     a.err = reinterpret_cast<int*>(w);
     a.counters = reinterpret_cast<int*>(w + kWorkspaceErrBytes);
-    a.slots = reinterpret_cast<float*>(w + kWorkspaceErrBytes + static_cast<size_t>(round_up(plan.tiles * 4 * 4, 256)));
+    a.slots = reinterpret_cast<float*>(w + plan.off_slots);
     if (s8) {
         if (x_f16)
             return plan.one ? launch_one<true, true, 1>(probs, a, plan, stream)
