@@ -346,8 +346,15 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
     const int hc = blockIdx.x - rest * a.HC;
     const int block = a.splits == 1 ? rest : rest / static_cast<uint32_t>(a.splits);
     const int split = rest - block * a.splits;
-    grid_launch_dependents();
     grid_dependency_wait();
+    // The next kernel is let in once this CTA has its tensor memory: a kernel that took
+    // tensor memory first and then waited for this one would never get to run (the
+    // allocation waits without a limit).
+    auto allocate = [&]() {
+        tmem_alloc(smem_u32(tmem_ptr), F::kTmemCols);
+        tmem_relinquish();
+        grid_launch_dependents();
+    };
     Item it = {};
     if constexpr (NT == 1) {
         // One warp finds the item, the others get it with the barrier: short blocks
@@ -359,8 +366,7 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
             if (!(a.B <= 64 ? find_item<1>(a, block, lane, it) : find_item<4>(a, block, lane, it))) it.nq = 0;
             if (lane == 0) found[0] = it.q0, found[1] = it.nq, found[2] = it.k0, found[3] = it.nk, found[4] = it.t0;
         } else if (warp == F::kMmaWarp) {
-            tmem_alloc(smem_u32(tmem_ptr), F::kTmemCols);
-            tmem_relinquish();
+            allocate();
         }
         tc_fence_before_sync();
         __syncthreads();
@@ -478,10 +484,7 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
         for (int n = 0; n < min(kSlots, 2 * (j1 - j0)); ++n) load_tile(n);
     }
     if constexpr (NT == 2) {
-        if (warp == F::kMmaWarp) {
-            tmem_alloc(smem_u32(tmem_ptr), F::kTmemCols);
-            tmem_relinquish();
-        }
+        if (warp == F::kMmaWarp) allocate();
         tc_fence_before_sync();
         __syncthreads();
         tc_fence_after_sync();
