@@ -476,7 +476,10 @@ tern_status tern_rope(int x_type, int layout, int64_t T, int64_t D, int64_t rot_
 /* Write T tokens: token t's keys d_K [T, ldk] and values d_V [T, ldv] to slot
  * d_slots[t] (device int64 [T]).  A negative slot skips the token (padding);
  * one at or above num_pages * page_size is skipped and counted in d_err
- * (optional device int32).  Two tokens with one slot: either may stay. */
+ * (optional device int32).  The slots of one call that are in the cache are
+ * distinct: tokens are stored by warps that do not wait for one another, so
+ * two tokens with one slot leave a mixture there, codes of both and the factor
+ * of one, which is the value of neither. */
 tern_status tern_kv_write(int x_type, int kv_type, int64_t T, int64_t Hkv, int64_t D, const void* d_K, int64_t ldk,
                           const void* d_V, int64_t ldv, const int64_t* d_slots, int64_t num_pages, int64_t page_size,
                           void* d_kcache, void* d_vcache, float* d_kscale, float* d_vscale, int32_t* d_err,
