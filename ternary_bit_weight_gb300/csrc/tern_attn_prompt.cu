@@ -44,6 +44,7 @@
 // Every wait is bounded; a timeout raises the workspace error word.
 
 #include <cuda.h>
+#include <float.h>
 #include <math_constants.h>
 #include <string.h>
 
@@ -77,6 +78,7 @@ constexpr int kShare = 256;
 constexpr int kCtrlBytes = kShare + kShareBytes;
 constexpr float kLazy = 8.0f;
 constexpr float kNone = -1.0e38f;
+constexpr float kFar = 2097152.0f;   // 2^21: from here on a reference's unit is 1/4 and more
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 // control block
@@ -611,6 +613,19 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
             // never asks for a new reference, so the others' do not depend on it
             if (!live) m[q] = CUDART_INF_F;
         }
+        float2* share = reinterpret_cast<float2*>(ctrl + kShare) + i * kTileM;
+        // Scores far from zero are taken relative to a base of their row (in share[].x): a
+        // reference is a rounded product, and the fused difference of a score and it would
+        // give the row's largest score 2^(what the rounding dropped) as its weight, past 16
+        // bits' range from 2^28 on.  `far`: some row of the warp has one.
+        bool far = false;
+        auto rebase = [&](float (&s)[kTileN / 2], int q, float base) {
+            const float up = 1.0f / scale2;
+#pragma unroll
+            for (int c = 0; c < kTileN / 8; ++c)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) s[4 * c + 2 * q + k] = (__fmul_rn(s[4 * c + 2 * q + k], scale2) - base) * up;
+        };
         bool ok = true;
         for (int j = j0; j < end; ++j) {
             if (!(ok = warp_wait(cb + kBarS + 8 * i, (j - j0) & 1, abort_flag))) break;
@@ -627,6 +642,11 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
                         if (8 * c + 1 >= keys) s[4 * c + 2 * q + 1] = -CUDART_INF_F;
                     }
                 }
+            }
+            if (far) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    if (share[r0 + 8 * q].x != 0.0f) rebase(s, q, share[r0 + 8 * q].x);
             }
             float mx[2];
 #pragma unroll
@@ -645,6 +665,22 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
                     f[q] = exp2_approx(m[q] - up);
                     m[q] = up;
                     l[q] *= f[q];
+                }
+                // (not rows that have seen nothing or do not exist)
+                auto is_far = [](float m) { return fabsf(m) >= kFar && fabsf(m) <= FLT_MAX && m != kNone; };
+                if (__any_sync(0xffffffffu, is_far(m[0]) || is_far(m[1]))) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float before = far ? share[r0 + 8 * q].x : 0.0f, more = is_far(m[q]) ? m[q] : 0.0f;
+                        __syncwarp();   // the four lanes of a row have read it
+                        if ((lane & 3) == 0) share[r0 + 8 * q].x = before + more;
+                        if (more != 0.0f) {
+                            rebase(s, q, more);
+                            m[q] = 0.0f;
+                        }
+                    }
+                    __syncwarp();
+                    far = true;
                 }
                 if (j > j0) {
                     if (!(ok = warp_wait(cb + kBarO + 8 * i, (j - j0 - 1) & 1, abort_flag))) break;
@@ -688,9 +724,10 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
         }
         // --------------------------------------------------------- epilogue
         // one thread per row of the quarter, the two warps half of the columns each
-        float2* share = reinterpret_cast<float2*>(ctrl + kShare) + i * kTileM;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
+            if (far) m[q] += share[r0 + 8 * q].x;
+            __syncwarp();
             l[q] += __shfl_xor_sync(0xffffffffu, l[q], 1);
             l[q] += __shfl_xor_sync(0xffffffffu, l[q], 2);
             if ((lane & 3) == 0) share[r0 + 8 * q] = make_float2(m[q], l[q]);

@@ -1,0 +1,90 @@
+"""Attention of scores, queries, keys and values at the ends of their types' range.
+
+Where scores are large, an error of 2^-24 of a score is many units of the
+exponent and the softmax of unequal scores is not determined by the inputs'
+bits; these tests use equal scores (the weights are then equal, whatever
+their size) or scores that differ by more than any rounding (the largest takes
+all).  Equal weights: the output is the mean of n values, each weight is the
+same 16-bit number w and the sum takes n times w unrounded, so it is within
+u |o| + (u + n 2^-23) max |v| of the mean (u covers the rounding of w)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+from attn_util import TYPES, UNIT, assert_close, f64, heads  # noqa: E402
+from gpu_util import DEV  # noqa: E402
+from test_gpu_attention import run_prompt  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+# Rows and keys: one tile per CTA; two tiles; keys split over CTAs.
+SIZES = [([40], [40], 2, 1, 128), ([900, 70], [900, 900], 16, 8, 64), ([16], [2100], 4, 1, 128)]
+
+
+def mean_rows(V, n, m, causal):
+    """[n, D] means of the values that rows 0 .. n-1 see of m keys."""
+    total = np.concatenate([np.zeros((1, V.shape[1])), np.cumsum(V, 0)])
+    seen = np.clip(np.arange(n) + 1 + m - n, 0, m) if causal else np.full(n, m)
+    return total[seen] / np.maximum(seen, 1)[:, None], seen
+
+
+def check_means(O, L, V, nq, nk, Hq, Hkv, D, t, causal, score):
+    o, l, v = f64(O), f64(L), f64(V)
+    a = c = 0
+    for n, m in zip(nq, nk):
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            vv = v[c:c + m, g * D:(g + 1) * D]
+            want, seen = mean_rows(vv, n, m, causal)
+            bound = UNIT[t] * np.abs(want) + (UNIT[t] + m * 2.0 ** -23) * np.abs(vv).max()
+            assert_close(o[a:a + n, h * D:(h + 1) * D], want, bound, f"head {h}")
+            lse = score + np.log(seen)
+            assert_close(l[a:a + n, h], lse, 1e-6 * np.abs(lse) + 1e-5, f"lse of head {h}")
+        a, c = a + n, c + m
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk,Hq,Hkv,D", SIZES)
+@pytest.mark.parametrize("q,k,t", [
+    (1.5e19, 1.5e19, "bf16"),
+    (3001.0, 3001.0, "f16"),        # 9e6: the score's unit is 1
+    (60000.0, -60000.0, "f16"),     # 3.6e9: the unit is 256 and more
+    (7e5, 7e5, "bf16"),
+])
+def test_prompt_of_equal_scores(q, k, t, nq, nk, Hq, Hkv, D, causal):
+    prompt_of_equal_scores(q, k, t, nq, nk, Hq, Hkv, D, causal)
+
+
+def prompt_of_equal_scores(q, k, t, nq, nk, Hq, Hkv, D, causal):
+    Q, K = (torch.zeros((sum(n), H * D), dtype=TYPES[t], device=DEV) for n, H in ((nq, Hq), (nk, Hkv)))
+    Q[:, ::D] = q
+    K[:, ::D] = k
+    V = heads(1, sum(nk), Hkv, D, t)
+    O, L = run_prompt(Q, K, V, nq, nk, Hq, Hkv, D, t, causal, 1.0)
+    score = float(Q[0, 0].double() * K[0, 0].double())
+    check_means(O, L, V, nq, nk, Hq, Hkv, D, t, causal, score)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("nq,nk,Hq,Hkv,D", SIZES)
+def test_prompt_of_far_scores(nq, nk, Hq, Hkv, D, t):
+    """One key is ahead of all others by far: every row takes its value."""
+    Q = torch.full((sum(nq), Hq * D), 2000.0, dtype=TYPES[t], device=DEV)
+    K = torch.full((sum(nk), Hkv * D), 2000.0, dtype=TYPES[t], device=DEV)
+    V = heads(2, sum(nk), Hkv, D, t)
+    c = a = 0
+    for m in nk:
+        K[c + m // 3] = 3001.0
+        c += m
+    O, L = run_prompt(Q, K, V, nq, nk, Hq, Hkv, D, t, False, 1.0)
+    score = float((Q[0, :D].double() * K[nk[0] // 3, :D].double()).sum())
+    assert torch.all((L.double() - score).abs() <= 1e-5 * score)
+    c = 0
+    for n, m in zip(nq, nk):
+        want = V[c + m // 3].reshape(Hkv, 1, D).expand(Hkv, Hq // Hkv, D).reshape(Hq * D)
+        # the weight 2^0 .. 2^8 of the one key cancels up to two roundings
+        assert torch.allclose(O[a:a + n, :Hq * D].float(), want.float().expand(n, -1), rtol=2 * UNIT[t], atol=0)
+        a, c = a + n, c + m
