@@ -46,6 +46,7 @@
 // 16 rows exist here.)
 
 #include <cuda.h>
+#include <float.h>
 #include <math_constants.h>
 #include <string.h>
 
@@ -65,7 +66,7 @@ constexpr int kJoin = 24;              // what a second segment and the joining 
 constexpr float kPart = 2.4f;          // what adding a part costs, against an eighth of a tile
 constexpr int kFirst = 4;              // parts that a join loads before it knows their statistics
 constexpr float kLazy = 8.0f;          // how far a score may pass the reference
-constexpr float kNone = -1.0e38f;      // reference before any key
+constexpr float kNone = -FLT_MAX;      // reference before any key: no finite score is below it
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 struct Args {

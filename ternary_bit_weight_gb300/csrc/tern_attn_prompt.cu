@@ -77,7 +77,7 @@ constexpr int kShareBytes = kMaxNT * kTileM * 8;       // reference and sum of e
 constexpr int kShare = 256;
 constexpr int kCtrlBytes = kShare + kShareBytes;
 constexpr float kLazy = 8.0f;
-constexpr float kNone = -1.0e38f;
+constexpr float kNone = -FLT_MAX;     // reference before any key: no finite score is below it
 constexpr float kFar = 2097152.0f;   // 2^21: from here on a reference's unit is 1/4 and more
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 

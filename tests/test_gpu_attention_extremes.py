@@ -16,7 +16,7 @@ if not torch.cuda.is_available():
 
 from attn_util import TYPES, UNIT, assert_close, f64, heads  # noqa: E402
 from gpu_util import DEV  # noqa: E402
-from test_gpu_attention import run_prompt  # noqa: E402
+from test_gpu_attention import make_cache, run_decode, run_prompt  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,46 @@ def test_prompt_of_far_scores(nq, nk, Hq, Hkv, D, t):
         # the weight 2^0 .. 2^8 of the one key cancels up to two roundings
         assert torch.allclose(O[a:a + n, :Hq * D].float(), want.float().expand(n, -1), rtol=2 * UNIT[t], atol=0)
         a, c = a + n, c + m
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk,Hq,Hkv,D", SIZES)
+def test_prompt_of_lowest_scores(nq, nk, Hq, Hkv, D, causal):
+    """-2.3e38, in base 2 -3.3e38: the far end of what is finite."""
+    prompt_of_equal_scores(1.5e19, -1.5e19, "bf16", nq, nk, Hq, Hkv, D, causal)
+
+
+DECODES = [([40, 700], 4, 2, 128), ([9000], 2, 1, 64), ([130], 12, 1, 128)]
+
+
+def decode_of_equal_scores(q, k, t, lens, Hq, Hkv, D, kind):
+    B = len(lens)
+    Q = torch.zeros((B, Hq * D), dtype=TYPES[t], device=DEV)
+    Q[:, ::D] = q
+    pages, cache, table, plain = make_cache(lens, Hkv, 16, D, kind, t, 6)
+    cache[0].zero_()
+    key = float(torch.tensor(k, dtype=TYPES[t]))
+    if kind == "x16":
+        cache[0][..., 0] = key
+    else:
+        # the largest code and its factor, as a write of such keys makes them
+        cache[0][..., 0] = (0x7E if kind == "e4m3" else 127) if k > 0 else (0xFE if kind == "e4m3" else 129)
+        top = 448.0 if kind == "e4m3" else 127.0
+        cache[2].fill_(abs(key) / top)
+        key = float(cache[2].reshape(-1)[0]) * top * (1 if k > 0 else -1)
+    O, L = run_decode(Q, lens, Hq, Hkv, D, 16, kind, t, 1.0, pages, cache, table)
+    score = float(Q[0, 0]) * key
+    o, l = f64(O), f64(L)
+    u = UNIT[t if kind == "x16" else "f16"]
+    for b, n in enumerate(lens):
+        for h in range(Hq):
+            v = plain[1][b][h // (Hq // Hkv)]
+            want = v.mean(0)
+            assert_close(o[b, h * D:(h + 1) * D], want, UNIT[t] * np.abs(want) + (u + n * 2.0 ** -23) * np.abs(v).max(), f"head {h}")
+            assert_close(l[b, h], score + np.log(n), 1e-6 * abs(score) + 1e-5, f"lse of head {h}")
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D", DECODES)
+@pytest.mark.parametrize("q,k,t", [(1.5e19, -1.5e19, "bf16"), (60000.0, -60000.0, "f16"), (7e5, 7e5, "bf16")])
+def test_decode_of_equal_scores(q, k, t, lens, Hq, Hkv, D):
+    decode_of_equal_scores(q, k, t, lens, Hq, Hkv, D, "x16")
