@@ -1022,9 +1022,9 @@ cudaError_t launch_prompt(bool x_f16, const PromptArgs& pa, void* ws, int sm_cou
     a.HC = p.HC;
     a.splits = p.splits;
     a.causal = pa.causal ? 1 : 0;
-    // a scale of zero as the smallest normal: products stay zero, and keys that
-    // are not seen stay at minus infinity
-    a.scale2 = fmaxf(pa.scale * kLog2e, 1.17549435e-38f);
+    // a scale of zero as the smallest number: the largest product stays below 2^-20, and
+    // keys that are not seen stay at minus infinity
+    a.scale2 = fmaxf(pa.scale * kLog2e, FLT_TRUE_MIN);
     if (pa.D > 64) return x_f16 ? launch_tiles<128, true>(maps, a, grid, stream) : launch_tiles<128, false>(maps, a, grid, stream);
     return x_f16 ? launch_tiles<64, true>(maps, a, grid, stream) : launch_tiles<64, false>(maps, a, grid, stream);
 }

@@ -131,3 +131,14 @@ def decode_of_equal_scores(q, k, t, lens, Hq, Hkv, D, kind):
 @pytest.mark.parametrize("q,k,t", [(1.5e19, -1.5e19, "bf16"), (60000.0, -60000.0, "f16"), (7e5, 7e5, "bf16")])
 def test_decode_of_equal_scores(q, k, t, lens, Hq, Hkv, D):
     decode_of_equal_scores(q, k, t, lens, Hq, Hkv, D, "x16")
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk,Hq,Hkv,D", SIZES)
+def test_prompt_of_scale_zero(nq, nk, Hq, Hkv, D, causal):
+    """Scale zero weighs all keys alike, however large the products are."""
+    Q, K, V = (heads(s, n, H, D, "bf16") for s, n, H in ((3, sum(nq), Hq), (4, sum(nk), Hkv), (5, sum(nk), Hkv)))
+    Q *= 2.0 ** 60
+    K *= 2.0 ** 50
+    O, L = run_prompt(Q, K, V, nq, nk, Hq, Hkv, D, "bf16", causal, 0.0)
+    check_means(O, L, V, nq, nk, Hq, Hkv, D, "bf16", causal, 0.0)
