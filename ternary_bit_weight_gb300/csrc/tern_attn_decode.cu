@@ -8,10 +8,12 @@
 // follows the running maximum lazily: it moves only when a score passes it by
 // 8, so weights stay below 2^8 and most tiles need one vote instead of a
 // reduction.  With coded values v = c f (code times factor) the products with
-// V use the codes, exact in fp16, and weights 2^(s + log2 f - mo) under a
-// reference mo of their own, so that factors of any size keep the weights
-// within fp16; keys' factors multiply the scores.  Queries are brought to fp16
-// by a power of two per row, which the scores' factor undoes.
+// V use the codes, exact in fp16, and weights 2^((s - m) + log2 f - r) with a
+// reference r of their own, so that factors of any size keep the weights
+// within fp16; keys' factors multiply the scores.  (r is relative to m, and the
+// difference s - m taken first: log2 f added to a large score is lost in its
+// rounding.)  Queries are brought to fp16 by a power of two per row, which the
+// scores' factor undoes.
 //
 // What bounds it: the bytes of the cache, read once (the G query heads of a
 // key/value head are rows of the same products).
@@ -228,6 +230,9 @@ __device__ __forceinline__ int arrive(int32_t* counter) {
     asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
     return before;
 }
+
+// The larger of two references of the products with V, finite.
+__device__ __forceinline__ float join_reference(float a, float b) { return fmaxf(fmaxf(a, b), kNone); }
 
 __device__ __forceinline__ float warp_max(float x) {
     float y;
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
     uint8_t* ring = smem + warp * S::kStages * S::kStage;
     uint8_t* factors = smem + kWarps * S::kStages * S::kStage + warp * S::kStages * S::kScaleBytes;
     float* merge = reinterpret_cast<float*>(smem + kWarps * S::kStages * (S::kStage + S::kScaleBytes));
-    float* stat = merge + S::kMerge / 4;         // [warp][row][m, mo, l]
+    float* stat = merge + S::kMerge / 4;         // [warp][row][m, r, l]
     const uint32_t bars = smem_u32(stat + S::kStat / 4) + warp * S::kStages * 8;   // a warp's stages
     volatile int* last_flag = reinterpret_cast<volatile int*>(reinterpret_cast<uint8_t*>(stat) + S::kStat +
                                                              kWarps * S::kStages * 8);
@@ -655,10 +660,10 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
     int parts = 0;
 
     // a warp stores the finished sums of one head
-    auto finish = [&](const Segment& s, int head, const float (&sum)[S::kEach], float M, float MO, float L) {
+    auto finish = [&](const Segment& s, int head, const float (&sum)[S::kEach], float M, float R, float L) {
         const int hk = a.passes == 1 ? s.hv : s.hv / a.passes;
         const int64_t q_head = static_cast<int64_t>(hk) * a.G + (s.hv - hk * a.passes) * kRows + head;
-        const float f = L == 0.0f ? 0.0f : exp2_approx(MO - M) / L;
+        const float f = L == 0.0f ? 0.0f : exp2_approx(R) / L;
         const int d = lane * S::kEach;
         if (d < a.D) {
             uint16_t* dst = a.o + s.b * a.ldo + q_head * a.D + d;
@@ -677,7 +682,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
         const int head0 = (seg.hv - hk * a.passes) * kRows;               // first of the group's heads
         const int heads = min(kRows, a.G - head0);
         // the thread's heads: 8c + 2t, 8c + 2t + 1
-        float m[COLS][2], mo[COLS][2], l[COLS][2], fac[COLS][2];
+        float m[COLS][2], r[COLS][2], l[COLS][2], fac[COLS][2];
         float o[COLS][S::kSteps][4];
         const bool mine = seg.begin + warp < seg.end;
         if (mine) {
@@ -708,7 +713,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     fac[c][h] = kCoded ? __shfl_sync(0xffffffffu, f, 4 * (2 * t + h)) : f;
-                    m[c][h] = mo[c][h] = kNone;
+                    m[c][h] = r[c][h] = kNone;
                     l[c][h] = 0.0f;
                 }
 #pragma unroll
@@ -779,8 +784,9 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
             for (int c = 0; c < COLS; ++c)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[c][i] = (s[c][0][i] + s[c][1][i]) * fac[c][i & 1];
-                    if (kCoded) x[c][i] *= kf[i >> 1];
+                    // rounded before the reference is taken off, which is one of them
+                    x[c][i] = __fmul_rn(s[c][0][i] + s[c][1][i], fac[c][i & 1]);
+                    if (kCoded) x[c][i] = __fmul_rn(x[c][i], kf[i >> 1]);
                 }
             if (mask != 0xFFFFu) {
 #pragma unroll
@@ -801,8 +807,8 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                     top[c][h] = fmaxf(x[c][h], x[c][2 + h]);
                     past = past || top[c][h] > m[c][h] + kLazy;
                     if (kCoded) {
-                        topo[c][h] = fmaxf(x[c][h] + vl[0], x[c][2 + h] + vl[1]);
-                        past = past || topo[c][h] > mo[c][h] + kLazy;
+                        topo[c][h] = fmaxf((x[c][h] - m[c][h]) + vl[0], (x[c][2 + h] - m[c][h]) + vl[1]);
+                        past = past || topo[c][h] > r[c][h] + kLazy;
                     }
                 }
             if (__any_sync(0xffffffffu, past)) {
@@ -815,16 +821,17 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
                         up = fmaxf(m[c][h], up);
-                        f[h] = exp2_approx(m[c][h] - up);
+                        const float moved = m[c][h] - up;
+                        f[h] = exp2_approx(moved);
                         l[c][h] *= f[h];
                         m[c][h] = up;
                         if (kCoded) {
-                            up = topo[c][h];
+                            up = fmaxf((x[c][h] - m[c][h]) + vl[0], (x[c][2 + h] - m[c][h]) + vl[1]);
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1) up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, d));
-                            up = fmaxf(mo[c][h], up);
-                            f[h] = exp2_approx(mo[c][h] - up);
-                            mo[c][h] = up;
+                            up = join_reference(r[c][h] + moved, up);
+                            f[h] = exp2_approx(moved + (r[c][h] - up));
+                            r[c][h] = up;
                         }
                     }
 #pragma unroll
@@ -841,9 +848,10 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                 float w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    w[i] = exp2_approx(x[c][i] - m[c][i & 1]);
+                    const float past_m = x[c][i] - m[c][i & 1];
+                    w[i] = exp2_approx(past_m);
                     l[c][i & 1] += w[i];
-                    if (kCoded) w[i] = exp2_approx(x[c][i] + vl[i >> 1] - mo[c][i & 1]);
+                    if (kCoded) w[i] = exp2_approx((past_m + vl[i >> 1]) - r[c][i & 1]);
                 }
                 p[c][0] = transpose8(pack_x2<kMma16>(w[0], w[1]));
                 p[c][1] = transpose8(pack_x2<kMma16>(w[2], w[3]));
@@ -941,7 +949,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                     if (g == 0) {
                         float* dst = stat + (warp * kSlotRows + 8 * c + 2 * t + h) * 3;
                         dst[0] = m[c][h];
-                        dst[1] = kCoded ? mo[c][h] : m[c][h];
+                        dst[1] = kCoded ? r[c][h] : 0.0f;
                         dst[2] = l[c][h];
                     }
                 }
@@ -969,9 +977,10 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
             if (head < heads) {
                 const float* sp = stat + ((lane & 7) * kSlotRows + head) * 3;
                 const bool had = lane < active;
-                const float M = warp_max(had ? sp[0] : kNone), MO = warp_max(had ? sp[1] : kNone);
+                const float M = warp_max(had ? sp[0] : kNone);
                 const float L = warp_add(had ? sp[2] * exp2_approx(sp[0] - M) : 0.0f);
-                const float fw = had ? exp2_approx(sp[1] - MO) : 0.0f;
+                const float ri = had ? sp[1] + (sp[0] - M) : kNone, R = join_reference(kNone, warp_max(ri));
+                const float fw = had ? exp2_approx(ri - R) : 0.0f;
                 float sum[S::kEach];
 #pragma unroll
                 for (int i = 0; i < S::kEach; ++i) sum[i] = 0.0f;
@@ -983,7 +992,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                     for (int i = 0; i < S::kEach; ++i) sum[i] += x.v[i] * f;
                 }
                 if (whole) {
-                    finish(done, head, sum, M, MO, L);
+                    finish(done, head, sum, M, R, L);
                 } else {
                     Floats<S::kEach> x;
 #pragma unroll
@@ -992,7 +1001,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                     if (lane == 0) {
                         float* dst = slot + kSlotRows * DP + head * 3;
                         dst[0] = M;
-                        dst[1] = MO;
+                        dst[1] = R;
                         dst[2] = L;
                     }
                 }
@@ -1033,7 +1042,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
         for (int c = 0; c < COLS; ++c) {
             const int head = 8 * c + warp;
             if (head >= heads) continue;
-            float M = kNone, MO = kNone, L = 0.0f;
+            float M = kNone, R = kNone, L = 0.0f;
             float sum[S::kEach];
 #pragma unroll
             for (int i = 0; i < S::kEach; ++i) sum[i] = 0.0f;
@@ -1046,12 +1055,12 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                     x0[k] = load_l2<S::kEach>(part(i0 + min(k, count - 1)) + head * DP + lane * S::kEach);
                 const float* sp = part(i0 + min(lane, count - 1)) + kSlotRows * DP + head * 3;
                 const bool had = lane < count;
-                const float mi = had ? __ldcg(sp) : kNone, moi = had ? __ldcg(sp + 1) : kNone, li = had ? __ldcg(sp + 2) : 0.0f;
-                const float up = fmaxf(M, warp_max(mi)), upo = fmaxf(MO, warp_max(moi));
-                const float keep = exp2_approx(MO - upo), f = exp2_approx(moi - upo);
+                const float mi = had ? __ldcg(sp) : kNone, rp = had ? __ldcg(sp + 1) : kNone, li = had ? __ldcg(sp + 2) : 0.0f;
+                const float up = fmaxf(M, warp_max(mi)), before = R + (M - up), ri = rp + (mi - up);
+                R = join_reference(before, warp_max(had ? ri : kNone));
+                const float keep = exp2_approx(before - R), f = exp2_approx(ri - R);
                 L = L * exp2_approx(M - up) + li * exp2_approx(mi - up);
                 M = up;
-                MO = upo;
 #pragma unroll
                 for (int i = 0; i < S::kEach; ++i) sum[i] *= keep;
 #pragma unroll
@@ -1069,7 +1078,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                     for (int i = 0; i < S::kEach; ++i) sum[i] += x.v[i] * fk;
                 }
             }
-            finish(done, head, sum, M, MO, warp_add(L));
+            finish(done, head, sum, M, R, warp_add(L));
         }
         if (threadIdx.x == 0) a.arrived[c0] = 0;
     }

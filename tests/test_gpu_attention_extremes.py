@@ -142,3 +142,12 @@ def test_prompt_of_scale_zero(nq, nk, Hq, Hkv, D, causal):
     K *= 2.0 ** 50
     O, L = run_prompt(Q, K, V, nq, nk, Hq, Hkv, D, "bf16", causal, 0.0)
     check_means(O, L, V, nq, nk, Hq, Hkv, D, "bf16", causal, 0.0)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "i8"])
+@pytest.mark.parametrize("lens,Hq,Hkv,D", DECODES)
+@pytest.mark.parametrize("q,k,t", [(100.0, 100.0, "bf16"), (3001.0, 3001.0, "f16"), (60000.0, -60000.0, "f16"),
+                                   (7e5, 7e5, "bf16"), (1.5e19, -1.5e19, "bf16"), (1.5e19, 1.5e19, "bf16")])
+def test_decode_of_equal_scores_over_codes(q, k, t, lens, Hq, Hkv, D, kind):
+    """Value factors of unequal size under large scores."""
+    decode_of_equal_scores(q, k, t, lens, Hq, Hkv, D, kind)
