@@ -690,7 +690,10 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
             for (int c = 0; c < COLS; ++c) {
                 float f = a.scale2;
                 if constexpr (kCoded) {
-                    // times 2^e, so that the row's largest magnitude lies in [2^14, 2^15)
+                    // times 2^e, so that the row's largest magnitude lies in [2^14, 2^15); or
+                    // lower: beyond 2^120 the factor that undoes it would lose bits below
+                    // fp32's normal range, and a row of bf16's smallest normal numbers is at
+                    // 2^-6 by then, well inside fp16's
                     float top = 0.0f;
 #pragma unroll
                     for (int w = 0; w < S::kSteps; ++w) {
@@ -699,7 +702,7 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
                     }
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const int e = top > 0.0f && top <= 3.4e38f ? 14 - ilogbf(top) : 0;
+                    const int e = top > 0.0f && top <= 3.4e38f ? min(14 - ilogbf(top), 120) : 0;
                     // in two steps: 2^e may pass fp32's range
                     const float up0 = exp2f(static_cast<float>(e / 2)), up1 = exp2f(static_cast<float>(e - e / 2));
                     f = f * exp2f(static_cast<float>(-(e / 2))) * exp2f(static_cast<float>(-(e - e / 2)));

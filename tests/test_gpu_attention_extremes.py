@@ -151,3 +151,22 @@ def test_prompt_of_scale_zero(nq, nk, Hq, Hkv, D, causal):
 def test_decode_of_equal_scores_over_codes(q, k, t, lens, Hq, Hkv, D, kind):
     """Value factors of unequal size under large scores."""
     decode_of_equal_scores(q, k, t, lens, Hq, Hkv, D, kind)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "i8"])
+@pytest.mark.parametrize("size", [2.0 ** -110, 2.0 ** -124])
+def test_decode_of_tiny_queries(size, kind):
+    """Queries at the small end of bf16 against keys at the large end: the scores are
+    of ordinary size (powers of two move between the two without a rounding)."""
+    lens, Hq, Hkv, D, t = [300, 17], 4, 2, 64, "bf16"
+    Q = heads(7, 2, Hq, D, t)
+    pages, cache, table, plain = make_cache(lens, Hkv, 16, D, kind, t, 8)
+    small = (Q.double() * size).to(TYPES[t])
+    keep = small.double() / size == Q.double()     # what is below bf16's range drops out in both
+    cache[2] *= 1.0 / size
+    O1, L1 = run_decode(torch.where(keep, Q, torch.zeros_like(Q)), lens, Hq, Hkv, D, 16, kind, t, 0.125, pages,
+                        [cache[0], cache[1], cache[2] * size, cache[3]], table)
+    O2, L2 = run_decode(torch.where(keep, small, torch.zeros_like(Q)), lens, Hq, Hkv, D, 16, kind, t, 0.125, pages, cache, table)
+    # scores of the two calls differ by fp32 roundings at most: their bound in attn_util.py, twice
+    assert torch.allclose(L1, L2, rtol=2.0 ** -16, atol=2.0 ** -14)
+    assert torch.allclose(O1[:, :Hq * D].float(), O2[:, :Hq * D].float(), rtol=2.0 ** -6, atol=2.0 ** -8)
