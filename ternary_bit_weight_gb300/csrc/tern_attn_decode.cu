@@ -663,7 +663,8 @@ __global__ void __launch_bounds__(Shape<DP, KV, COLS>::kThreads, Shape<DP, KV, C
     auto finish = [&](const Segment& s, int head, const float (&sum)[S::kEach], float M, float R, float L) {
         const int hk = a.passes == 1 ? s.hv : s.hv / a.passes;
         const int64_t q_head = static_cast<int64_t>(hk) * a.G + (s.hv - hk * a.passes) * kRows + head;
-        const float f = L == 0.0f ? 0.0f : exp2_approx(R) / L;
+        // (exact below 2^-126, too, which the reference of small values comes to)
+        const float f = L == 0.0f ? 0.0f : exp2f(R) / L;
         const int d = lane * S::kEach;
         if (d < a.D) {
             uint16_t* dst = a.o + s.b * a.ldo + q_head * a.D + d;

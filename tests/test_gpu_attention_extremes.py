@@ -170,3 +170,19 @@ def test_decode_of_tiny_queries(size, kind):
     # scores of the two calls differ by fp32 roundings at most: their bound in attn_util.py, twice
     assert torch.allclose(L1, L2, rtol=2.0 ** -16, atol=2.0 ** -14)
     assert torch.allclose(O1[:, :Hq * D].float(), O2[:, :Hq * D].float(), rtol=2.0 ** -6, atol=2.0 ** -8)
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "i8"])
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -121])
+def test_decode_of_tiny_values(size, kind):
+    """Values at the small end of bf16: the output is the value of the same call scaled by a power of two."""
+    lens, Hq, Hkv, D, t = [200, 1], 4, 2, 64, "bf16"
+    Q = heads(9, 2, Hq, D, t)
+    pages, cache, table, plain = make_cache(lens, Hkv, 16, D, kind, t, 10)
+    O1, L1 = run_decode(Q, lens, Hq, Hkv, D, 16, kind, t, 0.125, pages, cache, table)
+    cache[3] *= size
+    O2, L2 = run_decode(Q, lens, Hq, Hkv, D, 16, kind, t, 0.125, pages, cache, table)
+    assert torch.equal(L1, L2)
+    o1, o2 = O1[:, :Hq * D].double(), O2[:, :Hq * D].double() / size
+    # beside the roundings of both calls, half of bf16's smallest number
+    assert torch.all((o1 - o2).abs() <= 2 * UNIT[t] * o1.abs() + 2.0 ** -133 / size)
