@@ -1134,8 +1134,8 @@ cudaError_t launch(Args& a, const DecodeArgs& d, int sm_count, cudaStream_t stre
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
                 return cudaErrorInvalidValue;
     }
-    static const cudaError_t limit = cudaFuncSetAttribute(decode_kernel<DP, KV, F16, COLS>,
-                                                          cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    static OncePerDevice once;
+    const cudaError_t limit = allow_smem(once, decode_kernel<DP, KV, F16, COLS>, S::kSmem);
     if (limit != cudaSuccess) return limit;
     return launch_after(decode_kernel<DP, KV, F16, COLS>, dim3(static_cast<unsigned>(grid)), S::kThreads, S::kSmem, stream,
                         maps, a);

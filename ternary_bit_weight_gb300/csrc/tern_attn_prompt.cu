@@ -957,8 +957,8 @@ Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, in
 
 template <int DP, bool F16, int NT>
 cudaError_t launch_form(const Maps& maps, const Args& a, int64_t grid, cudaStream_t stream) {
-    static const cudaError_t limit =
-        cudaFuncSetAttribute(prompt_kernel<DP, F16, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DP, NT>());
+    static OncePerDevice once;
+    const cudaError_t limit = allow_smem(once, prompt_kernel<DP, F16, NT>, smem_bytes<DP, NT>());
     if (limit != cudaSuccess) return limit;
     return launch_after(prompt_kernel<DP, F16, NT>, dim3(static_cast<unsigned>(grid)), Form<NT>::kThreads,
                         smem_bytes<DP, NT>(), stream, maps, a);

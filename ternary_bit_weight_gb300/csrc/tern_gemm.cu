@@ -866,13 +866,8 @@ EncodeTiledFn encode_tiled_fn() {
 
 template <bool EXT, int AU, bool GROUPED>
 cudaError_t set_smem_limit() {
-    static cudaError_t status = cudaErrorUnknown;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        status = cudaFuncSetAttribute(gemm_kernel<EXT, AU, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      kSmemBytes);
-    });
-    return status;
+    static OncePerDevice once;
+    return allow_smem(once, gemm_kernel<EXT, AU, GROUPED>, kSmemBytes);
 }
 
 // The launch with the parameter block of its problem count (prepared for

@@ -6,7 +6,18 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "tern_device.h"
+
 namespace tern {
+
+// Lets `kernel` use up to `bytes` of dynamic shared memory on the current device.
+template <typename Kernel>
+cudaError_t allow_smem(OncePerDevice& once, Kernel kernel, int bytes) {
+    int device = 0;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    return once(device, [&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+}
 
 // ------------------------------------------------------------ pack family
 cudaError_t launch_pack(const int8_t* t, int64_t count, uint8_t* packed, int32_t* err,

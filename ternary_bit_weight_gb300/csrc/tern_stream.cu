@@ -742,13 +742,8 @@ EncodeTiledFn encode_tiled_fn() {
 
 template <bool ONE, bool XF16, int EXT>
 cudaError_t set_smem_limit() {
-    static cudaError_t status = cudaErrorUnknown;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        status = cudaFuncSetAttribute(stream_kernel<ONE, XF16, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      kSmemLimit);
-    });
-    return status;
+    static OncePerDevice once;
+    return allow_smem(once, stream_kernel<ONE, XF16, EXT>, kSmemLimit);
 }
 
 template <bool ONE, bool XF16, int EXT>
