@@ -9,12 +9,15 @@ If the library has not been built, importing this module raises.
 
 The attention-side calls go through a small extension module
 (csrc/tern_python.c) instead of ctypes, which converts their many arguments
-three times as fast; the functions below are the same to a caller.
+three times as fast; where it was not built for this interpreter (no Python
+headers), they go through ctypes to the same library.  The functions below are
+the same to a caller.
 """
 from __future__ import annotations
 
 import ctypes
 import importlib.util
+import operator
 import os
 
 from . import build as _build
@@ -155,9 +158,42 @@ def _load():
 _lib = _load()
 
 
+class _CtypesCalls:
+    """The extension module's calls through ctypes, with its conversions and refusals."""
+
+    def __getattr__(self, name):
+        fn = getattr(_lib, name)
+        kinds = fn.argtypes
+
+        def pointer(x):
+            if x is None or isinstance(x, int):
+                return x
+            return x.data_ptr()
+
+        def integer(bits):
+            def convert(x):
+                x = operator.index(x)
+                if not -(1 << (bits - 1)) <= x < 1 << (bits - 1):
+                    raise OverflowError(f"argument does not fit {bits} bits")
+                return x
+            return convert
+
+        convert = {ctypes.c_void_p: pointer, ctypes.c_int: integer(32), ctypes.c_int64: integer(64),
+                   ctypes.c_size_t: integer(64), ctypes.c_float: float}
+        convert = [convert[k] for k in kinds]
+
+        def call(*args):
+            if len(args) != len(convert):
+                raise TypeError(f"expected {len(convert)} arguments, got {len(args)}")
+            return fn(*[c(x) for c, x in zip(convert, args)])
+
+        setattr(self, name, call)
+        return call
+
+
 def _load_native():
     if not os.path.exists(_build.PY_LIB):
-        raise ImportError(f"{_build.PY_LIB} is not built; run `python -c 'import __graft_entry__ as g; g.build()'`")
+        return _CtypesCalls()
     spec = importlib.util.spec_from_file_location("_tern_python", _build.PY_LIB)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)

@@ -1,9 +1,11 @@
 """Build libtern.so in-tree with nvcc for sm_103a (GB300).
 
 Each ``csrc/*.cu`` file is compiled separately and in parallel, then linked
-into ``_build/libtern.so`` against the shared CUDA runtime; ``csrc/tern_python.c``
-becomes ``_build/_tern_python.so``, the argument marshalling of the calls made
-for single tokens.  Rebuilds only when a source or header is newer.
+into ``_build/libtern.so`` against the shared CUDA runtime.  ``csrc/tern_python.c``
+becomes an extension module of the interpreter that builds, beside it: the argument
+marshalling of the calls made for single tokens.  Where Python's headers are not
+installed it is left out, and the binding marshals with ctypes.  Rebuilds only what
+a newer source or header asks for.
 """
 from __future__ import annotations
 
@@ -21,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libtern.so")
 PY_SRC = os.path.join(CSRC, "tern_python.c")
-PY_LIB = os.path.join(BUILD, "_tern_python.so")
+PY_LIB = os.path.join(BUILD, "_tern_python" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-Wall",
@@ -43,19 +45,32 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(PY_LIB):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(PY_LIB))
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
-        + glob.glob(os.path.join(INCLUDE, "*.h")) + [PY_SRC, __file__]
-    return any(os.path.getmtime(d) > t for d in deps)
+def _newer(target: str, deps) -> bool:
+    """target is missing or older than one of deps."""
+    return not os.path.exists(target) or any(os.path.getmtime(d) > os.path.getmtime(target) for d in deps)
+
+
+def _headers():
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
+
+
+def python_headers():
+    """Folder of Python.h, or None where it is not installed."""
+    path = sysconfig.get_paths()["include"]
+    return path if os.path.exists(os.path.join(path, "Python.h")) else None
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libtern.so; returns its path."""
-    if not force and not _stale():
-        return LIB
+    """Compile and link libtern.so and the extension module; returns libtern.so's path."""
+    if force or _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+                       + _headers()):
+        _build_library(verbose, ptxas_info)
+    if python_headers() and (force or _newer(PY_LIB, _headers() + [PY_SRC])):
+        _build_python()
+    return LIB
+
+
+def _build_library(verbose: bool, ptxas_info: bool) -> None:
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if ptxas_info else []
@@ -81,13 +96,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if res.returncode != 0:
         raise RuntimeError(f"link of libtern.so failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
-    cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE, PY_SRC,
-           "-o", PY_LIB + f".tmp{os.getpid()}", "-L", BUILD, "-l:libtern.so", "-Wl,-rpath,$ORIGIN"]
+
+
+def _build_python() -> None:
+    """The extension module, by nvcc's host compiler."""
+    tmp = PY_LIB + f".tmp{os.getpid()}"
+    cmd = [_nvcc(), "-shared", "-cudart", "none", "-Xcompiler", "-fPIC,-O2,-Wall", "-I", python_headers(), "-I", INCLUDE,
+           PY_SRC, "-o", tmp, "-L", BUILD, "-Xlinker", "-l:libtern.so", "-Xlinker", "-rpath,$ORIGIN"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"gcc failed for tern_python.c:\n{res.stdout}\n{res.stderr}")
-    os.replace(PY_LIB + f".tmp{os.getpid()}", PY_LIB)
-    return LIB
+        raise RuntimeError(f"nvcc failed for tern_python.c:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, PY_LIB)
 
 
 if __name__ == "__main__":
