@@ -159,13 +159,6 @@ struct Shape {
 
 __host__ __device__ constexpr int slot_floats(int DP, int rows) { return rows * (DP + 3); }
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
 // N (2 or 4) floats at once.
 template <int N>
 struct __align__(4 * N) Floats {

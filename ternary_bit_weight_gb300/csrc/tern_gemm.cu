@@ -37,13 +37,13 @@
 
 #include <cuda.h>
 
-#include <mutex>
 #include <type_traits>
 #include <vector>
 
 #include "tern_common.cuh"
 #include "tern_internal.h"
 #include "tern_sm100.cuh"
+#include "tern_tensormap.h"
 
 namespace tern {
 namespace {
@@ -844,25 +844,6 @@ __global__ void __launch_bounds__(kTileRows) split_reduce_kernel(const ReduceArg
 }
 
 // ---------------------------------------------------------------- host
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
 
 template <bool EXT, int AU, bool GROUPED>
 cudaError_t set_smem_limit() {

@@ -58,11 +58,10 @@
 
 #include <cuda.h>
 
-#include <mutex>
-
 #include "tern_common.cuh"
 #include "tern_internal.h"
 #include "tern_sm100.cuh"
+#include "tern_tensormap.h"
 
 namespace tern {
 namespace {
@@ -720,25 +719,6 @@ stream_kernel(const __grid_constant__ XMaps xmaps, const StreamArgs a) {
 }
 
 // ---------------------------------------------------------------- host
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
 
 template <bool ONE, bool XF16, int EXT>
 cudaError_t set_smem_limit() {
