@@ -436,7 +436,12 @@ typedef enum { TERN_KV_X16 = 0, TERN_KV_E4M3 = 1, TERN_KV_I8 = 2 } tern_kv_type;
  * h_inv_freq[i] / (2 pi), the turns of pair i over the trained context, and
  * r = clamp((u_i - turns_low) / (turns_high - turns_low), 0, 1), the frequency
  * becomes f (r + (1 - r) / factor), and *h_amplitude = 0.1 ln(factor) + 1
- * (1 for factor <= 1); otherwise *h_amplitude = 1.  h_inv_freq and
+ * (1 for factor <= 1); otherwise *h_amplitude = 1.  This ramp is linear in
+ * the turns.  Models are also run with one that is linear in the pair's index
+ * between the pairs of turns_high and turns_low turns; the two agree outside
+ * it and differ inside (rot_dim 128, base 1e6, trained_len 32768, factor 4,
+ * turns 1 to 32: pair 30 is scaled by 0.42 here, by 0.69 there).  Take the one
+ * the model was trained with: tern_rope reads any table.  h_inv_freq and
  * h_amplitude are HOST memory.  rot_dim positive and even (above 2 for
  * TERN_ROPE_SCALE_BASE), base > 0, factor > 0; TERN_ROPE_SCALE_PARTS also
  * trained_len > 0 and turns_high > turns_low. */
@@ -468,7 +473,9 @@ tern_status tern_rope(int x_type, int layout, int64_t T, int64_t D, int64_t rot_
  * s / page_size.  The codes of a head's D values x with m = max |x|:
  *   factor = m / top, code = round(x * (top / m)) in fp32, ties to even,
  * top = 448 (TERN_KV_E4M3: to 8-bit floats of 4 exponent and 3 mantissa
- * bits) or 127 (TERN_KV_I8); m == 0 gives factor 0 and codes 0.  A head that
+ * bits) or 127 (TERN_KV_I8); m == 0 gives factor 0 and codes 0.  A quotient
+ * top / m past fp32's range is its largest number instead, so a head with m
+ * below some 1e-36 has smaller codes and reads back smaller.  A head that
  * holds a NaN or an infinity gets factor NaN and codes 0: it reads back as
  * NaN and nothing else does.  Cache pointers are 16-byte aligned, the factors
  * 4-byte. */
@@ -517,7 +524,10 @@ tern_status tern_kv_read(int x_type, int kv_type, int64_t T, int64_t Hkv, int64_
  *   d_O    device [Tq, ldo] of x_type; rows of no sequence are not written
  *   d_lse  optional device fp32 [Tq, Hq]
  *   d_ws   as tern_linear's (and may be the same one), of
- *          tern_attn_prompt_workspace_bytes
+ *          tern_attn_prompt_workspace_bytes.  That size does not grow with the
+ *          arguments: few rows against many keys need room for partial results
+ *          that more rows do without.  A workspace for calls of several sizes
+ *          is as large as the largest answer for any of them
  * Offsets outside [0, Tq] / [0, Tkv] are read as the nearest end, a sequence
  * whose offsets decrease as empty. */
 size_t tern_attn_prompt_workspace_bytes(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, int64_t D);

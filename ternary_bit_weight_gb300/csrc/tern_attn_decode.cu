@@ -13,13 +13,16 @@
 // within fp16; keys' factors multiply the scores.  (r is relative to m, and the
 // difference s - m taken first: log2 f added to a large score is lost in its
 // rounding.)  Queries are brought to fp16 by a power of two per row, which the
-// scores' factor undoes.
+// scores' factor undoes.  Weights are rounded to 16 bits for that product, whose
+// operands have one type; l sums them unrounded.  (Relative distance from 64 bits:
+// bf16 values 0.0021, and 0.0017 with the output's rounding alone; fp16 weights over
+// codes add nothing to 0.0017.)
 //
 // What bounds it: the bytes of the cache, read once (the G query heads of a
 // key/value head are rows of the same products).
 // Measured, 40 / 8 heads of 128: 128 sequences of 8192 over int8 codes 338 us
 // (6.6 TB/s), two of 32768 in fp16 49.1 us (5.5 TB/s), 32 of up to 8192 over e4m3
-// codes 39.0 us, one of 701 8.6 us, of which some 8 us are launch, start and join.
+// codes 39.3 us, one of 701 8.7 us, of which some 8 us are launch, start and join.
 //
 // Work.  An item is one (sequence, key/value head); its tiles of 16 keys are
 // dealt to the CTAs in one of three ways (see Share), a segment being the part of
@@ -283,9 +286,9 @@ struct Segment {
 // The last two have fewer segments and partial results than by weight, and less
 // equal loads.  Where the loads are within `slack` of equal, and kJoin, they are
 // faster, because the memory is what is busy, not every SM: bf16 cache of 18 sequences of 4064 (144
-// items for 152 CTAs) 50.0 us against 55 by weight, 32 of 2272 (two items each) 51
-// against 55; e4m3 codes of 30 of 3000 (240 for 304) 36.9 against 40.9, int8 of 32
-// of 512 11.5 against 16.4.  (int8 codes of 128 of 8192 in fours, 1.19 times the
+// items for 152 CTAs) 50.1 us against 55 by weight, 32 of 2272 (two items each) 51
+// against 55; e4m3 codes of 30 of 3000 (240 for 304) 37.4 against 41.8, int8 of 32
+// of 512 11.8 against 17.4.  (int8 codes of 128 of 8192 in fours, 1.19 times the
 // equal load, 367 against 338: there the SMs are as busy as the memory.)
 struct Share {
     int whole, several;

@@ -6,7 +6,10 @@
 // (s = scale log2(e) q.k), rescaled when m moves.  m follows the running
 // maximum lazily: it moves only when a tile's maximum passes it by 8, so
 // weights stay below 2^8 and the rescaling of o is rare.  Weights are rounded
-// to the 16-bit type for the product with V; l sums them unrounded in fp32.
+// to the 16-bit type for the product with V, the tensor cores taking both of its
+// operands in one type; l sums them unrounded in fp32.  (With it the output of 8192
+// bf16 tokens is 0.0021, relative, from 64 bits; with the output's rounding alone it
+// would be 0.0016.)
 //
 // What bounds it: for long prompts the tensor cores (4 D flops per pair that
 // attends) and, beside them, the exponential of every score; for short ones
@@ -19,8 +22,8 @@
 // tokens against the same keys: while the softmax of one runs, the tensor
 // cores multiply for the other.  For short sequences a CTA has one tile (10 warps,
 // the load warp is the guard, too) and two CTAs share an SM (see plan_prompt).
-// Measured, 40 / 8 heads of 128, causal, bf16: 8192 tokens 450-490 us (1.40-1.53
-// PFLOP/s, with the power limit), 4096 134 us, 512 11 us, 32 prompts of 128 39 us.
+// Measured, 40 / 8 heads of 128, causal, bf16: 8192 tokens 450-485 us (1.42-1.53
+// PFLOP/s, with the power limit), 4096 137 us, 512 11.2 us, 32 prompts of 128 40 us.
 //
 // Roles (two tiles, 20 warps):
 //   * warp 0 issues all tcgen05.mma: scores S_i = Q_i K_j^T (both operands in
@@ -360,9 +363,10 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
     Item it = {};
     if constexpr (NT == 1) {
         // One warp finds the item, the others get it with the barrier: short blocks
-        // are many, and ten warps' loads of the same offsets held one another up (32
-        // queries of up to 48 tokens 6.9 us instead of 7.6, 200 prompts of 64 117 instead
-        // of 135).  With two tiles the loads are earlier when nobody waits for a barrier.
+        // are many, and ten warps' loads of the same offsets held one another up (per
+        // call in a CUDA graph, 32 queries of up to 48 tokens 6.9 us instead of 7.6, 200
+        // prompts of 64 117 instead of 135).  With two tiles the loads are earlier when
+        // nobody waits for a barrier.
         int* found = reinterpret_cast<int*>(ctrl + kItem);
         if (warp == F::kLoadWarp) {
             if (!(a.B <= 64 ? find_item<1>(a, block, lane, it) : find_item<4>(a, block, lane, it))) it.nq = 0;
@@ -911,9 +915,9 @@ Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, in
     // the other's products, and where short blocks fit the GPU at once and their
     // latency counts.  Two tiles against the same keys otherwise, which read K and V
     // half as often.  27B-class heads, us, one tile / two: 32 prompts of 128 39 / 61,
-    // 64 of 256 155 / 190, 16 of 512 89 / 98, 16 of 768 154 / 158, 16 of 1024 236 / 235;
-    // 24 documents of up to 1023, not causal, 57 / 54; 8 of 256 new tokens after 1000
-    // 64 / 62; one prompt of 512 10.9 / 12.2, of 1500 32 / 27.
+    // 64 of 256 156 / 192, 16 of 512 89 / 99, 16 of 768 154 / 160, 16 of 1024 234 / 235;
+    // 24 documents of up to 1023, not causal, 56 / 54; 8 of 256 new tokens after 1000
+    // 63 / 61; one prompt of 512 11.1 / 12.4, of 1500 31 / 27, of 4096 143 / 134.
     const int64_t single = B * ceil_div(avg_q, p.tok) * p.HC;
     const int64_t seen = causal ? avg_k - avg_q / 2 : avg_k;   // keys of a row, on average
     p.nt = avg_q <= p.tok || 2 * seen < 5 * kTileN || (avg_k < 6 * kTileN && single <= 2 * sm_count) ? 1 : 2;
@@ -923,8 +927,8 @@ Plan plan_prompt(int64_t B, int64_t Tq, int64_t Tkv, int64_t Hq, int64_t Hkv, in
     // each a key tile at a time and 4.5 beside them; partial results written and
     // read at 8 TB/s, and a second launch.  A split keeps at least four key tiles.
     // From four waves on blocks of unequal length fill the GPU by themselves.
-    // 27B-class heads, us, split / not: 256 new tokens against 16384 74 / 198, 512
-    // 142 / 183, 1024 274 / 347, 2048 480 / 508; 8 x 128 against 4128 116 / 121.
+    // 27B-class heads, us, split / not: 256 new tokens against 16384 74 / 183, 512
+    // 143 / 185, 1024 278 / 351, 2048 490 / 515; 8 x 128 against 4128 117 / 120.
     const int64_t items = B * ceil_div(avg_q, p.nt * p.tok) * p.HC, places = static_cast<int64_t>(sm_count) * (p.nt == 1 ? 2 : 1);
     const double tiles = static_cast<double>(avg_k) / kTileN, step = p.nt == 1 ? 1.25 : 1.45;
     int64_t splits = 1;
