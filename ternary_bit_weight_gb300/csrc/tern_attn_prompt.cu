@@ -649,8 +649,23 @@ __global__ void __launch_bounds__(Form<NT>::kThreads, Form<NT>::kCtas) prompt_ke
             }
             if (far) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (share[r0 + 8 * q].x != 0.0f) rebase(s, q, share[r0 + 8 * q].x);
+                for (int q = 0; q < 2; ++q) {
+                    const float base = share[r0 + 8 * q].x;
+                    float top = s[2 * q];
+#pragma unroll
+                    for (int c = 0; c < kTileN / 8; ++c) top = fmaxf(top, fmaxf(s[4 * c + 2 * q], s[4 * c + 2 * q + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));   // (which also is the lanes' barrier)
+                    top = __fmul_rn(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)), scale2);
+                    if (top <= FLT_MAX && top - base > FLT_MAX) {
+                        // beyond fp32's range above the base: what the row has seen so far weighs
+                        // nothing, and it starts again
+                        m[q] = kNone;
+                        if ((lane & 3) == 0) share[r0 + 8 * q].x = 0.0f;
+                    } else if (base != 0.0f) {
+                        rebase(s, q, base);
+                    }
+                }
+                __syncwarp();
             }
             float mx[2];
 #pragma unroll

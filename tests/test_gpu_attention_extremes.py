@@ -186,3 +186,50 @@ def test_decode_of_tiny_values(size, kind):
     o1, o2 = O1[:, :Hq * D].double(), O2[:, :Hq * D].double() / size
     # beside the roundings of both calls, half of bf16's smallest number
     assert torch.all((o1 - o2).abs() <= 2 * UNIT[t] * o1.abs() + 2.0 ** -133 / size)
+
+
+def one_sided_means(V, n, m, causal, ahead):
+    """Means over the visible keys from `ahead` on, or over all that are visible where none is."""
+    out = np.zeros((n, V.shape[1]))
+    for i in range(n):
+        seen = min(m, max(0, i + 1 + m - n)) if causal else m
+        if seen > 0:
+            out[i] = V[ahead:seen].mean(0) if seen > ahead else V[:seen].mean(0)
+    return out
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("ahead", [20, 128, 300, 700])
+def test_prompt_of_scores_across_the_whole_range(ahead, causal):
+    """Keys with scores of -2.3e38 before keys with 2.3e38: their distance is beyond fp32."""
+    for n, m, Hq, Hkv, D in ((900, 900, 16, 8, 64), (40, 1000, 2, 1, 128), (16, 2100, 4, 1, 128)):
+        Q, K = (torch.zeros((r, H * D), dtype=torch.bfloat16, device=DEV) for r, H in ((n, Hq), (m, Hkv)))
+        Q[:, ::D] = 1.5e19
+        K[:ahead, ::D] = -1.5e19
+        K[ahead:, ::D] = 1.5e19
+        V = heads(11, m, Hkv, D, "bf16")
+        O, L = run_prompt(Q, K, V, [n], [m], Hq, Hkv, D, "bf16", causal, 1.0)
+        o, v = f64(O), f64(V)
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            vv = v[:, g * D:(g + 1) * D]
+            want = one_sided_means(vv, n, m, causal, ahead)
+            bound = UNIT["bf16"] * np.abs(want) + (UNIT["bf16"] + m * 2.0 ** -23) * np.abs(vv).max()
+            assert_close(o[:, h * D:(h + 1) * D], want, bound, f"head {h}")
+
+
+@pytest.mark.parametrize("ahead", [5, 16, 300])
+def test_decode_of_scores_across_the_whole_range(ahead):
+    Hq, Hkv, D, n = 4, 2, 64, 700
+    Q = torch.zeros((1, Hq * D), dtype=torch.bfloat16, device=DEV)
+    Q[:, ::D] = 1.5e19
+    pages, cache, table, plain = make_cache([n], Hkv, 16, D, "x16", "bf16", 12)
+    cache[0].zero_()
+    for j in range(n):
+        cache[0][int(table[0, j // 16]), :, j % 16, 0] = -1.5e19 if j < ahead else 1.5e19
+    O, L = run_decode(Q, [n], Hq, Hkv, D, 16, "x16", "bf16", 1.0, pages, cache, table)
+    o = f64(O)
+    for h in range(Hq):
+        v = plain[1][0][h // (Hq // Hkv)]
+        want = v[ahead:].mean(0)
+        assert_close(o[0, h * D:(h + 1) * D], want, UNIT["bf16"] * np.abs(want) + (UNIT["bf16"] + n * 2.0 ** -23) * np.abs(v).max(), f"head {h}")
