@@ -395,6 +395,39 @@ tern_status tern_linear_i8(const void* d_xq, const float* d_a, const void* d_til
                            void* d_ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Root-mean-square norm with the residual's addition: what stands before a
+ * decoder layer's linears.  The pages only name the layer; the definition is
+ *   s = x + r,   y[k] = s[k] / sqrt(mean_k s[k]^2 + eps) * (W[k] + w_add),
+ * in fp32 from the sum on, each output rounded once (y is formed from s before
+ * S is rounded).  w_add is 0, or 1 for models that store weights about zero.
+ * Rows: token t has H rows of K values beside one another, row h of X at
+ * t * ldx + h * K, so that H = 1 is the norm of the hidden state and H heads of
+ * dimension K, in the fused projection's output, are normalised one by one.
+ *   x_type   16-bit type of W and Y
+ *   in_type  type of X: tern_out_type (a linear's output serves as it is)
+ *   d_R      optional [T, ldr] of res_type, the residual stream
+ *   d_S      optional (with d_R only) [T, lds] of res_type: receives s; it may
+ *            be d_R or d_X, with the same type and leading dimension
+ *   d_W      device [K]; NULL: ones, and w_add is not used
+ *   d_Y      device [T, ldy]; it may be d_X, with the same type and leading
+ *            dimension (unless d_S is)
+ * K is a multiple of 8 up to 32768; data pointers are 16-byte aligned and every
+ * ld is a multiple of 8, at least H * K; eps and w_add are finite, eps not
+ * negative; T * H is at most 2^30.  T == 0 is a no-op. */
+tern_status tern_rms_norm(int x_type, int in_type, int64_t T, int64_t H, int64_t K, const void* d_X, int64_t ldx,
+                          int res_type, const void* d_R, int64_t ldr, void* d_S, int64_t lds, const void* d_W,
+                          float w_add, float eps, void* d_Y, int64_t ldy, void* stream);
+
+/* The same with int8 codes for tern_linear_i8: y is not rounded to 16 bits in
+ * between, and a[m] = max_k |y| / 127, q[m, k] = rint(y * (127 / max_k |y|)) are
+ * written as tern_quantize_x writes them (d_xq of tern_xq_bytes(M, K) bytes, d_a
+ * fp32 [M]).  A row that holds a NaN or an infinity gets a = NaN and codes 0.
+ * K is a multiple of 128 up to 32768. */
+tern_status tern_rms_norm_i8(int x_type, int in_type, int64_t M, int64_t K, const void* d_X, int64_t ldx, int res_type,
+                             const void* d_R, int64_t ldr, void* d_S, int64_t lds, const void* d_W, float w_add,
+                             float eps, void* d_xq, float* d_a, void* stream);
+
+/* ------------------------------------------------------------------------
  * Attention side of a decoder layer: rotary positions, the paged key/value
  * cache and attention.  The pages name them around the linear layer ([EMB]
  * §6: quantising the cache together with the kernel; [B27] and the other

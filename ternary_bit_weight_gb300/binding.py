@@ -7,7 +7,7 @@ tensors (their ``data_ptr()`` is passed) or raw integer addresses, and
 None (the current torch stream).  A non-zero status raises ``TernError``.
 If the library has not been built, importing this module raises.
 
-The attention-side calls go through a small extension module
+The attention-side calls and the norms go through a small extension module
 (csrc/tern_python.c) instead of ctypes, which converts their many arguments
 three times as fast; where it was not built for this interpreter (no Python
 headers), they go through ctypes to the same library.  The functions below are
@@ -42,7 +42,7 @@ EXPORTED = ("tern_status_string", "tern_version", "tern_pack", "tern_unpack", "t
             "tern_grouped_workspace_bytes", "tern_linear_grouped", "tern_repack_grouped",
             "tern_rope_freqs", "tern_rope", "tern_kv_write", "tern_rope_kv_write", "tern_kv_read",
             "tern_attn_prompt_workspace_bytes", "tern_attn_prompt", "tern_attn_decode_workspace_bytes",
-            "tern_attn_decode")
+            "tern_attn_decode", "tern_rms_norm", "tern_rms_norm_i8")
 
 MAX_GROUP = 8
 
@@ -152,6 +152,11 @@ def _load():
     lib.tern_attn_decode.argtypes = [i32, i32, i64, i64, i64, i64, f32, vp, i64, *cache, vp, i64, vp, vp, i64, vp, vp,
                                      sz, vp]
     lib.tern_attn_decode.restype = i32
+    norm = [vp, i64, i32, vp, i64, vp, i64, vp, f32, f32]
+    lib.tern_rms_norm.argtypes = [i32, i32, i64, i64, i64, *norm, vp, i64, vp]
+    lib.tern_rms_norm.restype = i32
+    lib.tern_rms_norm_i8.argtypes = [i32, i32, i64, i64, *norm, vp, vp, vp]
+    lib.tern_rms_norm_i8.restype = i32
     return lib
 
 
@@ -541,3 +546,17 @@ def tern_attn_decode(x_type: int, kv_type: int, B: int, Hq: int, Hkv: int, D: in
     _check(_native.tern_attn_decode(x_type, kv_type, B, Hq, Hkv, D, scale, Q, ldq, num_pages, page_size, kcache,
                                     vcache, kscale, vscale, page_table, max_pages, lens, O, ldo,
                                     lse, ws, ws_bytes, _s(stream)), "tern_attn_decode")
+
+
+def tern_rms_norm(x_type: int, in_type: int, T: int, H: int, K: int, X, ldx: int, res_type: int, R, ldr: int, S, lds: int,
+                  W, w_add: float, eps: float, Y, ldy: int, stream=None):
+    """Root-mean-square norm of T x H rows, with the residual's addition where R is given."""
+    _check(_native.tern_rms_norm(x_type, in_type, T, H, K, X, ldx, res_type, R, ldr, S, lds, W, w_add, eps, Y, ldy,
+                                 _s(stream)), "tern_rms_norm")
+
+
+def tern_rms_norm_i8(x_type: int, in_type: int, M: int, K: int, X, ldx: int, res_type: int, R, ldr: int, S, lds: int, W,
+                     w_add: float, eps: float, xq, a, stream=None):
+    """The same with int8 codes and a factor per row, as tern_linear_i8 takes them."""
+    _check(_native.tern_rms_norm_i8(x_type, in_type, M, K, X, ldx, res_type, R, ldr, S, lds, W, w_add, eps, xq, a,
+                                    _s(stream)), "tern_rms_norm_i8")

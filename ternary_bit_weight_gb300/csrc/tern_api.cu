@@ -49,6 +49,49 @@ size_t workspace_bytes(int64_t M, int64_t N, int64_t K) {
     return tern::plan_gemm(M, &N, &K, 1, sms).ws_bytes;
 }
 
+inline bool valid_elem(int type) { return type == TERN_OUT_F32 || type == TERN_OUT_BF16 || type == TERN_OUT_F16; }
+
+// Rows of a norm: input, residual stream and weights; fills everything but the
+// outputs.  *done: there are no rows.
+tern_status check_norm(int x_type, int in_type, int64_t T, int64_t H, int64_t K, const void* X, int64_t ldx, int res_type,
+                       const void* R, int64_t ldr, void* S, int64_t lds, const void* W, float w_add, float eps,
+                       tern::NormArgs* n, bool* done) {
+    constexpr int64_t kMost = int64_t(1) << 30, kMostLd = int64_t(1) << 40;
+    *done = false;
+    if ((x_type != TERN_X_BF16 && x_type != TERN_X_F16) || !valid_elem(in_type)) return TERN_ERR_SHAPE;
+    if (T < 0 || T > kMost || H < 1 || H > 4096 || T * H > kMost) return TERN_ERR_SHAPE;
+    if (K < 8 || K > tern::kNormMaxK || K % 8 != 0) return TERN_ERR_SHAPE;
+    if (!(eps >= 0.0f) || !(eps <= 3.4e38f) || !(w_add >= -3.4e38f && w_add <= 3.4e38f)) return TERN_ERR_SHAPE;
+    if ((R != nullptr || S != nullptr) && !valid_elem(res_type)) return TERN_ERR_SHAPE;
+    if (T == 0) {
+        *done = true;
+        return TERN_OK;
+    }
+    if (X == nullptr || (S != nullptr && R == nullptr)) return TERN_ERR_NULL;
+    if (ldx < H * K || ldx > kMostLd || (R != nullptr && (ldr < H * K || ldr > kMostLd)) ||
+        (S != nullptr && (lds < H * K || lds > kMostLd)))
+        return TERN_ERR_SHAPE;
+    if (!aligned(X, 16) || !aligned(R, 16) || !aligned(S, 16) || !aligned(W, 16)) return TERN_ERR_ALIGN;
+    if (ldx % 8 != 0 || (R != nullptr && ldr % 8 != 0) || (S != nullptr && lds % 8 != 0)) return TERN_ERR_ALIGN;
+    *n = {};
+    n->T = T;
+    n->H = H;
+    n->K = K;
+    n->x_type = in_type;
+    n->res_type = res_type;
+    n->y_f16 = x_type == TERN_X_F16;
+    n->x = X;
+    n->ldx = ldx;
+    n->r = R;
+    n->ldr = ldr;
+    n->s = S;
+    n->lds = lds;
+    n->w = static_cast<const uint16_t*>(W);
+    n->add = w_add;
+    n->eps = eps;
+    return TERN_OK;
+}
+
 tern_status check_x_w(const uint16_t* X, int64_t ldx, const void* tiled, int64_t M, int64_t K) {
     if (X == nullptr || tiled == nullptr) return TERN_ERR_NULL;
     if (ldx < K) return TERN_ERR_SHAPE;
@@ -431,6 +474,38 @@ tern_status tern_quantize_x(const void* d_X, int x_type, int64_t ldx, int64_t M,
     if (!aligned(d_X, 2) || !aligned(d_xq, 16) || !aligned(d_a, 4)) return TERN_ERR_ALIGN;
     return from_cuda(tern::launch_quantize_x(static_cast<const uint16_t*>(d_X), x_type == TERN_X_F16, ldx, M, K,
                                              static_cast<int8_t*>(d_xq), d_a, as_stream(stream)));
+}
+
+tern_status tern_rms_norm(int x_type, int in_type, int64_t T, int64_t H, int64_t K, const void* d_X, int64_t ldx,
+                          int res_type, const void* d_R, int64_t ldr, void* d_S, int64_t lds, const void* d_W,
+                          float w_add, float eps, void* d_Y, int64_t ldy, void* stream) {
+    tern::NormArgs n;
+    bool done;
+    const tern_status st = check_norm(x_type, in_type, T, H, K, d_X, ldx, res_type, d_R, ldr, d_S, lds, d_W, w_add, eps,
+                                      &n, &done);
+    if (st != TERN_OK || done) return st;
+    if (d_Y == nullptr) return TERN_ERR_NULL;
+    if (ldy < H * K || ldy > (int64_t(1) << 40)) return TERN_ERR_SHAPE;
+    if (!aligned(d_Y, 16) || ldy % 8 != 0) return TERN_ERR_ALIGN;
+    n.y = static_cast<uint16_t*>(d_Y);
+    n.ldy = ldy;
+    return from_cuda(tern::launch_norm(n, as_stream(stream)));
+}
+
+tern_status tern_rms_norm_i8(int x_type, int in_type, int64_t M, int64_t K, const void* d_X, int64_t ldx, int res_type,
+                             const void* d_R, int64_t ldr, void* d_S, int64_t lds, const void* d_W, float w_add,
+                             float eps, void* d_xq, float* d_a, void* stream) {
+    tern::NormArgs n;
+    bool done;
+    if (K % tern::kGroup != 0) return TERN_ERR_SHAPE;
+    const tern_status st = check_norm(x_type, in_type, M, 1, K, d_X, ldx, res_type, d_R, ldr, d_S, lds, d_W, w_add, eps,
+                                      &n, &done);
+    if (st != TERN_OK || done) return st;
+    if (d_xq == nullptr || d_a == nullptr) return TERN_ERR_NULL;
+    if (!aligned(d_xq, 16) || !aligned(d_a, 4)) return TERN_ERR_ALIGN;
+    n.q = static_cast<int8_t*>(d_xq);
+    n.a = d_a;
+    return from_cuda(tern::launch_norm(n, as_stream(stream)));
 }
 
 size_t tern_i8_workspace_bytes(int64_t M, int64_t N, int64_t K) {

@@ -148,6 +148,33 @@ cudaError_t launch_quantize_x(const uint16_t* X, bool x_f16, int64_t ldx, int64_
 cudaError_t launch_i8(const int8_t* xq, const float* a, const uint8_t* tiled, int64_t M, int64_t N,
                       const OutputSplit& out, void* ws, const I8Plan& plan, cudaStream_t stream);
 
+// ------------------------------------------------------------------ norms
+
+// Element types of a norm's input and residual stream.  Internal names of
+// tern_out_type.
+constexpr int kElemF32 = 0, kElemBf16 = 1, kElemF16 = 2;
+
+// Rows of K values, H beside one another for each of T tokens.
+struct NormArgs {
+    int64_t T, H, K;
+    int x_type, res_type;
+    bool y_f16;            // w and y: fp16, else bf16
+    const void* x;
+    int64_t ldx;
+    const void* r;         // optional, and s with it
+    int64_t ldr;
+    void* s;
+    int64_t lds;
+    const uint16_t* w;     // optional
+    float add, eps;
+    uint16_t* y;           // either 16-bit outputs
+    int64_t ldy;
+    int8_t* q;             // or codes and factors (quantize_x's layout)
+    float* a;
+};
+constexpr int64_t kNormMaxK = 32768;   // a row lies in the registers of one CTA
+cudaError_t launch_norm(const NormArgs& n, cudaStream_t stream);
+
 // -------------------------------------------------------- attention side
 
 // What a cache holds (kKvNone: no cache involved).  Internal names of

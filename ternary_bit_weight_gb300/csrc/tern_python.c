@@ -1,9 +1,9 @@
-/* Argument marshalling of the attention-side calls for Python: each function
- * takes the arguments of its namesake in tern.h, in order, and returns the
+/* Argument marshalling of the attention-side calls and the norms for Python: each
+ * function takes the arguments of its namesake in tern.h, in order, and returns the
  * status.  A pointer argument is None, an address or an object with a
  * data_ptr() method (a tensor).
  *
- * These calls take 18 to 28 arguments and are made for single tokens, where the
+ * These calls take 17 to 28 arguments and are made for single tokens, where the
  * GPU's part is 2 us: ctypes takes 1.8 us to convert the arguments and the
  * data_ptr() calls from Python another 0.9 us, against 0.5 us here. */
 #define PY_SSIZE_T_CLEAN
@@ -142,11 +142,26 @@ static PyObject* py_attn_decode(PyObject* self, PyObject* const* a, Py_ssize_t n
                                             (size_t)Q(22), P(23)));
 }
 
+static PyObject* py_rms_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    Slot s[18];
+    if (!parse(a, n, "iiqqqpqipqpqpffpqp", s)) return NULL;
+    CALL_AND_RETURN(tern_rms_norm(I(0), I(1), Q(2), Q(3), Q(4), P(5), Q(6), I(7), P(8), Q(9), P(10), Q(11), P(12), F(13),
+                                  F(14), P(15), Q(16), P(17)));
+}
+
+static PyObject* py_rms_norm_i8(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    Slot s[17];
+    if (!parse(a, n, "iiqqpqipqpqpffppp", s)) return NULL;
+    CALL_AND_RETURN(tern_rms_norm_i8(I(0), I(1), Q(2), Q(3), P(4), Q(5), I(6), P(7), Q(8), P(9), Q(10), P(11), F(12),
+                                     F(13), P(14), P(15), P(16)));
+}
+
 #define CALL(name) {"tern_" #name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, "tern_" #name " of tern.h"}
 static PyMethodDef g_methods[] = {CALL(rope),        CALL(kv_write),    CALL(rope_kv_write), CALL(kv_read),
-                                  CALL(attn_prompt), CALL(attn_decode), {NULL, NULL, 0, NULL}};
+                                  CALL(attn_prompt), CALL(attn_decode), CALL(rms_norm),      CALL(rms_norm_i8),
+                                  {NULL, NULL, 0, NULL}};
 
-static struct PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_tern_python", "libtern's attention-side calls", -1, g_methods,
+static struct PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_tern_python", "libtern's calls made per token", -1, g_methods,
                                       NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__tern_python(void) {
