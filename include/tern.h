@@ -588,6 +588,63 @@ tern_status tern_attn_decode(int x_type, int kv_type, int64_t B, int64_t Hq, int
                              const int32_t* d_page_table, int64_t max_pages, const int32_t* d_lens, void* d_O,
                              int64_t ldo, float* d_lse, void* d_ws, size_t ws_bytes, void* stream);
 
+/* Keeping a cache within a budget of tokens: each cached token's attention weight
+ * is accumulated, the tokens with the most are kept, and moved to the front of
+ * their sequence, whose last pages are then free.  Every key/value head keeps
+ * tokens of its own, the same number.  Keys were rotated when they were written, so
+ * a moved token keeps its position.
+ *
+ * The weights are one more plane of the cache: fp32, that of (page, head, row) at
+ * (page * Hkv + head) * page_size + row of d_weight. */
+
+/* Accumulate.  Sequence b has d_lens[b] cached tokens, the last nq of them those of
+ * its query rows [d_cu_q[b], d_cu_q[b+1]) of Tq (d_cu_q NULL: one row per sequence,
+ * Tq == B).  Row i sees the tokens j <= i + len - nq, as in tern_attn_prompt (causal)
+ * and tern_attn_decode; with d_lse [Tq, Hq] as those calls report it,
+ *   add[j, g] = sum over rows i that see j and query heads h of g of
+ *               exp(scale * Q[i, h].K[j, g] - lse[i, h]),
+ *   weight[j, g] = (j < d_known[b] ? decay * weight[j, g] : 0) + add[j, g].
+ * d_known (device int32 [B], NULL: all): tokens at or past it have no weight yet and
+ * what lies there is not read, so that a step of one token each passes lens - 1.
+ * A row with lse = -infinity saw nothing and adds nothing.  A sequence without rows
+ * or tokens is left as it is, and so are cells of no token.  Keys as tern_kv_read
+ * gives them before rounding; products, exponentials and sums are fp32, and the
+ * order of a sum does not depend on timing.  scale and decay are finite and not
+ * negative; offsets, lengths and page ids are read as tern_attn_prompt and
+ * tern_attn_decode read them.  The sequences of one call have different pages: a
+ * token that two of them share gets the weight of one. */
+tern_status tern_attn_weights(int x_type, int kv_type, int64_t B, const int32_t* d_cu_q, int64_t Tq, int64_t Hq,
+                              int64_t Hkv, int64_t D, float scale, const void* d_Q, int64_t ldq, const float* d_lse,
+                              int64_t num_pages, int64_t page_size, const void* d_kcache, const float* d_kscale,
+                              const int32_t* d_page_table, int64_t max_pages, const int32_t* d_lens,
+                              const int32_t* d_known, float decay, float* d_weight, void* stream);
+
+/* Choose.  A sequence of more than `budget` tokens keeps its first `first`, its last
+ * `recent`, and of the others those of the largest weight, of equal weights the
+ * earlier ones; a shorter one keeps all.  NaN weights and tokens of pages outside
+ * the cache come last.
+ *   d_keep      device int32 [B, Hkv, budget]: the kept tokens ascending, then -1
+ *   d_new_lens  device int32 [B]: min(len, budget); not d_lens
+ * budget at least 1 and first + recent, up to 2^30; B * Hkv up to 2^30. */
+tern_status tern_kv_keep(int64_t B, int64_t Hkv, int64_t num_pages, int64_t page_size, const float* d_weight,
+                         const int32_t* d_page_table, int64_t max_pages, const int32_t* d_lens, int64_t budget,
+                         int64_t first, int64_t recent, int32_t* d_keep, int32_t* d_new_lens, void* stream);
+
+/* Move.  Entry j of list (b, g) of d_keep [B, Hkv, budget], up to its first negative
+ * one, names the token that becomes token j: its key, value, factors and weight
+ * (d_weight NULL: none) go to row j % page_size of page d_to_table[b * to_pages +
+ * j / page_size].  d_to_table NULL (or d_page_table): in place, for lists that
+ * ascend strictly, as tern_kv_keep's do; a list that does not, or that names a token
+ * at or past max_pages * page_size, is left unmoved and counted in d_err (optional
+ * device int32).  With another table, which holds `budget` tokens, lists may be in
+ * any order, and no page that is written is read; the source stays as it is.
+ * Entries whose source or target page is outside the cache are skipped.  Sequences
+ * that share pages must not be compacted in place.  B * Hkv up to 2^25. */
+tern_status tern_kv_compact(int kv_type, int64_t B, int64_t Hkv, int64_t D, int64_t num_pages, int64_t page_size,
+                            void* d_kcache, void* d_vcache, float* d_kscale, float* d_vscale, float* d_weight,
+                            const int32_t* d_page_table, int64_t max_pages, const int32_t* d_keep, int64_t budget,
+                            const int32_t* d_to_table, int64_t to_pages, int32_t* d_err, void* stream);
+
 /* ------------------------------------------------------------------------
  * Workspace maintenance (library conveniences; the pages have none).
  * ---------------------------------------------------------------------- */

@@ -42,7 +42,8 @@ EXPORTED = ("tern_status_string", "tern_version", "tern_pack", "tern_unpack", "t
             "tern_grouped_workspace_bytes", "tern_linear_grouped", "tern_repack_grouped",
             "tern_rope_freqs", "tern_rope", "tern_kv_write", "tern_rope_kv_write", "tern_kv_read",
             "tern_attn_prompt_workspace_bytes", "tern_attn_prompt", "tern_attn_decode_workspace_bytes",
-            "tern_attn_decode", "tern_rms_norm", "tern_rms_norm_i8")
+            "tern_attn_decode", "tern_rms_norm", "tern_rms_norm_i8", "tern_attn_weights", "tern_kv_keep",
+            "tern_kv_compact")
 
 MAX_GROUP = 8
 
@@ -152,6 +153,13 @@ def _load():
     lib.tern_attn_decode.argtypes = [i32, i32, i64, i64, i64, i64, f32, vp, i64, *cache, vp, i64, vp, vp, i64, vp, vp,
                                      sz, vp]
     lib.tern_attn_decode.restype = i32
+    lib.tern_attn_weights.argtypes = [i32, i32, i64, vp, i64, i64, i64, i64, f32, vp, i64, vp, i64, i64, vp, vp, vp, i64, vp,
+                                      vp, f32, vp, vp]
+    lib.tern_attn_weights.restype = i32
+    lib.tern_kv_keep.argtypes = [i64, i64, i64, i64, vp, vp, i64, vp, i64, i64, i64, vp, vp, vp]
+    lib.tern_kv_keep.restype = i32
+    lib.tern_kv_compact.argtypes = [i32, i64, i64, i64, *cache, vp, vp, i64, vp, i64, vp, i64, vp, vp]
+    lib.tern_kv_compact.restype = i32
     norm = [vp, i64, i32, vp, i64, vp, i64, vp, f32, f32]
     lib.tern_rms_norm.argtypes = [i32, i32, i64, i64, i64, *norm, vp, i64, vp]
     lib.tern_rms_norm.restype = i32
@@ -560,3 +568,28 @@ def tern_rms_norm_i8(x_type: int, in_type: int, M: int, K: int, X, ldx: int, res
     """The same with int8 codes and a factor per row, as tern_linear_i8 takes them."""
     _check(_native.tern_rms_norm_i8(x_type, in_type, M, K, X, ldx, res_type, R, ldr, S, lds, W, w_add, eps, xq, a,
                                     _s(stream)), "tern_rms_norm_i8")
+
+
+def tern_attn_weights(x_type: int, kv_type: int, B: int, cu_q, Tq: int, Hq: int, Hkv: int, D: int, scale: float, Q, ldq: int,
+                      lse, num_pages: int, page_size: int, kcache, kscale, page_table, max_pages: int, lens, known,
+                      decay: float, weight, stream=None):
+    """Add the attention weight that cached tokens receive from their sequences' newest rows."""
+    _check(_native.tern_attn_weights(x_type, kv_type, B, cu_q, Tq, Hq, Hkv, D, scale, Q, ldq, lse, num_pages, page_size,
+                                     kcache, kscale, page_table, max_pages, lens, known, decay, weight, _s(stream)),
+           "tern_attn_weights")
+
+
+def tern_kv_keep(B: int, Hkv: int, num_pages: int, page_size: int, weight, page_table, max_pages: int, lens, budget: int,
+                 first: int, recent: int, keep, new_lens, stream=None):
+    """Choose the tokens of each sequence and head that stay in the cache."""
+    _check(_native.tern_kv_keep(B, Hkv, num_pages, page_size, weight, page_table, max_pages, lens, budget, first, recent,
+                                keep, new_lens, _s(stream)), "tern_kv_keep")
+
+
+def tern_kv_compact(kv_type: int, B: int, Hkv: int, D: int, num_pages: int, page_size: int, kcache, vcache, kscale, vscale,
+                    weight, page_table, max_pages: int, keep, budget: int, to_table=None, to_pages: int = 0, err=None,
+                    stream=None):
+    """Move the kept tokens to the front of their sequence."""
+    _check(_native.tern_kv_compact(kv_type, B, Hkv, D, num_pages, page_size, kcache, vcache, kscale, vscale, weight,
+                                   page_table, max_pages, keep, budget, to_table, to_pages, err, _s(stream)),
+           "tern_kv_compact")

@@ -15,6 +15,7 @@ constexpr int64_t kMaxHeads = 4096;
 constexpr int64_t kMaxHeadDim = 128;       // cache and attention
 constexpr int64_t kMaxRopeDim = 256;
 constexpr int64_t kMaxPageSize = 32768;
+constexpr int64_t kMaxMoves = int64_t(1) << 25;   // (sequence, head) pairs of one compaction
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
@@ -300,6 +301,95 @@ tern_status tern_attn_decode(int x_type, int kv_type, int64_t B, int64_t Hq, int
     a.ldo = ldo;
     a.lse = d_lse;
     return from_cuda(tern::launch_decode(x_type == TERN_X_F16, a, d_ws, sms, as_stream(stream)));
+}
+
+tern_status tern_attn_weights(int x_type, int kv_type, int64_t B, const int32_t* d_cu_q, int64_t Tq, int64_t Hq,
+                              int64_t Hkv, int64_t D, float scale, const void* d_Q, int64_t ldq, const float* d_lse,
+                              int64_t num_pages, int64_t page_size, const void* d_kcache, const float* d_kscale,
+                              const int32_t* d_page_table, int64_t max_pages, const int32_t* d_lens,
+                              const int32_t* d_known, float decay, float* d_weight, void* stream) {
+    int shift = 0;
+    if (!valid_x_type(x_type) || B < 0 || B > kMaxRows || Tq < 0 || Tq > kMaxRows) return TERN_ERR_SHAPE;
+    TERN_TRY(check_pages(kv_type, Hkv, D, num_pages, page_size, &shift));
+    if (!valid_heads(Hq) || Hq % Hkv != 0 || !valid_scale(scale) || !valid_scale(decay)) return TERN_ERR_SHAPE;
+    if (max_pages < 0 || max_pages > (INT32_MAX >> shift)) return TERN_ERR_SHAPE;
+    if (d_cu_q == nullptr && Tq != B) return TERN_ERR_SHAPE;
+    if (B == 0 || Tq == 0) return TERN_OK;
+    if (d_lse == nullptr || d_lens == nullptr || d_weight == nullptr || (max_pages > 0 && d_page_table == nullptr))
+        return TERN_ERR_NULL;
+    if (!aligned(d_cu_q, 4) || !aligned(d_lse, 4) || !aligned(d_lens, 4) || !aligned(d_known, 4) || !aligned(d_weight, 4) ||
+        !aligned(d_page_table, 4))
+        return TERN_ERR_ALIGN;
+    TERN_TRY(check_rows(d_Q, ldq, Hq, D));
+    TERN_TRY(check_cache(kv_type, d_kcache, d_kcache, d_kscale, d_kscale));
+    const int sms = tern::device_sm_count();
+    if (sms <= 0) return TERN_ERR_UNSUPPORTED;
+    tern::WeightsArgs w = {};
+    w.B = static_cast<int>(B);
+    w.cu_q = d_cu_q;
+    w.Tq = static_cast<int>(Tq);
+    w.Hq = static_cast<int>(Hq);
+    w.Hkv = static_cast<int>(Hkv);
+    w.D = static_cast<int>(D);
+    w.scale = scale;
+    w.decay = decay;
+    w.q = u16(d_Q);
+    w.ldq = ldq;
+    w.lse = d_lse;
+    w.cache = {kv_type, num_pages, shift, d_kcache, nullptr, d_kscale, nullptr};
+    w.table = d_page_table;
+    w.max_pages = max_pages;
+    w.lens = d_lens;
+    w.known = d_known;
+    w.weight = d_weight;
+    return from_cuda(tern::launch_weights(x_type == TERN_X_F16, w, sms, as_stream(stream)));
+}
+
+tern_status tern_kv_keep(int64_t B, int64_t Hkv, int64_t num_pages, int64_t page_size, const float* d_weight,
+                         const int32_t* d_page_table, int64_t max_pages, const int32_t* d_lens, int64_t budget,
+                         int64_t first, int64_t recent, int32_t* d_keep, int32_t* d_new_lens, void* stream) {
+    int shift = 0;
+    if (B < 0) return TERN_ERR_SHAPE;
+    TERN_TRY(check_pages(TERN_KV_X16, Hkv, kMaxHeadDim, num_pages, page_size, &shift));
+    if (B > kMaxRows / Hkv) return TERN_ERR_SHAPE;
+    if (max_pages < 0 || max_pages > (INT32_MAX >> shift)) return TERN_ERR_SHAPE;
+    if (budget < 1 || budget > kMaxRows || first < 0 || recent < 0 || first > budget || recent > budget - first)
+        return TERN_ERR_SHAPE;
+    if (B == 0) return TERN_OK;
+    if (d_weight == nullptr || d_lens == nullptr || d_keep == nullptr || d_new_lens == nullptr ||
+        (max_pages > 0 && d_page_table == nullptr))
+        return TERN_ERR_NULL;
+    if (!aligned(d_weight, 4) || !aligned(d_lens, 4) || !aligned(d_keep, 4) || !aligned(d_new_lens, 4) ||
+        !aligned(d_page_table, 4))
+        return TERN_ERR_ALIGN;
+    const tern::KeepCall c = {B, static_cast<int>(Hkv), num_pages, shift, d_weight, d_page_table, max_pages, d_lens,
+                              budget, first, recent, d_keep, d_new_lens};
+    return from_cuda(tern::launch_keep(c, as_stream(stream)));
+}
+
+tern_status tern_kv_compact(int kv_type, int64_t B, int64_t Hkv, int64_t D, int64_t num_pages, int64_t page_size,
+                            void* d_kcache, void* d_vcache, float* d_kscale, float* d_vscale, float* d_weight,
+                            const int32_t* d_page_table, int64_t max_pages, const int32_t* d_keep, int64_t budget,
+                            const int32_t* d_to_table, int64_t to_pages, int32_t* d_err, void* stream) {
+    int shift = 0;
+    if (B < 0) return TERN_ERR_SHAPE;
+    TERN_TRY(check_pages(kv_type, Hkv, D, num_pages, page_size, &shift));
+    if (B > kMaxMoves / Hkv) return TERN_ERR_SHAPE;
+    if (max_pages < 0 || max_pages > (INT32_MAX >> shift)) return TERN_ERR_SHAPE;
+    if (budget < 1 || budget > kMaxRows) return TERN_ERR_SHAPE;
+    if (d_to_table != nullptr && (to_pages < 0 || to_pages > (INT32_MAX >> shift) || (to_pages << shift) < budget))
+        return TERN_ERR_SHAPE;
+    if (d_to_table != nullptr && d_to_table == d_page_table && to_pages != max_pages) return TERN_ERR_SHAPE;
+    if (B == 0) return TERN_OK;
+    if (d_keep == nullptr || (max_pages > 0 && d_page_table == nullptr)) return TERN_ERR_NULL;
+    if (!aligned(d_weight, 4) || !aligned(d_keep, 4) || !aligned(d_page_table, 4) || !aligned(d_to_table, 4) ||
+        !aligned(d_err, 4))
+        return TERN_ERR_ALIGN;
+    TERN_TRY(check_cache(kv_type, d_kcache, d_vcache, d_kscale, d_vscale));
+    const tern::CompactCall c = {B, static_cast<int>(Hkv), static_cast<int>(D),
+                                 {kv_type, num_pages, shift, d_kcache, d_vcache, d_kscale, d_vscale},
+                                 d_weight, d_page_table, max_pages, d_keep, budget, d_to_table, to_pages, d_err};
+    return from_cuda(tern::launch_compact(c, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -194,18 +194,6 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <bool F16>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (F16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Transpose of an 8 x 8 matrix of 16-bit values, thread (g, t) holding
 // elements 2t, 2t + 1 of row g.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -214,11 +202,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // Count an arrival; what the CTA wrote before is visible to the CTAs that arrive
 // later, and theirs before to this one.
 __device__ __forceinline__ int arrive(int32_t* counter) {
@@ -244,25 +227,6 @@ __device__ __forceinline__ float log2_approx(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// The four codes of a word as two fp16 pairs, exactly.
-template <int KV>
-__device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    if constexpr (KV == kKvE4m3) {
-        const __half2 a = e4m3x2_to_half2(w & 0xFFFFu), b = e4m3x2_to_half2(w >> 16);
-        lo = *reinterpret_cast<const uint32_t*>(&a);
-        hi = *reinterpret_cast<const uint32_t*>(&b);
-    } else {
-        // byte + 128 in the low mantissa bits of 1024.0, less 1152
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
-        const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-        const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&x), bias);
-        const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&y), bias);
-        lo = *reinterpret_cast<const uint32_t*>(&a);
-        hi = *reinterpret_cast<const uint32_t*>(&b);
-    }
 }
 
 // One segment: the tiles [begin, end) of item (b, hv).

@@ -244,12 +244,6 @@ __device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t saddr, uint
 }
 constexpr uint32_t kBMnMajor = 1u << 16;   // instruction descriptor: B is MN-major
 
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Each lane with `active` set waits for its own barrier; the warp goes on when
 // all have completed.
 __device__ __forceinline__ bool vote_wait(uint32_t bar, uint32_t parity, bool active, volatile int* abort) {

@@ -255,6 +255,53 @@ struct DecodeArgs {
 size_t decode_ws_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_len, int sm_count);
 cudaError_t launch_decode(bool x_f16, const DecodeArgs& a, void* ws, int sm_count, cudaStream_t stream);
 
+struct WeightsArgs {
+    int B;
+    const int32_t* cu_q;      // optional: else one row per sequence
+    int Tq, Hq, Hkv, D;
+    float scale, decay;
+    const uint16_t* q;
+    int64_t ldq;
+    const float* lse;
+    KvCache cache;            // keys
+    const int32_t* table;
+    int64_t max_pages;
+    const int32_t* lens;
+    const int32_t* known;     // optional
+    float* weight;
+};
+cudaError_t launch_weights(bool x_f16, const WeightsArgs& w, int sm_count, cudaStream_t stream);
+
+struct KeepCall {
+    int64_t B;
+    int Hkv;
+    int64_t num_pages;
+    int page_shift;
+    const float* weight;
+    const int32_t* table;
+    int64_t max_pages;
+    const int32_t* lens;
+    int64_t budget, first, recent;
+    int32_t* keep;
+    int32_t* new_lens;
+};
+cudaError_t launch_keep(const KeepCall& c, cudaStream_t stream);
+
+struct CompactCall {
+    int64_t B;
+    int Hkv, D;
+    KvCache cache;
+    float* weight;            // optional
+    const int32_t* table;
+    int64_t max_pages;
+    const int32_t* keep;
+    int64_t budget;
+    const int32_t* to;        // optional: else in place
+    int64_t to_pages;
+    int32_t* err;             // optional
+};
+cudaError_t launch_compact(const CompactCall& c, cudaStream_t stream);
+
 // Every workspace begins with the error word (padded), and behind it the
 // counters of arrivals, which are zero between calls: 4 per SM for the
 // streaming kernel (a worker's row quarters), 2 for single-token attention (a

@@ -3,7 +3,7 @@
  * status.  A pointer argument is None, an address or an object with a
  * data_ptr() method (a tensor).
  *
- * These calls take 17 to 28 arguments and are made for single tokens, where the
+ * These calls take 14 to 28 arguments and are made for single tokens, where the
  * GPU's part is 2 us: ctypes takes 1.8 us to convert the arguments and the
  * data_ptr() calls from Python another 0.9 us, against 0.5 us here. */
 #define PY_SSIZE_T_CLEAN
@@ -156,9 +156,30 @@ static PyObject* py_rms_norm_i8(PyObject* self, PyObject* const* a, Py_ssize_t n
                                      F(13), P(14), P(15), P(16)));
 }
 
+static PyObject* py_attn_weights(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    Slot s[23];
+    if (!parse(a, n, "iiqpqqqqfpqpqqpppqppfpp", s)) return NULL;
+    CALL_AND_RETURN(tern_attn_weights(I(0), I(1), Q(2), P(3), Q(4), Q(5), Q(6), Q(7), F(8), P(9), Q(10), P(11), Q(12),
+                                      Q(13), P(14), P(15), P(16), Q(17), P(18), P(19), F(20), P(21), P(22)));
+}
+
+static PyObject* py_kv_keep(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    Slot s[14];
+    if (!parse(a, n, "qqqqppqpqqqppp", s)) return NULL;
+    CALL_AND_RETURN(tern_kv_keep(Q(0), Q(1), Q(2), Q(3), P(4), P(5), Q(6), P(7), Q(8), Q(9), Q(10), P(11), P(12), P(13)));
+}
+
+static PyObject* py_kv_compact(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    Slot s[19];
+    if (!parse(a, n, "iqqqqqppppppqpqpqpp", s)) return NULL;
+    CALL_AND_RETURN(tern_kv_compact(I(0), Q(1), Q(2), Q(3), Q(4), Q(5), P(6), P(7), P(8), P(9), P(10), P(11), Q(12), P(13),
+                                    Q(14), P(15), Q(16), P(17), P(18)));
+}
+
 #define CALL(name) {"tern_" #name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, "tern_" #name " of tern.h"}
 static PyMethodDef g_methods[] = {CALL(rope),        CALL(kv_write),    CALL(rope_kv_write), CALL(kv_read),
                                   CALL(attn_prompt), CALL(attn_decode), CALL(rms_norm),      CALL(rms_norm_i8),
+                                  CALL(attn_weights), CALL(kv_keep),    CALL(kv_compact),
                                   {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_tern_python", "libtern's calls made per token", -1, g_methods,
