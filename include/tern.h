@@ -612,12 +612,14 @@ tern_status tern_attn_decode(int x_type, int kv_type, int64_t B, int64_t Hq, int
  * order of a sum does not depend on timing.  scale and decay are finite and not
  * negative; offsets, lengths and page ids are read as tern_attn_prompt and
  * tern_attn_decode read them.  The sequences of one call have different pages: a
- * token that two of them share gets the weight of one. */
+ * token that two of them share gets the weight of one.  d_err (optional device
+ * int32) is set non-zero only if a pipeline wait timed out (2 s), which correct
+ * inputs never cause; the weights that were waited for are NaN then. */
 tern_status tern_attn_weights(int x_type, int kv_type, int64_t B, const int32_t* d_cu_q, int64_t Tq, int64_t Hq,
                               int64_t Hkv, int64_t D, float scale, const void* d_Q, int64_t ldq, const float* d_lse,
                               int64_t num_pages, int64_t page_size, const void* d_kcache, const float* d_kscale,
                               const int32_t* d_page_table, int64_t max_pages, const int32_t* d_lens,
-                              const int32_t* d_known, float decay, float* d_weight, void* stream);
+                              const int32_t* d_known, float decay, float* d_weight, int32_t* d_err, void* stream);
 
 /* Choose.  A sequence of more than `budget` tokens keeps its first `first`, its last
  * `recent`, and of the others those of the largest weight, of equal weights the

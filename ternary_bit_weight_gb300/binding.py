@@ -154,7 +154,7 @@ def _load():
                                      sz, vp]
     lib.tern_attn_decode.restype = i32
     lib.tern_attn_weights.argtypes = [i32, i32, i64, vp, i64, i64, i64, i64, f32, vp, i64, vp, i64, i64, vp, vp, vp, i64, vp,
-                                      vp, f32, vp, vp]
+                                      vp, f32, vp, vp, vp]
     lib.tern_attn_weights.restype = i32
     lib.tern_kv_keep.argtypes = [i64, i64, i64, i64, vp, vp, i64, vp, i64, i64, i64, vp, vp, vp]
     lib.tern_kv_keep.restype = i32
@@ -572,11 +572,11 @@ def tern_rms_norm_i8(x_type: int, in_type: int, M: int, K: int, X, ldx: int, res
 
 def tern_attn_weights(x_type: int, kv_type: int, B: int, cu_q, Tq: int, Hq: int, Hkv: int, D: int, scale: float, Q, ldq: int,
                       lse, num_pages: int, page_size: int, kcache, kscale, page_table, max_pages: int, lens, known,
-                      decay: float, weight, stream=None):
+                      decay: float, weight, err=None, stream=None):
     """Add the attention weight that cached tokens receive from their sequences' newest rows."""
     _check(_native.tern_attn_weights(x_type, kv_type, B, cu_q, Tq, Hq, Hkv, D, scale, Q, ldq, lse, num_pages, page_size,
-                                     kcache, kscale, page_table, max_pages, lens, known, decay, weight, _s(stream)),
-           "tern_attn_weights")
+                                     kcache, kscale, page_table, max_pages, lens, known, decay, weight, err,
+                                     _s(stream)), "tern_attn_weights")
 
 
 def tern_kv_keep(B: int, Hkv: int, num_pages: int, page_size: int, weight, page_table, max_pages: int, lens, budget: int,

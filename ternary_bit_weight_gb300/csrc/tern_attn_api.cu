@@ -307,7 +307,7 @@ tern_status tern_attn_weights(int x_type, int kv_type, int64_t B, const int32_t*
                               int64_t Hkv, int64_t D, float scale, const void* d_Q, int64_t ldq, const float* d_lse,
                               int64_t num_pages, int64_t page_size, const void* d_kcache, const float* d_kscale,
                               const int32_t* d_page_table, int64_t max_pages, const int32_t* d_lens,
-                              const int32_t* d_known, float decay, float* d_weight, void* stream) {
+                              const int32_t* d_known, float decay, float* d_weight, int32_t* d_err, void* stream) {
     int shift = 0;
     if (!valid_x_type(x_type) || B < 0 || B > kMaxRows || Tq < 0 || Tq > kMaxRows) return TERN_ERR_SHAPE;
     TERN_TRY(check_pages(kv_type, Hkv, D, num_pages, page_size, &shift));
@@ -318,7 +318,7 @@ tern_status tern_attn_weights(int x_type, int kv_type, int64_t B, const int32_t*
     if (d_lse == nullptr || d_lens == nullptr || d_weight == nullptr || (max_pages > 0 && d_page_table == nullptr))
         return TERN_ERR_NULL;
     if (!aligned(d_cu_q, 4) || !aligned(d_lse, 4) || !aligned(d_lens, 4) || !aligned(d_known, 4) || !aligned(d_weight, 4) ||
-        !aligned(d_page_table, 4))
+        !aligned(d_page_table, 4) || !aligned(d_err, 4))
         return TERN_ERR_ALIGN;
     TERN_TRY(check_rows(d_Q, ldq, Hq, D));
     TERN_TRY(check_cache(kv_type, d_kcache, d_kcache, d_kscale, d_kscale));
@@ -342,6 +342,7 @@ tern_status tern_attn_weights(int x_type, int kv_type, int64_t B, const int32_t*
     w.lens = d_lens;
     w.known = d_known;
     w.weight = d_weight;
+    w.err = d_err;
     return from_cuda(tern::launch_weights(x_type == TERN_X_F16, w, sms, as_stream(stream)));
 }
 

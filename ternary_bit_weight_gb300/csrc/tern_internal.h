@@ -269,6 +269,7 @@ struct WeightsArgs {
     const int32_t* lens;
     const int32_t* known;     // optional
     float* weight;
+    int32_t* err;             // optional
 };
 cudaError_t launch_weights(bool x_f16, const WeightsArgs& w, int sm_count, cudaStream_t stream);
 

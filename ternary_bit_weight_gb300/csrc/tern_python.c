@@ -157,10 +157,11 @@ static PyObject* py_rms_norm_i8(PyObject* self, PyObject* const* a, Py_ssize_t n
 }
 
 static PyObject* py_attn_weights(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    Slot s[23];
-    if (!parse(a, n, "iiqpqqqqfpqpqqpppqppfpp", s)) return NULL;
+    Slot s[24];
+    if (!parse(a, n, "iiqpqqqqfpqpqqpppqppfppp", s)) return NULL;
     CALL_AND_RETURN(tern_attn_weights(I(0), I(1), Q(2), P(3), Q(4), Q(5), Q(6), Q(7), F(8), P(9), Q(10), P(11), Q(12),
-                                      Q(13), P(14), P(15), P(16), Q(17), P(18), P(19), F(20), P(21), P(22)));
+                                      Q(13), P(14), P(15), P(16), Q(17), P(18), P(19), F(20), P(21), P(22),
+                                      P(23)));
 }
 
 static PyObject* py_kv_keep(PyObject* self, PyObject* const* a, Py_ssize_t n) {

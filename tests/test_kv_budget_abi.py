@@ -8,7 +8,7 @@ from test_attention_abi import ALIGN, FAKE, NULL, OK, SHAPE, call  # noqa: E402
 
 WEIGHTS = dict(x_type=0, kv_type=1, B=2, cu_q=FAKE, Tq=5, Hq=16, Hkv=8, D=128, scale=0.1, Q=FAKE, ldq=2048, lse=FAKE,
                num_pages=10, page_size=16, k=FAKE, ks=FAKE, table=FAKE, max_pages=7, lens=FAKE, known=FAKE, decay=1.0,
-               weight=FAKE, stream=None)
+               weight=FAKE, err=FAKE, stream=None)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -20,7 +20,8 @@ WEIGHTS = dict(x_type=0, kv_type=1, B=2, cu_q=FAKE, Tq=5, Hq=16, Hkv=8, D=128, s
     (dict(ks=None), NULL), (dict(table=None), NULL), (dict(lens=None), NULL), (dict(weight=None), NULL),
     (dict(Q=FAKE + 8), ALIGN), (dict(ldq=2052), ALIGN), (dict(lse=FAKE + 2), ALIGN), (dict(k=FAKE + 8), ALIGN),
     (dict(cu_q=FAKE + 2), ALIGN), (dict(known=FAKE + 1), ALIGN), (dict(weight=FAKE + 2), ALIGN), (dict(lens=FAKE + 2), ALIGN),
-    (dict(table=FAKE + 2), ALIGN), (dict(ks=FAKE + 1), ALIGN), (dict(B=0), OK), (dict(Tq=0), OK),
+    (dict(table=FAKE + 2), ALIGN), (dict(ks=FAKE + 1), ALIGN), (dict(err=FAKE + 2), ALIGN),
+    (dict(B=0), OK), (dict(Tq=0), OK),
     (dict(B=0, cu_q=None, Tq=0, Q=None, weight=None), OK)])
 def test_weights_refusals(change, status):
     assert call("tern_attn_weights", WEIGHTS, **change) == status
