@@ -23,52 +23,19 @@
 #include <math_constants.h>
 #include <string.h>
 
-#include "tern_attn.cuh"
-#include "tern_common.cuh"
-#include "tern_internal.h"
+#include "tern_attn_weights.cuh"
 
 namespace tern {
 namespace {
 
+using weights::Args;
+using weights::kLog2e;
+using weights::Sequence;
+using weights::sequence_at;
+using weights::tiles_of;
+
 constexpr int kWarps = 4;
 constexpr int kItemBytes = 8192;     // of keys, per item
-constexpr float kLog2e = 1.44269504088896340736f;
-
-struct Args {
-    const int32_t* cu_q;
-    const int32_t* lens;
-    const int32_t* known;
-    const int32_t* table;
-    const uint16_t* q;
-    const float* lse;
-    const uint8_t* k;
-    const float* kscale;
-    float* weight;
-    int32_t* err;
-    int64_t ldq, max_pages, num_pages;
-    int64_t capacity;      // max_pages * page_size
-    int B, Tq, Hq, Hkv, G, D;
-    int shift;
-    float scale2;          // scale * log2(e)
-    float decay;
-};
-
-struct Sequence {
-    int q0, nq, len;
-};
-__device__ __forceinline__ Sequence sequence_at(const Args& a, int b) {
-    Sequence s;
-    if (a.cu_q == nullptr) {
-        s.q0 = b;
-        s.nq = 1;
-    } else {
-        s.q0 = min(max(a.cu_q[b], 0), a.Tq);
-        s.nq = max(0, min(max(a.cu_q[b + 1], 0), a.Tq) - s.q0);
-    }
-    s.len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), a.capacity));
-    return s;
-}
-
 // A thread's part of 8 columns: operands of its column c0 + g, and what its scores'
 // columns c0 + 2t, c0 + 2t + 1 need.
 template <int DP>
@@ -156,11 +123,6 @@ __device__ __forceinline__ void multiply(const uint4 (&k0)[PIECES], const uint4 
             mma<kCoded || F16>(s[w & 1], o, q[p * kPer + w][0], q[p * kPer + w][1]);
         }
     }
-}
-
-// Tiles of `keys` keys of a sequence, over all its heads.
-__device__ __forceinline__ int64_t tiles_of(const Args& a, const Sequence& s, int keys) {
-    return s.nq == 0 ? 0 : static_cast<int64_t>((s.len + (keys - 1)) / keys) * a.Hkv;
 }
 
 // -------------------------------------------------- keys that come by TMA
@@ -625,6 +587,8 @@ cudaError_t launch_weights(bool x_f16, const WeightsArgs& w, int sm_count, cudaS
     a.D = w.D;
     a.scale2 = w.scale * kLog2e;
     a.decay = w.decay;
+    // many rows against many keys are the tensor cores' work
+    if (weights::rows_form(a)) return weights::launch_rows(x_f16, w.cache.kv, a, sm_count, stream);
     if (w.D > 64) return x_f16 ? launch_kind<128, true>(w.cache.kv, a, sm_count, stream) : launch_kind<128, false>(w.cache.kv, a, sm_count, stream);
     return x_f16 ? launch_kind<64, true>(w.cache.kv, a, sm_count, stream) : launch_kind<64, false>(w.cache.kv, a, sm_count, stream);
 }

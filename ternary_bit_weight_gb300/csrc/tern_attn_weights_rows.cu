@@ -1,0 +1,459 @@
+// Attention weight that cached tokens receive from many query rows: the form of
+// tern_attn_weights for windows of a prompt and whole prompts.
+//
+// Mathematics: as in tern_attn_weights.cu.  A key is a row of the product S = K Q^T
+// and a query row and head a column, so a thread that has a key adds up what it
+// receives without asking another.
+//
+// What bounds it: the tensor cores and beside them the exponential of every score
+// (16 a cycle and SM, against 26 scores of 128 dimensions from the tensor cores).
+//
+// Work.  An item is 128 keys of one (sequence, key/value head), against the columns
+// of all rows that see them, 192 or fewer at a time.  Items are dealt to one CTA per
+// SM, there and back, a sequence's first keys, which most rows see, first.  The keys
+// lie in tensor memory (codes exactly as 16-bit values, their factor being the
+// thread's), which leaves shared memory to the queries alone: two reads of it per
+// product would fill its bandwidth.
+//
+// Roles, each a loop over the CTA's items:
+//   warp 0       queries of a column tile by TMA, one box of heads x rows
+//   warp 1       tcgen05.mma, scores into one of two buffers of tensor memory
+//   warp 2       the columns' logarithms
+//   warps 4-7    keys, one per thread, into one of two buffers of tensor memory,
+//                an item ahead
+//   warps 8-15   exponentials and sums: a thread has a key and half of the columns
+// Every wait is bounded; after a timeout the weights not yet written become NaN.
+
+#include <float.h>
+#include <math_constants.h>
+#include <string.h>
+
+#include "tern_attn_weights.cuh"
+
+namespace tern {
+namespace weights {
+namespace {
+
+constexpr int kKeys = 128;               // of an item
+constexpr int kColumns = 192;            // of a column tile, at most
+constexpr int kThreads = 512;
+constexpr int kOffStages = 4;
+// Column tiles in shared memory; so many that one CTA fills an SM.
+template <int DP>
+constexpr int kQStagesOf = DP == 64 ? 6 : 3;
+constexpr int kHalfBytes = kColumns * 128;   // 64 dimensions of a column tile
+constexpr int kSCol = 128;               // tensor memory: two key buffers of 64 columns, two of scores
+constexpr int kTmemCols = 512;
+static_assert(kSCol + 2 * kColumns <= kTmemCols, "tensor-memory budget");
+
+// control block
+constexpr int kMostQStages = 6;
+constexpr int kBarQFull = 0, kBarQEmpty = kBarQFull + 8 * kMostQStages;
+constexpr int kBarOffFull = kBarQEmpty + 8 * kMostQStages, kBarOffEmpty = kBarOffFull + 8 * kOffStages;
+constexpr int kBarSFull = kBarOffEmpty + 8 * kOffStages, kBarSEmpty = kBarSFull + 16;
+constexpr int kBarKFull = kBarSEmpty + 16, kBarKEmpty = kBarKFull + 16;
+constexpr int kBarDrain = kBarKEmpty + 16;
+constexpr int kTmemPtr = kBarDrain + 8, kAbort = kTmemPtr + 4;
+constexpr int kPartial = 256;                          // [2][128] sums of the second halves
+constexpr int kOff = kPartial + 2 * kKeys * 4;         // [stages][columns]
+constexpr int kCtrlBytes = kOff + kOffStages * kColumns * 4;
+static_assert(kAbort + 4 <= kPartial, "control block");
+
+template <int DP>
+constexpr int smem_bytes() {
+    return 1024 + kQStagesOf<DP> * (DP / 64) * kHalfBytes + kCtrlBytes;
+}
+static_assert(smem_bytes<128>() <= 232448, "shared-memory budget");
+
+struct Maps {
+    CUtensorMap q;
+};
+
+// 128 keys of a sequence from j0, and the rows from i0 on that see some of them.
+struct Item {
+    int b, hk, j0, i0;
+    int q0, nq, len;
+};
+
+// The CTA's items in turn; one warp.
+struct Walker {
+    Sequence mine = {0, 0, 0};
+    int64_t incl = 0, base = 0, index;
+    int b0 = 0, round = 0;
+
+    __device__ __forceinline__ void load(const Args& a, int lane) {
+        mine = {0, 0, 0};
+        if (b0 + lane < a.B) mine = sequence_at(a, b0 + lane);
+        incl = tiles_of(a, mine, kKeys);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += up;
+        }
+    }
+    __device__ __forceinline__ Walker(const Args& a, int lane) { load(a, lane); }
+    __device__ __forceinline__ bool next(const Args& a, int lane, Item& o) {
+        index = static_cast<int64_t>(round) * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        ++round;
+        for (;;) {
+            const uint32_t past = __ballot_sync(0xffffffffu, base + incl > index);
+            if (past != 0) {
+                const int src = __ffs(past) - 1;
+                o.b = b0 + src;
+                o.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
+                o.nq = __shfl_sync(0xffffffffu, mine.nq, src);
+                o.len = __shfl_sync(0xffffffffu, mine.len, src);
+                const int64_t in = index - (base + __shfl_sync(0xffffffffu, incl, src)) +
+                                   static_cast<int64_t>((o.len + (kKeys - 1)) / kKeys) * a.Hkv;
+                const int64_t block = (in >> 32) == 0 ? static_cast<uint32_t>(in) / static_cast<uint32_t>(a.Hkv) : in / a.Hkv;
+                o.hk = static_cast<int>(in - block * a.Hkv);
+                o.j0 = static_cast<int>(block) * kKeys;
+                o.i0 = max(0, o.j0 - (o.len - o.nq));
+                return true;
+            }
+            base += __shfl_sync(0xffffffffu, incl, 31);
+            b0 += 32;
+            if (b0 >= a.B) return false;
+            load(a, lane);
+        }
+    }
+};
+
+// Four codes as two pairs of 16-bit values, exactly.
+template <int KV, bool F16>
+__device__ __forceinline__ void decode4_as(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (F16) {
+        decode4<KV>(w, lo, hi);
+    } else if constexpr (KV == kKvE4m3) {
+        decode4<KV>(w, lo, hi);
+        const float2 x = unpack_x2<true>(lo), y = unpack_x2<true>(hi);
+        lo = pack_x2<false>(x.x, x.y);
+        hi = pack_x2<false>(y.x, y.y);
+    } else {
+        // (128 + low 7 bits) - (128, or 256 where the code is negative)
+        const uint32_t u = w & 0x7F7F7F7Fu, n = w & 0x80808080u;
+        const uint32_t x = __byte_perm(u, 0x43434343u, 0x4140), y = __byte_perm(u, 0x43434343u, 0x4342);
+        const uint32_t bx = __byte_perm(n, 0x43434343u, 0x4140), by = __byte_perm(n, 0x43434343u, 0x4342);
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(bx));
+        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(by));
+    }
+}
+
+template <int DP, int KV, bool F16>
+__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args a,
+                                                           const int R) {
+    constexpr bool kCoded = KV != kKvX16;
+    constexpr int kQStages = kQStagesOf<DP>;
+    constexpr int kHalves = DP / 64, kStageBytes = kHalves * kHalfBytes;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sq = smem_u32(smem);
+    uint8_t* ctrl = smem + kQStages * kStageBytes;
+    const uint32_t cb = smem_u32(ctrl);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(ctrl + kAbort);
+    uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(ctrl + kTmemPtr);
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&maps.q);
+        for (int i = 0; i < kQStages; ++i) {
+            mbar_init(cb + kBarQFull + 8 * i, 1);
+            mbar_init(cb + kBarQEmpty + 8 * i, 1);
+        }
+        for (int i = 0; i < kOffStages; ++i) {
+            mbar_init(cb + kBarOffFull + 8 * i, 1);
+            mbar_init(cb + kBarOffEmpty + 8 * i, 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(cb + kBarSFull + 8 * i, 1);
+            mbar_init(cb + kBarSEmpty + 8 * i, 8);
+            mbar_init(cb + kBarKFull + 8 * i, 4);
+            mbar_init(cb + kBarKEmpty + 8 * i, 1);
+        }
+        mbar_init(cb + kBarDrain, 1);
+        *abort_flag = 0;
+        mbar_fence_init();
+    }
+    grid_dependency_wait();
+    // the next kernel is let in once this CTA has its tensor memory: one that took
+    // tensor memory first and then waited for this one would never get to run
+    if (warp == 3) {
+        tmem_alloc(smem_u32(tmem_ptr), kTmemCols);
+        tmem_relinquish();
+        grid_launch_dependents();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_ptr;
+    Item it;
+
+    if (warp == 0) {
+        // ------------------------------------------------------ queries
+        Walker walk(a, lane);
+        int n = 0;
+        bool ok = true;
+        while (ok && walk.next(a, lane, it)) {
+            for (int i = it.i0; ok && i < it.nq; i += R, ++n) {
+                const int st = n % kQStages;
+                ok = mbar_wait(cb + kBarQEmpty + 8 * st, (n / kQStages + 1) & 1, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t bar = cb + kBarQFull + 8 * st;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(bar, kHalves * R * a.G * 128);
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+                        tma_load_3d(sq + st * kStageBytes + h * kHalfBytes, &maps.q, 64 * h, it.hk * a.G, it.q0 + i, bar);
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) {   // let the copies land
+            volatile int no_abort = 0;
+            for (int i = n < kQStages ? 0 : n - kQStages; i < n; ++i)
+                (void)mbar_wait(cb + kBarQFull + 8 * (i % kQStages), (i / kQStages) & 1, &no_abort);
+        }
+    } else if (warp == 1) {
+        // ----------------------------------------------------- products
+        Walker walk(a, lane);
+        int n = 0, k = 0;
+        bool ok = true;
+        while (ok && walk.next(a, lane, it)) {
+            ok = __all_sync(0xffffffffu, mbar_wait(cb + kBarKFull + 8 * (k & 1), (k >> 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint32_t keys = tmem + (k & 1) * 64;
+            for (int i = it.i0; ok && i < it.nq; i += R, ++n) {
+                const int st = n % kQStages, sb = n & 1;
+                bool got = mbar_wait(cb + kBarQFull + 8 * st, (n / kQStages) & 1, abort_flag);
+                got = got && mbar_wait(cb + kBarSEmpty + 8 * sb, ((n >> 1) + 1) & 1, abort_flag);
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint32_t columns = (min(R, it.nq - i) * a.G + 15) & ~15;
+                const uint32_t idesc = F16 ? idesc_fp16_f32(128, columns) : idesc_bf16_f32(128, columns);
+                const uint64_t bd = smem_desc_kmajor_sw128(sq + st * kStageBytes);
+                if (elect_one()) {
+                    const int steps = a.D >> 4;
+                    for (int s = 0; s < steps; ++s)
+                        umma_bf16_tmem_a(tmem + kSCol + sb * kColumns, keys + 8 * s,
+                                         bd + (s >> 2) * (kHalfBytes >> 4) + (s & 3) * 2, idesc, s > 0);
+                    umma_commit(cb + kBarQEmpty + 8 * st);
+                    umma_commit(cb + kBarSFull + 8 * sb);
+                }
+                __syncwarp();
+            }
+            if (ok && elect_one()) umma_commit(cb + kBarKEmpty + 8 * (k & 1));
+            __syncwarp();
+            ++k;
+        }
+        if (!ok) {   // let the products finish
+            volatile int no_abort = 0;
+            if (elect_one()) umma_commit(cb + kBarDrain);
+            __syncwarp();
+            (void)mbar_wait(cb + kBarDrain, 0, &no_abort);
+        }
+    } else if (warp == 2) {
+        // --------------------------------------------------- logarithms
+        Walker walk(a, lane);
+        float* ring = reinterpret_cast<float*>(ctrl + kOff);
+        int n = 0;
+        bool ok = true;
+        while (ok && walk.next(a, lane, it)) {
+            for (int i = it.i0; i < it.nq; i += R, ++n) {
+                const int st = n % kOffStages, columns = min(R, it.nq - i) * a.G;
+                float x[kColumns / 32];
+#pragma unroll
+                for (int m = 0; m < kColumns / 32; ++m) {
+                    const uint32_t c = lane + 32 * m, r = c / static_cast<uint32_t>(a.G);
+                    x[m] = 0.0f;
+                    if (c < static_cast<uint32_t>(columns))
+                        x[m] = a.lse[(static_cast<int64_t>(it.q0) + i + r) * a.Hq + it.hk * a.G + (c - r * a.G)];
+                }
+                ok = __all_sync(0xffffffffu, mbar_wait(cb + kBarOffEmpty + 8 * st, (n / kOffStages + 1) & 1, abort_flag));
+                if (!ok) break;
+#pragma unroll
+                for (int m = 0; m < kColumns / 32; ++m)   // a row that saw nothing gives nothing
+                    ring[st * kColumns + lane + 32 * m] = x[m] == -CUDART_INF_F ? x[m] : -x[m] * kLog2e;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(cb + kBarOffFull + 8 * st);
+            }
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // --------------------------------------------------------- keys
+        Walker walk(a, lane);
+        constexpr int kWords = DP / 2;                       // of a key in tensor memory
+        constexpr int kRuns = DP * (kCoded ? 1 : 2) / 16;    // and in the cache
+        const uint32_t lanes = tmem + ((warp & 3) << 21);
+        const int bytes = a.D * (kCoded ? 1 : 2);
+        int k = 0;
+        bool ok = true;
+        while (ok && walk.next(a, lane, it)) {
+            const int key = it.j0 + 32 * (warp & 3) + lane;
+            const uint8_t* src = nullptr;
+            if (key < it.len) {
+                const int page = a.table[it.b * a.max_pages + (key >> a.shift)];
+                if (page >= 0 && page < a.num_pages)
+                    src = a.k + (((static_cast<int64_t>(page) * a.Hkv + it.hk) << a.shift) + (key & ((1 << a.shift) - 1))) * bytes;
+            }
+            uint4 u[kRuns];
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i)
+                u[i] = src != nullptr && 16 * i < bytes ? __ldg(reinterpret_cast<const uint4*>(src + 16 * i)) : make_uint4(0, 0, 0, 0);
+            ok = __all_sync(0xffffffffu, mbar_wait(cb + kBarKEmpty + 8 * (k & 1), ((k >> 1) + 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int h = 0; h < kWords / 32; ++h) {
+                uint32_t v[32];
+#pragma unroll
+                for (int i = 0; i < 32 / (kCoded ? 8 : 4); ++i) {
+                    const uint4& x = u[h * (kCoded ? 4 : 8) + i];
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (kCoded)
+                            decode4_as<KV, F16>(w[j], v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+                        else
+                            v[4 * i + j] = w[j];
+                    }
+                }
+                tmem_st_32x32b_x32(lanes + (k & 1) * 64 + 32 * h, v);
+            }
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(cb + kBarKFull + 8 * (k & 1));
+            ++k;
+        }
+    } else if (warp >= 8) {
+        // --------------------------------------------------------- sums
+        Walker walk(a, lane);
+        const int half = (warp - 8) >> 2, row = 32 * (warp & 3) + lane;
+        const uint32_t scores = tmem + kSCol + ((warp & 3) << 21);
+        float* partial = reinterpret_cast<float*>(ctrl + kPartial);
+        const float* ring = reinterpret_cast<const float*>(ctrl + kOff);
+        int n = 0, k = 0;
+        bool ok = true;
+        while (walk.next(a, lane, it)) {
+            const int key = it.j0 + row, before = it.len - it.nq;
+            int64_t cell = -1;
+            if (key < it.len) {
+                const int page = a.table[it.b * a.max_pages + (key >> a.shift)];
+                if (page >= 0 && page < a.num_pages)
+                    cell = ((static_cast<int64_t>(page) * a.Hkv + it.hk) << a.shift) + (key & ((1 << a.shift) - 1));
+            }
+            float f = a.scale2, old = 0.0f;
+            if (kCoded && cell >= 0) f *= a.kscale[cell];
+            bool had = false;
+            if (half == 0 && cell >= 0) {
+                had = key < (a.known == nullptr ? it.len : a.known[it.b]);
+                if (had) old = a.weight[cell];
+            }
+            float sum = 0.0f;
+            for (int i = it.i0; i < it.nq; i += R, ++n) {
+                const int st = n % kOffStages, sb = n & 1;
+                const int columns = min(R, it.nq - i) * a.G;
+                const bool full = it.j0 + kKeys - 1 <= before + i;   // every row of the tile sees every key
+                const int first = max(0, key - before - i) * a.G;    // column from which the key is seen
+                bool got = ok && mbar_wait(cb + kBarOffFull + 8 * st, (n / kOffStages) & 1, abort_flag);
+                got = got && mbar_wait(cb + kBarSFull + 8 * sb, (n >> 1) & 1, abort_flag);
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
+                tc_fence_after_sync();
+                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+                for (int c = half * (kColumns / 2); c < min(columns, (half + 1) * (kColumns / 2)); c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32_sync(scores + sb * kColumns + c, v);
+                    const float4* off = reinterpret_cast<const float4*>(ring + st * kColumns + c);
+                    if (full && c + 32 <= columns) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 o = off[j];
+                            part[0] += exp2_approx(fmaf(__uint_as_float(v[4 * j]), f, o.x));
+                            part[1] += exp2_approx(fmaf(__uint_as_float(v[4 * j + 1]), f, o.y));
+                            part[2] += exp2_approx(fmaf(__uint_as_float(v[4 * j + 2]), f, o.z));
+                            part[3] += exp2_approx(fmaf(__uint_as_float(v[4 * j + 3]), f, o.w));
+                        }
+                    } else {
+                        const int lo = first - c, hi = columns - c;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 o4 = off[j];
+                            const float o[4] = {o4.x, o4.y, o4.z, o4.w};
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                const float p = exp2_approx(fmaf(__uint_as_float(v[4 * j + m]), f, o[m]));
+                                part[m] += 4 * j + m >= lo && 4 * j + m < hi ? p : 0.0f;
+                            }
+                        }
+                    }
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(cb + kBarSEmpty + 8 * sb);
+                    mbar_arrive(cb + kBarOffEmpty + 8 * st);
+                }
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
+            }
+            if (!ok) sum = CUDART_NAN_F;
+            if (half == 1) partial[(k & 1) * kKeys + row] = sum;
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (half == 0 && cell >= 0) {
+                sum += partial[(k & 1) * kKeys + row];
+                a.weight[cell] = had ? fmaf(a.decay, old, sum) : sum;
+            }
+            ++k;
+        }
+    }
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0 && a.err != nullptr) atomicOr(a.err, 1);
+    if (warp == 3) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int DP, int KV, bool F16>
+cudaError_t launch(const Args& a, int sm_count, cudaStream_t stream) {
+    const int R = kColumns / a.G;
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    const EncodeTiledFn enc = encode_tiled_fn();
+    if (enc == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.Tq)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.D) * 2, static_cast<cuuint64_t>(a.ldq) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(R)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (enc(&maps.q, F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<uint16_t*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    static OncePerDevice once;
+    const cudaError_t limit = allow_smem(once, rows_kernel<DP, KV, F16>, smem_bytes<DP>());
+    if (limit != cudaSuccess) return limit;
+    const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * ceil_div(a.capacity, kKeys);
+    const dim3 grid(static_cast<unsigned>(items < 1 ? 1 : items < sm_count ? items : sm_count));
+    return launch_after(rows_kernel<DP, KV, F16>, grid, kThreads, smem_bytes<DP>(), stream, maps, a, R);
+}
+
+template <int DP, bool F16>
+cudaError_t launch_kind(int kv, const Args& a, int sm_count, cudaStream_t stream) {
+    if (kv == kKvX16) return launch<DP, kKvX16, F16>(a, sm_count, stream);
+    if (kv == kKvE4m3) return launch<DP, kKvE4m3, F16>(a, sm_count, stream);
+    return launch<DP, kKvI8, F16>(a, sm_count, stream);
+}
+
+}  // namespace
+
+bool rows_form(const Args& a) {
+    // the tensor map's stride stays below 2^40 bytes
+    return a.G <= kColumns && a.ldq < (int64_t(1) << 39) && static_cast<int64_t>(a.Tq) * a.G > static_cast<int64_t>(a.B) * 16;
+}
+
+cudaError_t launch_rows(bool x_f16, int kv, const Args& a, int sm_count, cudaStream_t stream) {
+    if (a.D > 64) return x_f16 ? launch_kind<128, true>(kv, a, sm_count, stream) : launch_kind<128, false>(kv, a, sm_count, stream);
+    return x_f16 ? launch_kind<64, true>(kv, a, sm_count, stream) : launch_kind<64, false>(kv, a, sm_count, stream);
+}
+
+}  // namespace weights
+}  // namespace tern
