@@ -244,45 +244,6 @@ __device__ __forceinline__ uint64_t smem_desc_mnmajor_sw128(uint32_t saddr, uint
 }
 constexpr uint32_t kBMnMajor = 1u << 16;   // instruction descriptor: B is MN-major
 
-// Each lane with `active` set waits for its own barrier; the warp goes on when
-// all have completed.
-__device__ __forceinline__ bool vote_wait(uint32_t bar, uint32_t parity, bool active, volatile int* abort) {
-    uint64_t t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (__all_sync(0xffffffffu, !active || mbar_test_wait(bar, parity))) return true;
-        if ((i & 255u) == 0) {
-            if (__any_sync(0xffffffffu, *abort != 0)) return false;
-            const uint64_t t = global_timer_ns();
-            if (t0 == 0) {
-                t0 = t;
-            } else if (__any_sync(0xffffffffu, t - t0 > kWaitTimeoutNs)) {
-                *abort = 1;
-                return false;
-            }
-        }
-    }
-}
-
-// Two fp32 values in one register pair, and arithmetic on both.
-__device__ __forceinline__ uint64_t pair(float x, float y) {
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
-    return p;
-}
-__device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
-}
-__device__ __forceinline__ uint64_t fma_x2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add_x2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // acc + 0 * w on both halves: a non-finite half makes its sum NaN for good.
 template <bool F16>
 __device__ __forceinline__ uint32_t times_zero(uint32_t w, uint32_t acc) {

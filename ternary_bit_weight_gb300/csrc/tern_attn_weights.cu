@@ -542,8 +542,7 @@ cudaError_t launch_stream(const Args& a, int sm_count, cudaStream_t stream) {
 
 template <int DP, int KV, bool F16>
 cudaError_t launch(const Args& a, int sm_count, cudaStream_t stream) {
-    // tiles' halves of 16 keys that lie in one page, and (page, head) counts that fit a coordinate
-    if (a.shift >= 4 && a.num_pages > 0 && a.num_pages * a.Hkv <= INT32_MAX)
+    if (weights::by_tma(a))
         return a.G <= 8 ? launch_stream<DP, KV, F16, 1>(a, sm_count, stream) : launch_stream<DP, KV, F16, 2>(a, sm_count, stream);
     constexpr int kKeys = kItemBytes / (DP * (KV == kKvX16 ? 2 : 1));
     const int64_t items = static_cast<int64_t>(a.B) * a.Hkv * ceil_div(a.capacity, kKeys);

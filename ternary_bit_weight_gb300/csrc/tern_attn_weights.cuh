@@ -50,6 +50,10 @@ __device__ __forceinline__ int64_t tiles_of(const Args& a, const Sequence& s, in
     return s.nq == 0 ? 0 : static_cast<int64_t>((s.len + (keys - 1)) / keys) * a.Hkv;
 }
 
+// Whether keys come by TMA, 16 at a time: they lie in one page, and the (page, head)
+// count fits a coordinate.
+inline bool by_tma(const Args& a) { return a.shift >= 4 && a.num_pages > 0 && a.num_pages * a.Hkv <= INT32_MAX; }
+
 // Whether the form for many rows takes the call, and that form.
 bool rows_form(const Args& a);
 cudaError_t launch_rows(bool x_f16, int kv, const Args& a, int sm_count, cudaStream_t stream);

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_ptr;
-    Item it;
+    Item it = {};
 
     if (warp == 0) {
         // ------------------------------------------------------ queries
@@ -216,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     } else if (warp == 1) {
         // ----------------------------------------------------- products
         Walker walk(a, lane);
+        const int steps = a.D >> 4;
         int n = 0, k = 0;
         bool ok = true;
         while (ok && walk.next(a, lane, it)) {
@@ -225,19 +226,20 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             const uint32_t keys = tmem + (k & 1) * 64;
             for (int i = it.i0; ok && i < it.nq; i += R, ++n) {
                 const int st = n % kQStages, sb = n & 1;
-                bool got = mbar_wait(cb + kBarQFull + 8 * st, (n / kQStages) & 1, abort_flag);
-                got = got && mbar_wait(cb + kBarSEmpty + 8 * sb, ((n >> 1) + 1) & 1, abort_flag);
-                ok = __all_sync(0xffffffffu, got);
+                // one vote for both: a wait costs some 170 cycles even where nothing is waited for
+                ok = vote_wait(lane == 0 ? cb + kBarQFull + 8 * st : cb + kBarSEmpty + 8 * sb,
+                               lane == 0 ? (n / kQStages) & 1 : ((n >> 1) + 1) & 1, lane < 2, abort_flag);
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint32_t columns = (min(R, it.nq - i) * a.G + 15) & ~15;
                 const uint32_t idesc = F16 ? idesc_fp16_f32(128, columns) : idesc_bf16_f32(128, columns);
                 const uint64_t bd = smem_desc_kmajor_sw128(sq + st * kStageBytes);
                 if (elect_one()) {
-                    const int steps = a.D >> 4;
-                    for (int s = 0; s < steps; ++s)
-                        umma_bf16_tmem_a(tmem + kSCol + sb * kColumns, keys + 8 * s,
-                                         bd + (s >> 2) * (kHalfBytes >> 4) + (s & 3) * 2, idesc, s > 0);
+#pragma unroll
+                    for (int s = 0; s < DP / 16; ++s)
+                        if (s < steps)
+                            umma_bf16_tmem_a(tmem + kSCol + sb * kColumns, keys + 8 * s, bd + (s >> 2) * (kHalfBytes >> 4) + (s & 3) * 2,
+                                             idesc, s > 0);
                     umma_commit(cb + kBarQEmpty + 8 * st);
                     umma_commit(cb + kBarSFull + 8 * sb);
                 }
@@ -255,28 +257,57 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         }
     } else if (warp == 2) {
         // --------------------------------------------------- logarithms
+        // Loaded two tiles ahead: they come from L2, 1000 cycles away, and a tile takes not
+        // much more.
+        constexpr int kAhead = 3, kEach = kColumns / 32;
         Walker walk(a, lane);
-        float* ring = reinterpret_cast<float*>(ctrl + kOff);
-        int n = 0;
-        bool ok = true;
-        while (ok && walk.next(a, lane, it)) {
-            for (int i = it.i0; i < it.nq; i += R, ++n) {
-                const int st = n % kOffStages, columns = min(R, it.nq - i) * a.G;
-                float x[kColumns / 32];
+        float* ring = reinterpret_cast<float*>(ctrl + kOff) + lane;
+        int64_t place[kEach];   // of the lane's columns among the logarithms of a tile
+        int row[kEach];
 #pragma unroll
-                for (int m = 0; m < kColumns / 32; ++m) {
-                    const uint32_t c = lane + 32 * m, r = c / static_cast<uint32_t>(a.G);
-                    x[m] = 0.0f;
-                    if (c < static_cast<uint32_t>(columns))
-                        x[m] = a.lse[(static_cast<int64_t>(it.q0) + i + r) * a.Hq + it.hk * a.G + (c - r * a.G)];
+        for (int e = 0; e < kEach; ++e) {
+            row[e] = (lane + 32 * e) / static_cast<uint32_t>(a.G);
+            place[e] = static_cast<int64_t>(row[e]) * a.Hq + (lane + 32 * e - row[e] * a.G);
+        }
+        const float* src = nullptr;
+        float x[kAhead][kEach];
+        int left = 0, have = 0, n = 0;   // rows of the item from the next tile on
+        bool more = true, ok = true;
+        auto load = [&](float (&y)[kEach]) {
+            if (left <= 0 && more) {
+                more = walk.next(a, lane, it);
+                if (more) {
+                    left = it.nq - it.i0;
+                    src = a.lse + (static_cast<int64_t>(it.q0) + it.i0) * a.Hq + it.hk * a.G;
                 }
+            }
+            if (!more) return;
+            const int rows = min(R, left);
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) y[e] = row[e] < rows ? src[place[e]] : 0.0f;
+            src += static_cast<int64_t>(R) * a.Hq;
+            left -= R;
+            ++have;
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead - 1; ++i) load(x[i]);
+        while (ok && n < have) {
+            // (by turns, not moved along: a number that is moved is waited for)
+#pragma unroll
+            for (int now = 0; now < kAhead; ++now) {
+                if (!ok || n >= have) break;
+                load(x[(now + kAhead - 1) % kAhead]);
+                const int st = n % kOffStages;
                 ok = __all_sync(0xffffffffu, mbar_wait(cb + kBarOffEmpty + 8 * st, (n / kOffStages + 1) & 1, abort_flag));
                 if (!ok) break;
 #pragma unroll
-                for (int m = 0; m < kColumns / 32; ++m)   // a row that saw nothing gives nothing
-                    ring[st * kColumns + lane + 32 * m] = x[m] == -CUDART_INF_F ? x[m] : -x[m] * kLog2e;
+                for (int e = 0; e < kEach; ++e) {   // a row that saw nothing gives nothing
+                    const float l = x[now][e];
+                    ring[st * kColumns + 32 * e] = l == -CUDART_INF_F ? l : -l * kLog2e;
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(cb + kBarOffFull + 8 * st);
+                ++n;
             }
         }
     } else if (warp >= 4 && warp < 8) {
@@ -361,32 +392,31 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok) break;
                 tc_fence_after_sync();
-                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                uint64_t part[2] = {0, 0};   // pairs of sums
+                const uint64_t ff = pair(f, f);
 #pragma unroll 1
                 for (int c = half * (kColumns / 2); c < min(columns, (half + 1) * (kColumns / 2)); c += 32) {
                     uint32_t v[32];
                     tmem_ld32_sync(scores + sb * kColumns + c, v);
-                    const float4* off = reinterpret_cast<const float4*>(ring + st * kColumns + c);
+                    const ulonglong2* off = reinterpret_cast<const ulonglong2*>(ring + st * kColumns + c);
                     if (full && c + 32 <= columns) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 o = off[j];
-                            part[0] += exp2_approx(fmaf(__uint_as_float(v[4 * j]), f, o.x));
-                            part[1] += exp2_approx(fmaf(__uint_as_float(v[4 * j + 1]), f, o.y));
-                            part[2] += exp2_approx(fmaf(__uint_as_float(v[4 * j + 2]), f, o.z));
-                            part[3] += exp2_approx(fmaf(__uint_as_float(v[4 * j + 3]), f, o.w));
+                        for (int j = 0; j < 16; ++j) {
+                            const ulonglong2 o = off[j / 2];
+                            float x0, x1;
+                            unpair(fma_x2(pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), ff, j & 1 ? o.y : o.x), x0, x1);
+                            part[j & 1] = add_x2(part[j & 1], pair(exp2_approx(x0), exp2_approx(x1)));
                         }
                     } else {
                         const int lo = first - c, hi = columns - c;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 o4 = off[j];
-                            const float o[4] = {o4.x, o4.y, o4.z, o4.w};
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const float p = exp2_approx(fmaf(__uint_as_float(v[4 * j + m]), f, o[m]));
-                                part[m] += 4 * j + m >= lo && 4 * j + m < hi ? p : 0.0f;
-                            }
+                        for (int j = 0; j < 16; ++j) {
+                            const ulonglong2 o = off[j / 2];
+                            float x0, x1;
+                            unpair(fma_x2(pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), ff, j & 1 ? o.y : o.x), x0, x1);
+                            x0 = 2 * j >= lo && 2 * j < hi ? exp2_approx(x0) : 0.0f;
+                            x1 = 2 * j + 1 >= lo && 2 * j + 1 < hi ? exp2_approx(x1) : 0.0f;
+                            part[j & 1] = add_x2(part[j & 1], pair(x0, x1));
                         }
                     }
                 }
@@ -396,7 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     mbar_arrive(cb + kBarSEmpty + 8 * sb);
                     mbar_arrive(cb + kBarOffEmpty + 8 * st);
                 }
-                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                float p0, p1;
+                unpair(add_x2(part[0], part[1]), p0, p1);
+                sum += p0 + p1;
             }
             if (!ok) sum = CUDART_NAN_F;
             if (half == 1) partial[(k & 1) * kKeys + row] = sum;
@@ -447,7 +479,7 @@ cudaError_t launch_kind(int kv, const Args& a, int sm_count, cudaStream_t stream
 
 bool rows_form(const Args& a) {
     // the tensor map's stride stays below 2^40 bytes
-    return a.G <= kColumns && a.ldq < (int64_t(1) << 39) && static_cast<int64_t>(a.Tq) * a.G > static_cast<int64_t>(a.B) * 16;
+    return by_tma(a) && a.G <= kColumns && a.ldq < (int64_t(1) << 39) && static_cast<int64_t>(a.Tq) * a.G > static_cast<int64_t>(a.B) * 16;
 }
 
 cudaError_t launch_rows(bool x_f16, int kv, const Args& a, int sm_count, cudaStream_t stream) {
