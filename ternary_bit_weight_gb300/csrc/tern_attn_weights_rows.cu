@@ -447,7 +447,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
 
 template <int DP, int KV, bool F16>
 cudaError_t launch(const Args& a, int sm_count, cudaStream_t stream) {
-    const int R = kColumns / a.G;
+    // rows of a column tile: as many as fit, spread evenly over a sequence's tiles
+    const int64_t fit = kColumns / a.G, rows = ceil_div(a.Tq, a.B);
+    const int R = static_cast<int>(rows < fit ? rows : ceil_div(rows, ceil_div(rows, fit)));
     Maps maps;
     memset(&maps, 0, sizeof(maps));
     const EncodeTiledFn enc = encode_tiled_fn();

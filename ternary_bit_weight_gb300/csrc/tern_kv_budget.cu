@@ -3,14 +3,21 @@
 //
 // Mathematics.  Weights become 32-bit keys in the order of the numbers (a NaN, or
 // a token of a page outside the cache, below all of them).  The smallest kept key
-// is found digit by digit, 8 bits at a time, by counting; of the tokens that have
-// it the first ones are kept.  Counts are whole numbers, so the result does not
-// depend on the order of the atomics.
+// is found digit by digit, 8 bits of its distance from the smallest key at a time, by
+// counting; of the tokens that have it the first ones are kept.  Counts are whole
+// numbers, so the result does not depend on the order of the atomics.  What bounds the
+// choice: a chain of loads, counts and votes per row.  (512 of 577 tokens of 8 heads 4.0 us,
+// 4096 of 8192 of 512 rows 33 us; digits of the keys themselves, whose counts meet in few
+// places, and 128 registers a thread 52 us.)
 //
 // Moves.  A list of kept tokens ascends, so entry j is at or behind place j: tokens
 // taken in order, a block of places at a time, never write what a later block
 // still reads.  A CTA has one (sequence, head) and a slice of the row's bytes, reads
 // a block of tokens, meets, and writes it; slices do not touch one another's bytes.
+// What bounds the moves: DRAM, and that a block's list, page table and data follow from
+// one another, which many CTAs on an SM hide (32 sequences of 8192 to 4096 tokens in bf16
+// 205 us, 5.3 TB/s read and written; with the next block's loads ahead in registers fewer CTAs
+// fit and it took 257 to 336, with whole rows instead of 64 bytes 249).
 
 #include <float.h>
 
@@ -32,20 +39,25 @@ struct KeepArgs {
     int64_t max_pages, num_pages, capacity, budget;
     int first, recent;
     int Hkv, shift;
-    int stored;            // tokens whose keys fit in shared memory
 };
 
-// Order of the numbers; -0 is 0.
+// Keys in the order of the numbers, -0 being 0, between 1 (NaN, or a hidden token)
+// and that of infinity.
+constexpr uint32_t kAbsent = 0, kLowest = 1, kMust = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t order_key(float w) {
-    if (w != w) return 0;
+    if (w != w) return kLowest;
     const uint32_t u = __float_as_uint(w == 0.0f ? 0.0f : w);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(1024) keep_kernel(const KeepArgs a) {
-    extern __shared__ uint32_t keys[];
-    __shared__ uint32_t bins[256];
-    __shared__ uint32_t found[2];          // digit, and how many above it
+// A thread's tokens lie 32 apart in its warp's run of tokens, so that loads are
+// coalesced and a warp lists its tokens in order with votes.  EACH keys of a thread
+// stay in registers; EACH == 0: more tokens than that, each pass loads them again.
+// Every warp works out a digit by itself from the counts, so a digit costs one barrier.
+template <int EACH, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) keep_kernel(const KeepArgs a) {
+    __shared__ __align__(16) uint32_t bins[4][256];
+    __shared__ uint32_t ends[2][32];       // per warp: smallest and largest key
     __shared__ int above[32], equal[32];   // per warp
     grid_launch_dependents();
     grid_dependency_wait();
@@ -61,103 +73,122 @@ __global__ void __launch_bounds__(1024) keep_kernel(const KeepArgs a) {
         return;
     }
     const int page_mask = (1 << a.shift) - 1;
-    auto load = [&](int j) -> uint32_t {
-        const int page = a.table[b * a.max_pages + (j >> a.shift)];
-        if (page < 0 || page >= a.num_pages) return 0;
-        return order_key(a.weight[((static_cast<int64_t>(page) * a.Hkv + hk) << a.shift) + (j & page_mask)]);
-    };
-    for (int j = threadIdx.x; j < min(len, a.stored); j += blockDim.x) keys[j] = load(j);
-    auto key = [&](int j) { return j < a.stored ? keys[j] : load(j); };
-
-    // the key of which `take` are left to keep when all above it are kept
+    const int32_t* table = a.table + b * a.max_pages;
     const int lo = a.first, hi = len - a.recent;
-    uint32_t take = static_cast<uint32_t>(kept - a.first - a.recent), prefix = 0;
-    if (take > 0) {
-        for (int at = 24; at >= 0; at -= 8) {
-            __syncthreads();   // (the first time: the keys are there)
-            for (int i = threadIdx.x; i < 256; i += blockDim.x) bins[i] = 0;
-            __syncthreads();
-            const uint32_t known = at == 24 ? 0u : 0xFFFFFFFFu << (at + 8);
-            for (int j = lo + threadIdx.x; j < hi; j += blockDim.x) {
-                const uint32_t k = key(j);
-                if ((k & known) == prefix) atomicAdd(&bins[(k >> at) & 255], 1u);
-            }
-            __syncthreads();
-            if (warp == 0) {
-                // lane l has digits 255 - 8l - 7 .. 255 - 8l, the largest first
-                uint32_t c[8], mine = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mine += c[i] = bins[255 - 8 * lane - i];
-                uint32_t incl = mine;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
-                    if (lane >= d) incl += up;
-                }
-                uint32_t before = incl - mine;
-                if (before < take && incl >= take) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (before < take && before + c[i] >= take) {
-                            found[0] = 255 - 8 * lane - i;
-                            found[1] = before;
-                        }
-                        before += c[i];
-                    }
-                }
-            }
-            __syncthreads();
-            prefix |= found[0] << at;
-            take -= found[1];
-        }
-    } else {
-        prefix = 0xFFFFFFFFu;   // no key has it
-        __syncthreads();
-    }
-
-    // each warp lists a run of tokens in order
+    // the warp's run of tokens [j0, j1)
     const int run = ((len + warps - 1) / warps + 31) & ~31;
     const int j0 = min(len, warp * run), j1 = min(len, j0 + run);
-    auto kind = [&](int j, bool& over, bool& same) {
-        over = same = false;
-        if (j >= j1) return;
-        if (j < lo || j >= hi) {
-            over = true;
-            return;
-        }
-        const uint32_t k = key(j);
-        over = k > prefix;
-        same = k == prefix;
+    auto page_of = [&](int j) { return j < j1 ? table[j >> a.shift] : -1; };
+    auto load = [&](int j, int page) -> uint32_t {
+        const bool there = page >= 0 && page < a.num_pages;
+        float w = 0.0f;
+        if (there) w = a.weight[((static_cast<int64_t>(page) * a.Hkv + hk) << a.shift) + (j & page_mask)];
+        return j >= j1 ? kAbsent : j < lo || j >= hi ? kMust : there ? order_key(w) : kLowest;
     };
-    int n_over = 0, n_same = 0;
-    for (int j = j0; j < j1; j += 32) {
-        bool over, same;
-        kind(j + lane, over, same);
-        n_over += __popc(__ballot_sync(0xffffffffu, over));
-        n_same += __popc(__ballot_sync(0xffffffffu, same));
+    uint32_t keys[EACH == 0 ? 1 : EACH];
+    if constexpr (EACH > 0) {
+        constexpr int kAtOnce = EACH < 16 ? EACH : 16;
+#pragma unroll
+        for (int i0 = 0; i0 < EACH; i0 += kAtOnce) {
+            int pages[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) pages[i] = page_of(j0 + 32 * (i0 + i) + lane);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) keys[i0 + i] = load(j0 + 32 * (i0 + i) + lane, pages[i]);
+        }
     }
+    for (int i = threadIdx.x; i < 4 * 256; i += blockDim.x) bins[0][i] = 0;
+    // what(j, key) for the thread's tokens, the whole warp together
+    auto each = [&](auto&& what) {
+        if constexpr (EACH > 0) {
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) what(j0 + 32 * i + lane, keys[i]);
+        } else {
+            for (int j = j0; j < j1; j += 32) what(j + lane, load(j + lane, page_of(j + lane)));
+        }
+    };
+    // the key of which `take` are left to keep when all above it are kept: digits of the
+    // distance from the smallest key, so that the first ones are spread over the counts
+    uint32_t take = static_cast<uint32_t>(kept - a.first - a.recent), prefix = kMust - 1;   // take == 0: no key has it
+    if (take > 0) {
+        // (one less and one more, so that kAbsent and kMust are out of the way)
+        uint32_t least = 0xFFFFFFFFu, most = 0;
+        each([&](int, uint32_t k) {
+            least = min(least, k - 1);
+            most = max(most, k + 1);
+        });
+        least = __reduce_min_sync(0xffffffffu, least);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) ends[0][warp] = least, ends[1][warp] = most;
+        __syncthreads();   // (and the counts are zero)
+        least = __reduce_min_sync(0xffffffffu, lane < warps ? ends[0][lane] : 0xFFFFFFFFu) + 1;
+        most = __reduce_max_sync(0xffffffffu, lane < warps ? ends[1][lane] : 0u) - 1;
+        prefix = least;
+        uint32_t span = most - least;        // keys looked at: prefix to prefix + span
+        int at = 32 - __clz(span);           // bits that are not known yet
+        for (int turn = 0; at > 0; ++turn) {
+            at = max(0, at - 8);
+            uint32_t* count = bins[turn];
+            each([&](int, uint32_t k) {
+                if (k - prefix <= span) atomicAdd(&count[(k - prefix) >> at], 1u);
+            });
+            __syncthreads();
+            // lane l has digits 255 - 8l - 7 .. 255 - 8l, the largest first
+            uint32_t c[8], mine = 0;
+            const uint4 c0 = *reinterpret_cast<const uint4*>(count + 248 - 8 * lane), c1 = *reinterpret_cast<const uint4*>(count + 252 - 8 * lane);
+            c[7] = c0.x, c[6] = c0.y, c[5] = c0.z, c[4] = c0.w, c[3] = c1.x, c[2] = c1.y, c[1] = c1.z, c[0] = c1.w;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mine += c[i];
+            uint32_t incl = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t up = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += up;
+            }
+            // the first lane whose count passes `take` has the digit
+            const int src = __ffs(__ballot_sync(0xffffffffu, incl >= take)) - 1;
+            uint32_t before = incl - mine, digit = 0, over = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (before < take && before + c[i] >= take) {
+                    digit = 255 - 8 * lane - i;
+                    over = before;
+                }
+                before += c[i];
+            }
+            prefix += __shfl_sync(0xffffffffu, digit, src) << at;
+            take -= __shfl_sync(0xffffffffu, over, src);
+            span = min(most - prefix, (1u << at) - 1);
+        }
+    }
+
+    int n_over = 0, n_same = 0;
+    each([&](int, uint32_t k) {
+        n_over += __popc(__ballot_sync(0xffffffffu, k > prefix));
+        n_same += __popc(__ballot_sync(0xffffffffu, k == prefix));
+    });
     if (lane == 0) above[warp] = n_over, equal[warp] = n_same;
     __syncthreads();
-    int over_before = 0, same_before = 0;
-    for (int w = 0; w < warp; ++w) over_before += above[w], same_before += equal[w];
+    // what the warps before list
+    int over_before = lane < warp ? above[lane] : 0, same_before = lane < warp ? equal[lane] : 0;
+    over_before = __reduce_add_sync(0xffffffffu, over_before);
+    same_before = __reduce_add_sync(0xffffffffu, same_before);
     int place = over_before + min(same_before, static_cast<int>(take));
     const uint32_t below = (1u << lane) - 1;
-    for (int j = j0; j < j1; j += 32) {
-        bool over, same;
-        kind(j + lane, over, same);
+    each([&](int j, uint32_t k) {
+        const bool same = k == prefix;
         const uint32_t sames = __ballot_sync(0xffffffffu, same);
-        const bool in = over || (same && same_before + __popc(sames & below) < static_cast<int>(take));
+        const bool in = k > prefix || (same && same_before + __popc(sames & below) < static_cast<int>(take));
         const uint32_t ins = __ballot_sync(0xffffffffu, in);
-        if (in) out[place + __popc(ins & below)] = j + lane;
+        if (in) out[place + __popc(ins & below)] = j;
         place += __popc(ins);
         same_before += __popc(sames);
-    }
+    });
 }
 
 // --------------------------------------------------------------------- moves
 
-constexpr int kMoveThreads = 256;
-constexpr int kUnroll = 4;         // tokens of a thread in a block of places
+constexpr int kUnroll = 2;         // tokens of a thread in a block of places
 
 struct MoveArgs {
     const int32_t* table;
@@ -178,10 +209,10 @@ struct MoveArgs {
 };
 
 // Runs of 16 bytes of the keys (or values) of one head, or its fp32 numbers.
-template <typename T>
+template <int THREADS, typename T>
 __device__ __forceinline__ void move(const MoveArgs& a, T* data, int64_t row_bytes, int64_t at, bool live, int width, int b, int hk,
                                      int start, int count) {
-    const int per = kMoveThreads / width;           // tokens at a time
+    const int per = THREADS / width;           // tokens at a time
     const int me = threadIdx.x / static_cast<uint32_t>(width);
     const int page_mask = (1 << a.shift) - 1;
     const int32_t* list = a.keep + (static_cast<int64_t>(b) * a.Hkv + hk) * a.budget;
@@ -215,7 +246,8 @@ __device__ __forceinline__ void move(const MoveArgs& a, T* data, int64_t row_byt
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveArgs a) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) move_kernel(const MoveArgs a) {
     __shared__ int moved, ends, bad;
     grid_launch_dependents();
     grid_dependency_wait();
@@ -232,7 +264,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveArgs a) {
     // the first entry that moves, the list's end, and whether it is one
     const int budget = static_cast<int>(a.budget);
     int my_moved = INT32_MAX, my_end = budget;
-    for (int j = threadIdx.x; j < budget; j += kMoveThreads)
+    for (int j = threadIdx.x; j < budget; j += THREADS)
         if (list[j] < 0) {
             my_end = j;
             break;
@@ -241,7 +273,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveArgs a) {
     __syncthreads();
     const int count = ends;
     bool wrong = false;
-    for (int j = threadIdx.x; j < count; j += kMoveThreads) {
+    for (int j = threadIdx.x; j < count; j += THREADS) {
         const int at = list[j];
         if (at >= a.capacity || (a.in_place && j > 0 && list[j - 1] >= at)) wrong = true;
         if (at != j && my_moved == INT32_MAX) my_moved = j;
@@ -258,11 +290,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveArgs a) {
         const int slice = part < a.slices ? part : part - a.slices;
         const int run = slice * a.lanes + threadIdx.x % a.lanes;
         uint8_t* data = part < a.slices ? a.k : a.v;
-        move(a, reinterpret_cast<uint4*>(data), a.bytes, 16 * run, 16 * run < a.bytes, a.lanes, b, hk, start, count);
+        move<THREADS>(a, reinterpret_cast<uint4*>(data), a.bytes, 16 * run, 16 * run < a.bytes, a.lanes, b, hk, start, count);
     } else {
-        if (a.kscale != nullptr) move(a, a.kscale, 4, 0, true, 1, b, hk, start, count);
-        if (a.vscale != nullptr) move(a, a.vscale, 4, 0, true, 1, b, hk, start, count);
-        if (a.weight != nullptr) move(a, a.weight, 4, 0, true, 1, b, hk, start, count);
+        if (a.kscale != nullptr) move<THREADS>(a, a.kscale, 4, 0, true, 1, b, hk, start, count);
+        if (a.vscale != nullptr) move<THREADS>(a, a.vscale, 4, 0, true, 1, b, hk, start, count);
+        if (a.weight != nullptr) move<THREADS>(a, a.weight, 4, 0, true, 1, b, hk, start, count);
     }
 }
 
@@ -283,13 +315,15 @@ cudaError_t launch_keep(const KeepCall& c, cudaStream_t stream) {
     a.recent = static_cast<int>(c.recent);
     a.Hkv = c.Hkv;
     a.shift = c.page_shift;
-    constexpr int kMostStored = 49152;
-    a.stored = static_cast<int>(a.capacity < kMostStored ? a.capacity : kMostStored);
-    static OncePerDevice once;
-    const cudaError_t limit = allow_smem(once, keep_kernel, kMostStored * 4);
-    if (limit != cudaSuccess) return limit;
-    const unsigned threads = a.capacity <= 2048 ? 256 : a.capacity <= 8192 ? 512 : 1024;
-    return launch_after(keep_kernel, dim3(static_cast<unsigned>(c.B * c.Hkv)), threads, static_cast<size_t>(a.stored) * 4, stream, a);
+    // registers for every token that there may be; small sequences in few threads
+    const dim3 grid(static_cast<unsigned>(c.B * c.Hkv));
+    if (a.capacity <= 1024) return launch_after(keep_kernel<4, 256>, grid, 256, 0, stream, a);
+    if (a.capacity <= 2048) return launch_after(keep_kernel<8, 256>, grid, 256, 0, stream, a);
+    if (a.capacity <= 4096) return launch_after(keep_kernel<16, 256>, grid, 256, 0, stream, a);
+    if (a.capacity <= 8192) return launch_after(keep_kernel<32, 256>, grid, 256, 0, stream, a);
+    if (a.capacity <= 16384) return launch_after(keep_kernel<32, 512>, grid, 512, 0, stream, a);
+    if (a.capacity <= 32768) return launch_after(keep_kernel<32, 1024>, grid, 1024, 0, stream, a);
+    return launch_after(keep_kernel<0, 1024>, grid, 1024, 0, stream, a);
 }
 
 cudaError_t launch_compact(const CompactCall& c, cudaStream_t stream) {
@@ -313,9 +347,15 @@ cudaError_t launch_compact(const CompactCall& c, cudaStream_t stream) {
     a.in_place = a.to == a.table;
     a.bytes = c.D * (c.cache.kv == kKvX16 ? 2 : 1);
     const int runs = a.bytes / 16;
-    a.lanes = 4;
+    // slices of 64 bytes, of 32 where there are few CTAs
+    a.lanes = c.B * c.Hkv * 2 * ceil_div(runs, 4) < 2 * static_cast<int64_t>(device_sm_count()) ? 2 : 4;
     a.slices = static_cast<int>(ceil_div(runs, a.lanes));
-    return launch_after(move_kernel, dim3(static_cast<unsigned>(c.B * c.Hkv * (2 * a.slices + 1))), kMoveThreads, 0, stream, a);
+    const int64_t ctas = c.B * c.Hkv * (2 * a.slices + 1);
+    const dim3 grid(static_cast<unsigned>(ctas));
+    // (tokens of fp8 codes, one sequence of 577: 4.3 us with 256 threads, 3.7 with 512; 32 of
+    // 8192 in bf16: 205 and 218)
+    if (ctas < 2 * static_cast<int64_t>(device_sm_count())) return launch_after(move_kernel<512>, grid, 512, 0, stream, a);
+    return launch_after(move_kernel<256>, grid, 256, 0, stream, a);
 }
 
 }  // namespace tern
