@@ -9,11 +9,19 @@ then decoding steps, with ternary projections and an 8-bit paged cache.
   decoding step:     o = tern_attn_decode(q, cache)
   y = tern_linear_ex(o)                         ternary projection
 
+With --norm the block begins with the norm of its input (tern_rms_norm).  With
+--budget N the cache is kept at N tokens from the first decoding step on: after
+each step the tokens' weights are accumulated (tern_attn_weights), and where a
+sequence has grown past the budget the tokens of the least weight leave
+(tern_kv_keep, tern_kv_compact); the comparison with 64 bits is then left out, since
+the attention is no longer over all tokens.
+
 Every step runs on the GPU through libtern; the script prints the times and
 compares the last decoding step with the same block computed from the formulas
 in 64 bits (--check, on by default).
 
     python examples/attention_block.py [--seqs 4] [--prompt 1500] [--part 512] [--steps 8] [--cache e4m3]
+                                       [--norm] [--budget 1024]
 """
 import argparse
 import os
@@ -71,6 +79,7 @@ class Cache:
         order = torch.randperm(self.pages, generator=torch.Generator().manual_seed(0))
         self.table = order.to(torch.int32).reshape(seqs, self.per).to(dev)
         self.lens = torch.zeros(seqs, dtype=torch.int32, device=dev)
+        self.weight = torch.zeros(shape[:3], device=dev)
 
     def slots(self, seq, position):
         """Slots of tokens at `position` [n] of sequences `seq` [n]."""
@@ -82,7 +91,13 @@ class Cache:
 
 
 class Block:
-    def __init__(self, kind, seqs, longest, dev):
+    def __init__(self, kind, seqs, longest, dev, norm=False, budget=None):
+        self.norm = torch.linspace(0.5, 1.5, HIDDEN, device=dev).to(torch.bfloat16) if norm else None
+        self.budget = budget
+        if budget:
+            self.keep = torch.empty((seqs, HKV, budget), dtype=torch.int32, device=dev)
+            self.known = torch.zeros(seqs, dtype=torch.int32, device=dev)   # tokens that have a weight
+        self.position = torch.zeros(seqs, dtype=torch.int64, device=dev)        # tokens so far, kept or not
         self.qkv, self.o = Linear("qkv", dev), Linear("o", dev)
         self.cache = Cache(kind, seqs, longest, dev)
         freq, self.amplitude = tb.tern_rope_freqs(D, 1e6, tb.TERN_ROPE_SCALE_PARTS, 4.0, 8192.0)
@@ -90,13 +105,37 @@ class Block:
         self.ws_decode = torch.zeros(tb.tern_attn_decode_workspace_bytes(seqs, HQ, HKV, D, self.cache.per * PAGE),
                                      dtype=torch.uint8, device=dev)
 
-    def store(self, qkv, seq, position):
-        """Rotated queries; the keys and values go to the cache."""
+    def project(self, x):
+        """Queries, keys and values of the (normalised) input."""
+        if self.norm is not None:
+            y = torch.empty_like(x)
+            tb.tern_rms_norm(tb.TERN_X_BF16, tb.TERN_OUT_BF16, x.shape[0], 1, HIDDEN, x, HIDDEN, tb.TERN_OUT_BF16, None, 0, None, 0,
+                             self.norm, 0.0, 1e-6, y, HIDDEN)
+            x = y
+        return self.qkv(x)
+
+    def accumulate(self, q, lse, cu):
+        """Add what the newest rows' queries gave to the tokens' weights."""
+        c = self.cache
+        tb.tern_attn_weights(tb.TERN_X_BF16, c.kind, c.lens.numel(), cu, q.shape[0], HQ, HKV, D, SCALE, q, HQ * D, lse, c.pages, PAGE,
+                             c.k, c.ks, c.table, c.per, c.lens, self.known, 1.0, c.weight)
+        self.known.copy_(c.lens)
+
+    def shrink(self):
+        """Keep the tokens with the most weight, and half of the budget's newest."""
+        c, seqs = self.cache, self.known.numel()
+        tb.tern_kv_keep(seqs, HKV, c.pages, PAGE, c.weight, c.table, c.per, c.lens, self.budget, min(4, self.budget // 2),
+                        self.budget // 2, self.keep, self.known)
+        tb.tern_kv_compact(c.kind, seqs, HKV, D, *c.arguments, c.weight, c.table, c.per, self.keep, self.budget)
+        c.lens.copy_(self.known)
+
+    def store(self, qkv, seq, position, place):
+        """Rotated queries; the keys and values go to the cache as tokens `place` of `seq`."""
         t, ld = qkv.shape
         q = torch.empty((t, HQ * D), dtype=qkv.dtype, device=qkv.device)
         tb.tern_rope_kv_write(tb.TERN_X_BF16, self.cache.kind, tb.TERN_ROPE_HALF, t, HQ, HKV, D, D,
                               position.to(torch.int32), self.freq, self.amplitude, qkv, ld, q, HQ * D,
-                              qkv[:, HQ * D:], ld, qkv[:, (HQ + HKV) * D:], ld, self.cache.slots(seq, position),
+                              qkv[:, HQ * D:], ld, qkv[:, (HQ + HKV) * D:], ld, self.cache.slots(seq, place),
                               *self.cache.arguments)
         return q
 
@@ -106,7 +145,9 @@ class Block:
         seqs = c.lens.numel()
         past = int(c.lens[0])                      # prompts of one length here
         seq = torch.arange(seqs, device=dev).repeat_interleave(new)
-        q = self.store(self.qkv(x), seq, past + torch.arange(new, device=dev).repeat(seqs))
+        place = past + torch.arange(new, device=dev).repeat(seqs)
+        q = self.store(self.project(x), seq, place, place)
+        self.position += new
         c.lens += new
         total = past + new
         # all keys and values so far, packed by sequence
@@ -117,25 +158,36 @@ class Block:
         o = torch.empty((x.shape[0], HQ * D), dtype=x.dtype, device=dev)
         cu = torch.arange(seqs + 1, dtype=torch.int32, device=dev)
         ws = torch.zeros(tb.tern_attn_prompt_workspace_bytes(seqs, x.shape[0], rows, HQ, HKV, D), dtype=torch.uint8, device=dev)
+        lse = torch.empty((x.shape[0], HQ), device=dev) if self.budget else None
         tb.tern_attn_prompt(tb.TERN_X_BF16, seqs, cu * new, cu * total, x.shape[0], rows, HQ, HKV, D, True, SCALE,
-                            q, HQ * D, k, HKV * D, v, HKV * D, o, HQ * D, None, ws)
+                            q, HQ * D, k, HKV * D, v, HKV * D, o, HQ * D, lse, ws)
+        if self.budget:
+            self.accumulate(q, lse, cu * new)
         return self.o(o)
 
     def step(self, x):
         """x [seqs, hidden]: one new token of every sequence."""
         c = self.cache
-        q = self.store(self.qkv(x), torch.arange(c.lens.numel(), device=x.device), c.lens.long())
+        q = self.store(self.project(x), torch.arange(c.lens.numel(), device=x.device), self.position, c.lens.long())
+        self.position += 1
         c.lens += 1
         o = torch.empty((x.shape[0], HQ * D), dtype=x.dtype, device=x.device)
+        lse = torch.empty((x.shape[0], HQ), device=x.device) if self.budget else None
         tb.tern_attn_decode(tb.TERN_X_BF16, c.kind, x.shape[0], HQ, HKV, D, SCALE, q, HQ * D, *c.arguments, c.table, c.per,
-                            c.lens, o, HQ * D, None, self.ws_decode)
+                            c.lens, o, HQ * D, lse, self.ws_decode)
+        if self.budget:
+            self.accumulate(q, lse, None)
+            self.shrink()
         return self.o(o)
 
 
 def reference(block, xs):
     """The last token's output of every sequence in 64 bits, nothing rounded: xs [seqs, tokens, hidden]."""
     seqs, n, _ = xs.shape
-    qkv = xs.double() @ block.qkv.dense.T
+    x = xs.double()
+    if block.norm is not None:
+        x = x / torch.sqrt((x * x).mean(-1, keepdim=True) + 1e-6) * block.norm.double()
+    qkv = x @ block.qkv.dense.T
     angle = torch.arange(n, device=xs.device).double()[:, None] * block.freq.double()
     c, s = angle.cos()[:, None] * block.amplitude, angle.sin()[:, None] * block.amplitude
     heads = qkv.reshape(seqs, n, HQ + 2 * HKV, D)
@@ -148,9 +200,10 @@ def reference(block, xs):
     return o @ block.o.dense.T
 
 
-def run(seqs=4, prompt=1500, part=512, steps=8, cache="e4m3", check=True, out=print):
+def run(seqs=4, prompt=1500, part=512, steps=8, cache="e4m3", check=True, out=print, norm=False, budget=None):
     dev = torch.device("cuda:0")
-    block = Block(cache, seqs, prompt + steps, dev)
+    check = check and not budget
+    block = Block(cache, seqs, prompt + steps, dev, norm, budget)
     gen = torch.Generator(device=dev).manual_seed(1)
     xs = torch.randn((seqs, prompt + steps, HIDDEN), generator=gen, device=dev).to(torch.bfloat16)
 
@@ -176,6 +229,8 @@ def run(seqs=4, prompt=1500, part=512, steps=8, cache="e4m3", check=True, out=pr
         want = reference(block, xs)
         err = float((y.double() - want).norm() / want.norm())
         out(f"last step against 64 bits: relative error {err:.4f}")
+    if budget:
+        out(f"tokens kept: {block.cache.lens.tolist()} of {prompt + steps}")
     return err
 
 
@@ -186,6 +241,8 @@ if __name__ == "__main__":
     ap.add_argument("--part", type=int, default=512)
     ap.add_argument("--steps", type=int, default=8)
     ap.add_argument("--cache", choices=["x16", "e4m3", "i8"], default="e4m3")
+    ap.add_argument("--norm", action="store_true")
+    ap.add_argument("--budget", type=int, default=None)
     ap.add_argument("--no-check", dest="check", action="store_false")
     a = ap.parse_args()
-    run(a.seqs, a.prompt, a.part, a.steps, a.cache, a.check)
+    run(a.seqs, a.prompt, a.part, a.steps, a.cache, a.check, norm=a.norm, budget=a.budget)
