@@ -131,6 +131,34 @@ def test_rows(kv, t, lens, rows, Hq, Hkv, D):
     case(sum(lens) + D, lens, rows, Hq, Hkv, D, 16, kv, t, known=[max(0, n // 2) for n in lens], decay=0.5)
 
 
+@pytest.mark.parametrize("page,kv,Hq,Hkv,D", [(4, "x16", 10, 2, 128), (1, "i8", 6, 2, 64), (8, "e4m3", 3, 1, 80),
+                                              (16, "x16", 200, 1, 16), (32, "i8", 400, 2, 48)])
+def test_many_rows_in_every_form(page, kv, Hq, Hkv, D):
+    """Pages of fewer tokens than a copy takes, and more heads to a group than a column tile has."""
+    case(page + Hq, [90, 140], [60, 9], Hq, Hkv, D, page, kv, "bf16", decay=0.5)
+
+
+def test_one_prompt_among_idle_sequences():
+    """The form is chosen by the average; a sequence of many rows is right in the form for few."""
+    lens = [0] * 70 + [200] + [3] * 30
+    case(44, lens, [0] * 70 + [150] + [0] * 30, 10, 2, 128, 16, "x16", "bf16")
+    case(45, [130] + [5] * 90, [130] + [1] * 90, 8, 8, 64, 16, "i8", "f16")
+
+
+def test_no_room_and_no_rows():
+    """Tables of no pages, and calls whose sequences have nothing, change nothing."""
+    c = Cache(3, [20, 30], 2, 64, 16, "x16", "bf16")
+    q = heads(4, 4, 4, 64, "bf16")
+    lse = torch.zeros((4, 4), device=DEV)
+    before = c.weight.clone()
+    for cu in ([0, 0, 0], [4, 4, 4]):
+        assert torch.equal(run(c, q, 256, cu, lse, 4, 0.125, [0, 0], 1.0), before)
+    w = c.weight.clone()
+    tb.tern_attn_weights(0, 0, 2, torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV), 4, 4, 2, 64, 0.125, q, 256, lse, c.pages, 16,
+                         c.k, None, None, 0, c.dev_lens, None, 1.0, w)
+    assert torch.equal(w, before)
+
+
 def test_many_sequences():
     """More than a warp has lanes, some idle."""
     lens = [(7 * b) % 90 for b in range(150)]

@@ -97,6 +97,24 @@ def test_keep_long():
     check_keep(c, 69999, 0, 0)
 
 
+@pytest.mark.parametrize("n", [1024, 1025, 2049, 4097, 8193, 16385, 32768, 32769])
+def test_keep_capacities(n):
+    """Either side of the sizes at which the keys move from one form to the next; some keys in every digit."""
+    c = Cache(n, [n, n // 2], 1, 16, 128, "x16")
+    c.weight.copy_((torch.randint(0, 1 << 31, tuple(c.weight.shape), generator=torch.Generator().manual_seed(n), dtype=torch.int64) *
+                    2 - 1).to(torch.int32).view(torch.float32))      # any bits: NaN, negative, subnormal
+    check_keep(c, n // 3, 4, 16)
+    c.weight.uniform_(0.5, 0.50001)
+    check_keep(c, n - 1, 0, 0)
+
+
+def test_keep_empty_table():
+    out, new = torch.full((2, 3, 5), 7, dtype=torch.int32, device=DEV), torch.full((2,), 7, dtype=torch.int32, device=DEV)
+    w, lens = torch.zeros(1, device=DEV), torch.tensor([4, 0], dtype=torch.int32, device=DEV)
+    tb.tern_kv_keep(2, 3, 0, 16, w, None, 0, lens, 5, 0, 0, out, new)
+    assert (out == -1).all() and (new == 0).all()
+
+
 # --------------------------------------------------------------------- moves
 
 def compact(c, lists, to=None, to_per=0, err=None, weight=True, table=None):
