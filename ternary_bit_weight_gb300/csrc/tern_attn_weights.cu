@@ -10,14 +10,22 @@
 // fma(q.k, scale log2(e), -lse log2(e)): one rounding, of a number that is small
 // wherever the weight is not.
 //
-// What bounds it: for single tokens the keys, read once.
+// What bounds it: for single tokens the keys, read once.  Measured, 40 / 8 heads of 128:
+// 128 sequences of 8192 over int8 codes 206 us (5.7 TB/s), 32 of up to 8192 over e4m3 codes
+// 21 us, one of 701 in bf16 3.8 us a launch in a CUDA graph.
 //
-// Layout of the work.  An item is one (sequence, key/value head, 8 KB of keys);
-// items are dealt to the warps of a persistent grid in turn.  A warp holds its
-// keys as operands of mma.sync m16n8k16 (16 keys x 8 columns, a column being one
-// query row and head; the order of dimensions inside a product is free, so a
-// thread multiplies those it has loaded as 16-byte runs) and passes the columns
-// by them.
+// Layout of the work.  The product is mma.sync m16n8k16 with 16 keys as its rows and 8
+// columns, a column being one query row and head (tcgen05 would take 128 columns of which
+// a single token has 1 to 16; many rows go there, see tern_attn_weights_rows.cu).  The order
+// of dimensions inside a product is free, so a thread multiplies those it has loaded as
+// 16-byte runs.
+//   * stream_kernel: all tiles of 32 keys, one after the other, are cut into equal parts,
+//     one for each warp of a persistent grid, which brings them by TMA into a ring of its
+//     own; warps never wait for one another.  A tile's scalars (factor, weight so far) are
+//     loaded a tile ahead, one key per lane.
+//   * any_pages_kernel: pages of fewer than 16 tokens, which a copy does not take: 8 KB of keys
+//     at a time straight into registers (the first form of the above: 762 us for the 128
+//     sequences).
 
 #include <float.h>
 #include <math_constants.h>
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(Ring<DP, KV, COLS>::kThreads, Ring<DP, KV, COL
 // ------------------------------------------------------- keys of any pages
 
 template <int DP, int KV, bool F16>
-__global__ void __launch_bounds__(kWarps * 32) weights_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kWarps * 32) any_pages_kernel(const __grid_constant__ Args a) {
     constexpr bool kCoded = KV != kKvX16;
     constexpr int kElem = kCoded ? 1 : 2, kRowBytes = DP * kElem;
     constexpr int kPieces = kRowBytes / 64;            // 16-byte runs per lane and key
@@ -549,7 +557,7 @@ cudaError_t launch(const Args& a, int sm_count, cudaStream_t stream) {
     const int64_t most = static_cast<int64_t>(sm_count) * 4;
     const int64_t ctas = ceil_div(items, kWarps);
     const dim3 grid(static_cast<unsigned>(ctas < 1 ? 1 : ctas < most ? ctas : most));
-    return launch_after(weights_kernel<DP, KV, F16>, grid, kWarps * 32, 0, stream, a);
+    return launch_after(any_pages_kernel<DP, KV, F16>, grid, kWarps * 32, 0, stream, a);
 }
 
 template <int DP, bool F16>

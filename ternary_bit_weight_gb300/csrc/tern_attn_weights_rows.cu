@@ -5,15 +5,24 @@
 // and a query row and head a column, so a thread that has a key adds up what it
 // receives without asking another.
 //
-// What bounds it: the tensor cores and beside them the exponential of every score
-// (16 a cycle and SM, against 26 scores of 128 dimensions from the tensor cores).
+// What bounds it: the tensor cores and beside them the warps that take a score out of
+// tensor memory, its exponential and its sum; for windows of few rows what an item
+// costs besides.  Measured, 40 / 8 heads of 128, bf16: a prompt of 4096 tokens 94 us (914
+// TFLOP/s of the pairs that see one another; the tensor pipe is active in 44 % of the
+// cycles), of 8192 322 us (1067), windows of 32 rows over 4 x 8191 tokens 37 us.  Without
+// the sums the prompt takes 55 us: a tile of 192 columns costs the summing warps some 900
+// cycles of exponentials and 600 of waits, accumulations and arrivals, so tiles are as
+// wide as tensor memory allows.  Tried and slower: tiles of 128 columns in three buffers
+// (115 us), twelve or sixteen summing warps instead of eight, in one team (95) or two
+// (112), 256 keys to an item with clusters that share its columns (99), keys by way of
+// shared memory (95; windows 37), a third of the exponentials by a polynomial (111:
+// the unit for them is not what is busy).
 //
 // Work.  An item is 128 keys of one (sequence, key/value head), against the columns
 // of all rows that see them, 192 or fewer at a time.  Items are dealt to one CTA per
 // SM, there and back, a sequence's first keys, which most rows see, first.  The keys
 // lie in tensor memory (codes exactly as 16-bit values, their factor being the
-// thread's), which leaves shared memory to the queries alone: two reads of it per
-// product would fill its bandwidth.
+// thread's), which leaves shared memory to the queries alone.
 //
 // Roles, each a loop over the CTA's items:
 //   warp 0       queries of a column tile by TMA, one box of heads x rows
@@ -408,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                             part[j & 1] = add_x2(part[j & 1], pair(exp2_approx(x0), exp2_approx(x1)));
                         }
                     } else {
+                        // columns before lo are of rows before the key, those from hi on of none
                         const int lo = first - c, hi = columns - c;
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
