@@ -95,6 +95,27 @@ __device__ __forceinline__ uint64_t add_x2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// ------------------------------------------------------------------- waits
+
+// Each lane with `active` set waits for its own barrier; the warp goes on when
+// all have completed.
+__device__ __forceinline__ bool vote_wait(uint32_t bar, uint32_t parity, bool active, volatile int* abort) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xffffffffu, !active || mbar_test_wait(bar, parity))) return true;
+        if ((i & 255u) == 0) {
+            if (__any_sync(0xffffffffu, *abort != 0)) return false;
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0) {
+                t0 = t;
+            } else if (__any_sync(0xffffffffu, t - t0 > kWaitTimeoutNs)) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // -------------------------------- tensor memory, 16 lanes of a warp's quarter
 
 // 16 lanes (taddr's lane 0 or 16 of the warp's quarter) x 128 columns, loaded and

@@ -117,25 +117,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
     return mbar_wait_slow(bar, parity, abort);
 }
 
-// Each lane with `active` set waits for its own barrier; the warp goes on when
-// all have completed.
-__device__ __forceinline__ bool vote_wait(uint32_t bar, uint32_t parity, bool active, volatile int* abort) {
-    uint64_t t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (__all_sync(0xffffffffu, !active || mbar_test_wait(bar, parity))) return true;
-        if ((i & 255u) == 0) {
-            if (__any_sync(0xffffffffu, *abort != 0)) return false;
-            const uint64_t t = global_timer_ns();
-            if (t0 == 0) {
-                t0 = t;
-            } else if (__any_sync(0xffffffffu, t - t0 > kWaitTimeoutNs)) {
-                *abort = 1;
-                return false;
-            }
-        }
-    }
-}
-
 // Named barrier `id` (1..15) across `count` threads (a multiple of 32) that
 // also ORs a predicate over them: every thread gets the same answer, so a
 // group of warps can agree to leave a loop together (none is left waiting
