@@ -84,11 +84,18 @@ struct Item {
     int q0, nq, len;
 };
 
-// The CTA's items in turn; one warp.
+// The CTA's items in turn; one warp.  Items that follow one another are mostly of one
+// sequence, whose place is kept: every role takes this step for every item, and the
+// search for the sequence alone made it 800 cycles.
 struct Walker {
-    Sequence mine = {0, 0, 0};
-    int64_t incl = 0, base = 0, index;
-    int b0 = 0, round = 0;
+    Sequence mine = {0, 0, 0};      // of the 32 sequences from b0, one per lane
+    int64_t incl = 0, base = 0;     // their items up to the lane's end, and those before
+    int b0 = 0;
+    int64_t index, step[2];         // there and back
+    int64_t first = 0, each = 0;    // items before the sequence at hand, and its own
+    int b = 0;
+    Sequence s = {0, 0, 0};
+    float inverse;                  // 1 / Hkv
 
     __device__ __forceinline__ void load(const Args& a, int lane) {
         mine = {0, 0, 0};
@@ -100,31 +107,63 @@ struct Walker {
             if (lane >= d) incl += up;
         }
     }
-    __device__ __forceinline__ Walker(const Args& a, int lane) { load(a, lane); }
+    __device__ __forceinline__ Walker(const Args& a, int lane) {
+        load(a, lane);
+        step[0] = 2 * static_cast<int64_t>(gridDim.x - 1 - blockIdx.x) + 1;
+        step[1] = 2 * static_cast<int64_t>(blockIdx.x) + 1;
+        index = static_cast<int64_t>(blockIdx.x) - step[1];
+        inverse = 1.0f / static_cast<float>(a.Hkv);
+    }
     __device__ __forceinline__ bool next(const Args& a, int lane, Item& o) {
-        index = static_cast<int64_t>(round) * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        ++round;
-        for (;;) {
-            const uint32_t past = __ballot_sync(0xffffffffu, base + incl > index);
-            if (past != 0) {
-                const int src = __ffs(past) - 1;
-                o.b = b0 + src;
-                o.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
-                o.nq = __shfl_sync(0xffffffffu, mine.nq, src);
-                o.len = __shfl_sync(0xffffffffu, mine.len, src);
-                const int64_t in = index - (base + __shfl_sync(0xffffffffu, incl, src)) +
-                                   static_cast<int64_t>((o.len + (kKeys - 1)) / kKeys) * a.Hkv;
-                const int64_t block = (in >> 32) == 0 ? static_cast<uint32_t>(in) / static_cast<uint32_t>(a.Hkv) : in / a.Hkv;
-                o.hk = static_cast<int>(in - block * a.Hkv);
-                o.j0 = static_cast<int>(block) * kKeys;
-                o.i0 = max(0, o.j0 - (o.len - o.nq));
-                return true;
+        index += step[1];
+        const int64_t t = step[0];
+        step[0] = step[1];
+        step[1] = t;
+        if (index - first >= each) {   // (never below: indices grow)
+            for (;;) {
+                const uint32_t past = __ballot_sync(0xffffffffu, base + incl > index);
+                if (past != 0) {
+                    const int src = __ffs(past) - 1;
+                    b = b0 + src;
+                    s.q0 = __shfl_sync(0xffffffffu, mine.q0, src);
+                    s.nq = __shfl_sync(0xffffffffu, mine.nq, src);
+                    s.len = __shfl_sync(0xffffffffu, mine.len, src);
+                    each = tiles_of(a, s, kKeys);
+                    first = base + __shfl_sync(0xffffffffu, incl, src) - each;
+                    break;
+                }
+                base += __shfl_sync(0xffffffffu, incl, 31);
+                b0 += 32;
+                if (b0 >= a.B) return false;
+                load(a, lane);
             }
-            base += __shfl_sync(0xffffffffu, incl, 31);
-            b0 += 32;
-            if (b0 >= a.B) return false;
-            load(a, lane);
         }
+        const int64_t in = index - first;
+        int block, hk;
+        if (in < (1 << 22)) {
+            // (a quotient below 2^22 by fp32 is off by one at most)
+            const int n = static_cast<int>(in);
+            block = static_cast<int>(static_cast<float>(n) * inverse);
+            hk = n - block * a.Hkv;
+            if (hk < 0) {
+                --block;
+                hk += a.Hkv;
+            } else if (hk >= a.Hkv) {
+                ++block;
+                hk -= a.Hkv;
+            }
+        } else {
+            block = static_cast<int>(in / a.Hkv);
+            hk = static_cast<int>(in - static_cast<int64_t>(block) * a.Hkv);
+        }
+        o.b = b;
+        o.q0 = s.q0;
+        o.nq = s.nq;
+        o.len = s.len;
+        o.hk = hk;
+        o.j0 = block * kKeys;
+        o.i0 = max(0, o.j0 - (o.len - o.nq));
+        return true;
     }
 };
 
