@@ -7,16 +7,15 @@
 //
 // What bounds it: the tensor cores and beside them the warps that take a score out of
 // tensor memory, its exponential and its sum; for windows of few rows what an item
-// costs besides.  Measured, 40 / 8 heads of 128, bf16: a prompt of 4096 tokens 94 us (914
-// TFLOP/s of the pairs that see one another; the tensor pipe is active in 44 % of the
-// cycles), of 8192 322 us (1067), windows of 32 rows over 4 x 8191 tokens 37 us.  Without
-// the sums the prompt takes 55 us: a tile of 192 columns costs the summing warps some 900
-// cycles of exponentials and 600 of waits, accumulations and arrivals, so tiles are as
-// wide as tensor memory allows.  Tried and slower: tiles of 128 columns in three buffers
-// (115 us), twelve or sixteen summing warps instead of eight, in one team (95) or two
-// (112), 256 keys to an item with clusters that share its columns (99), keys by way of
-// shared memory (95; windows 37), a third of the exponentials by a polynomial (111:
-// the unit for them is not what is busy).
+// costs besides.  Measured, 40 / 8 heads of 128, bf16: a prompt of 4096 tokens 88 us (980
+// TFLOP/s of the pairs that see one another), of 8192 298 us (1150), windows of 32 rows
+// over 4 x 8191 tokens 35.7 us.  A tile of 192 columns costs the summing warps some 900
+// cycles of exponentials and 500 of waits, accumulations and arrivals, so tiles are as
+// wide as tensor memory allows.  Tried and slower, against 94 us for the prompt at the
+// time: tiles of 128 columns in three buffers (115), twelve or sixteen summing warps
+// instead of eight, in one team (95) or two (112), 256 keys to an item with clusters that
+// share its columns (99), keys by way of shared memory (95; windows the same), a third of
+// the exponentials by a polynomial (111: the unit for them is not what is busy).
 //
 // Work.  An item is 128 keys of one (sequence, key/value head), against the columns
 // of all rows that see them, 192 or fewer at a time.  Items are dealt to one CTA per
@@ -435,9 +434,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 const int columns = min(R, it.nq - i) * a.G;
                 const bool full = it.j0 + kKeys - 1 <= before + i;   // every row of the tile sees every key
                 const int first = max(0, key - before - i) * a.G;    // column from which the key is seen
-                bool got = ok && mbar_wait(cb + kBarOffFull + 8 * st, (n / kOffStages) & 1, abort_flag);
-                got = got && mbar_wait(cb + kBarSFull + 8 * sb, (n >> 1) & 1, abort_flag);
-                ok = __all_sync(0xffffffffu, got);
+                // (one vote for both)
+                ok = ok && vote_wait(lane == 0 ? cb + kBarOffFull + 8 * st : cb + kBarSFull + 8 * sb,
+                                     lane == 0 ? (n / kOffStages) & 1 : (n >> 1) & 1, lane < 2, abort_flag);
+                __syncwarp();
                 if (!ok) break;
                 tc_fence_after_sync();
                 uint64_t part[2] = {0, 0};   // pairs of sums
