@@ -611,10 +611,11 @@ tern_status tern_attn_decode(int x_type, int kv_type, int64_t B, int64_t Hq, int
  * gives them before rounding; products, exponentials and sums are fp32, and the
  * order of a sum does not depend on timing.  scale and decay are finite and not
  * negative; offsets, lengths and page ids are read as tern_attn_prompt and
- * tern_attn_decode read them.  The sequences of one call have different pages: a
- * token that two of them share gets the weight of one.  d_err (optional device
- * int32) is set non-zero only if a pipeline wait timed out (2 s), which correct
- * inputs never cause; the weights that were waited for are NaN then. */
+ * tern_attn_decode read them, but max_pages * page_size is at most 2^30.  The sequences
+ * of one call have different pages: what a token gets that two of them share is not
+ * defined.  d_err (optional device int32) is set non-zero only if a pipeline wait timed
+ * out (2 s), which correct inputs never cause; the weights that were waited for are
+ * NaN then. */
 tern_status tern_attn_weights(int x_type, int kv_type, int64_t B, const int32_t* d_cu_q, int64_t Tq, int64_t Hq,
                               int64_t Hkv, int64_t D, float scale, const void* d_Q, int64_t ldq, const float* d_lse,
                               int64_t num_pages, int64_t page_size, const void* d_kcache, const float* d_kscale,
@@ -627,7 +628,8 @@ tern_status tern_attn_weights(int x_type, int kv_type, int64_t B, const int32_t*
  * the cache come last.
  *   d_keep      device int32 [B, Hkv, budget]: the kept tokens ascending, then -1
  *   d_new_lens  device int32 [B]: min(len, budget); not d_lens
- * budget at least 1 and first + recent, up to 2^30; B * Hkv up to 2^30. */
+ * budget at least 1 and first + recent, up to 2^30; B * Hkv and max_pages * page_size
+ * up to 2^30. */
 tern_status tern_kv_keep(int64_t B, int64_t Hkv, int64_t num_pages, int64_t page_size, const float* d_weight,
                          const int32_t* d_page_table, int64_t max_pages, const int32_t* d_lens, int64_t budget,
                          int64_t first, int64_t recent, int32_t* d_keep, int32_t* d_new_lens, void* stream);
@@ -639,7 +641,8 @@ tern_status tern_kv_keep(int64_t B, int64_t Hkv, int64_t num_pages, int64_t page
  * ascend strictly, as tern_kv_keep's do; a list that does not, or that names a token
  * at or past max_pages * page_size, is left unmoved and counted in d_err (optional
  * device int32).  With another table, which holds `budget` tokens, lists may be in
- * any order, and no page that is written is read; the source stays as it is.
+ * any order; its pages must not be among those that are read, and the source stays
+ * as it is.
  * Entries whose source or target page is outside the cache are skipped.  Sequences
  * that share pages must not be compacted in place.  B * Hkv up to 2^25. */
 tern_status tern_kv_compact(int kv_type, int64_t B, int64_t Hkv, int64_t D, int64_t num_pages, int64_t page_size,

@@ -312,7 +312,7 @@ tern_status tern_attn_weights(int x_type, int kv_type, int64_t B, const int32_t*
     if (!valid_x_type(x_type) || B < 0 || B > kMaxRows || Tq < 0 || Tq > kMaxRows) return TERN_ERR_SHAPE;
     TERN_TRY(check_pages(kv_type, Hkv, D, num_pages, page_size, &shift));
     if (!valid_heads(Hq) || Hq % Hkv != 0 || !valid_scale(scale) || !valid_scale(decay)) return TERN_ERR_SHAPE;
-    if (max_pages < 0 || max_pages > (INT32_MAX >> shift)) return TERN_ERR_SHAPE;
+    if (max_pages < 0 || max_pages > (kMaxRows >> shift)) return TERN_ERR_SHAPE;   // (a token past a tile's end still counts in 32 bits)
     if (d_cu_q == nullptr && Tq != B) return TERN_ERR_SHAPE;
     if (B == 0 || Tq == 0) return TERN_OK;
     if (d_lse == nullptr || d_lens == nullptr || d_weight == nullptr || (max_pages > 0 && d_page_table == nullptr))
@@ -353,7 +353,7 @@ tern_status tern_kv_keep(int64_t B, int64_t Hkv, int64_t num_pages, int64_t page
     if (B < 0) return TERN_ERR_SHAPE;
     TERN_TRY(check_pages(TERN_KV_X16, Hkv, kMaxHeadDim, num_pages, page_size, &shift));
     if (B > kMaxRows / Hkv) return TERN_ERR_SHAPE;
-    if (max_pages < 0 || max_pages > (INT32_MAX >> shift)) return TERN_ERR_SHAPE;
+    if (max_pages < 0 || max_pages > (kMaxRows >> shift)) return TERN_ERR_SHAPE;   // (a token past a tile's end still counts in 32 bits)
     if (budget < 1 || budget > kMaxRows || first < 0 || recent < 0 || first > budget || recent > budget - first)
         return TERN_ERR_SHAPE;
     if (B == 0) return TERN_OK;

@@ -57,3 +57,13 @@ COMPACT = dict(kv_type=1, B=2, Hkv=8, D=128, num_pages=10, page_size=16, k=FAKE,
     (dict(to=FAKE + 2), ALIGN), (dict(err=FAKE + 2), ALIGN), (dict(B=0), OK)])
 def test_compact_refusals(change, status):
     assert call("tern_kv_compact", COMPACT, **change) == status
+
+
+@pytest.mark.parametrize("name,args", [("tern_attn_weights", WEIGHTS), ("tern_kv_keep", KEEP)])
+@pytest.mark.parametrize("page_size", [1, 16, 1024])
+def test_tables_of_more_tokens_than_a_tile_can_count(name, args, page_size):
+    """A tile that begins below 2^31 tokens must not end past them: tables hold 2^30 at most."""
+    limit = (1 << 30) // page_size
+    assert call(name, args, page_size=page_size, max_pages=limit + 1) == SHAPE
+    assert call(name, args, page_size=page_size, max_pages=(2 ** 31 - 1) // page_size) == SHAPE
+    assert call(name, args, page_size=page_size, max_pages=limit, lens=None) == NULL   # (the shape itself passes)
