@@ -73,6 +73,8 @@ tern_status check_norm(int x_type, int in_type, int64_t T, int64_t H, int64_t K,
         return TERN_ERR_SHAPE;
     if (!aligned(X, 16) || !aligned(R, 16) || !aligned(S, 16) || !aligned(W, 16)) return TERN_ERR_ALIGN;
     if (ldx % 8 != 0 || (R != nullptr && ldr % 8 != 0) || (S != nullptr && lds % 8 != 0)) return TERN_ERR_ALIGN;
+    // S in the place of its inputs: an element must be its own, not another row's
+    if (S != nullptr && ((S == R && lds != ldr) || (S == X && (res_type != in_type || lds != ldx)))) return TERN_ERR_SHAPE;
     *n = {};
     n->T = T;
     n->H = H;
@@ -487,6 +489,8 @@ tern_status tern_rms_norm(int x_type, int in_type, int64_t T, int64_t H, int64_t
     if (d_Y == nullptr) return TERN_ERR_NULL;
     if (ldy < H * K || ldy > (int64_t(1) << 40)) return TERN_ERR_SHAPE;
     if (!aligned(d_Y, 16) || ldy % 8 != 0) return TERN_ERR_ALIGN;
+    if (d_Y == d_S || (d_Y == d_X && ((x_type == TERN_X_F16 ? TERN_OUT_F16 : TERN_OUT_BF16) != in_type || ldy != ldx)))
+        return TERN_ERR_SHAPE;
     n.y = static_cast<uint16_t*>(d_Y);
     n.ldy = ldy;
     return from_cuda(tern::launch_norm(n, as_stream(stream)));

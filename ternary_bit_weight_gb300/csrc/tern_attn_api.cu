@@ -363,6 +363,7 @@ tern_status tern_kv_keep(int64_t B, int64_t Hkv, int64_t num_pages, int64_t page
     if (!aligned(d_weight, 4) || !aligned(d_lens, 4) || !aligned(d_keep, 4) || !aligned(d_new_lens, 4) ||
         !aligned(d_page_table, 4))
         return TERN_ERR_ALIGN;
+    if (d_new_lens == d_lens) return TERN_ERR_SHAPE;   // (every head of a sequence reads its length)
     const tern::KeepCall c = {B, static_cast<int>(Hkv), num_pages, shift, d_weight, d_page_table, max_pages, d_lens,
                               budget, first, recent, d_keep, d_new_lens};
     return from_cuda(tern::launch_keep(c, as_stream(stream)));

@@ -67,3 +67,7 @@ def test_tables_of_more_tokens_than_a_tile_can_count(name, args, page_size):
     assert call(name, args, page_size=page_size, max_pages=limit + 1) == SHAPE
     assert call(name, args, page_size=page_size, max_pages=(2 ** 31 - 1) // page_size) == SHAPE
     assert call(name, args, page_size=page_size, max_pages=limit, lens=None) == NULL   # (the shape itself passes)
+
+
+def test_new_lengths_have_a_place_of_their_own():
+    assert call("tern_kv_keep", KEEP, lens=FAKE, new_lens=FAKE) == SHAPE

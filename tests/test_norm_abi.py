@@ -32,3 +32,20 @@ def test_norm_refusals(change, status):
     (dict(q=FAKE + 8), ALIGN), (dict(a=FAKE + 2), ALIGN), (dict(M=0), OK)])
 def test_norm_i8_refusals(change, status):
     assert call("tern_rms_norm_i8", NORM_I8, **change) == status
+
+
+APART = dict(S=FAKE + 4096, Y=FAKE + 8192, R=FAKE + 12288)
+
+
+@pytest.mark.parametrize("change", [
+    dict(Y=FAKE + 4096),                               # both outputs in one place
+    dict(Y=FAKE, ldy=264), dict(Y=FAKE, in_type=0), dict(Y=FAKE, in_type=2), dict(Y=FAKE, x_type=1),
+    dict(S=FAKE, lds=264), dict(S=FAKE, res_type=2), dict(S=FAKE, res_type=0), dict(S=FAKE + 12288, lds=264)])
+def test_in_place_only_element_by_element(change):
+    """An output in its input's place, by another type or leading dimension, would be read after it is written."""
+    assert call("tern_rms_norm", NORM, **{**APART, **change}) == SHAPE
+
+
+@pytest.mark.parametrize("change", [dict(S=FAKE, lds=264), dict(S=FAKE, res_type=1), dict(S=FAKE + 12288, lds=264)])
+def test_i8_in_place_only_element_by_element(change):
+    assert call("tern_rms_norm_i8", NORM_I8, **{**dict(S=FAKE + 4096, R=FAKE + 12288), **change}) == SHAPE
