@@ -20,6 +20,7 @@
 // fit and it took 257 to 336, with whole rows instead of 64 bytes 249).
 
 #include <float.h>
+#include <math_constants.h>
 
 #include "tern_attn.cuh"
 #include "tern_common.cuh"
@@ -50,9 +51,16 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A thread's tokens lie 32 apart in its warp's run of tokens, so that loads are
-// coalesced and a warp lists its tokens in order with votes.  EACH keys of a thread
-// stay in registers; EACH == 0: more tokens than that, each pass loads them again.
+// Whether the weights of four tokens are one access.
+__host__ __device__ __forceinline__ bool by_four(const KeepArgs& a) {
+    return a.shift >= 2 && (reinterpret_cast<uintptr_t>(a.weight) & 15) == 0;
+}
+
+// Four tokens beside one another are one lane's, one page look-up and one load (with a
+// load for each of them the 512 rows below spent half of 33 us on it); 128 of them are a
+// step of the warp, which lists its tokens in order with votes.  EACH keys of a thread stay
+// in registers; EACH == 0: more tokens than that, or pages and planes that do not take four
+// weights in one access; each pass loads them again.
 // Every warp works out a digit by itself from the counts, so a digit costs one barrier.
 template <int EACH, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) keep_kernel(const KeepArgs a) {
@@ -76,36 +84,72 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) keep_kernel(c
     const int32_t* table = a.table + b * a.max_pages;
     const int lo = a.first, hi = len - a.recent;
     // the warp's run of tokens [j0, j1)
-    const int run = ((len + warps - 1) / warps + 31) & ~31;
+    const int run = ((len + warps - 1) / warps + 127) & ~127;
     const int j0 = min(len, warp * run), j1 = min(len, j0 + run);
+    const bool wide = EACH > 0 || by_four(a);
     auto page_of = [&](int j) { return j < j1 ? table[j >> a.shift] : -1; };
-    auto load = [&](int j, int page) -> uint32_t {
-        const bool there = page >= 0 && page < a.num_pages;
-        float w = 0.0f;
-        if (there) w = a.weight[((static_cast<int64_t>(page) * a.Hkv + hk) << a.shift) + (j & page_mask)];
-        return j >= j1 ? kAbsent : j < lo || j >= hi ? kMust : there ? order_key(w) : kLowest;
+    auto weights_of = [&](int page, int j) {   // NaN outside the cache
+        return page >= 0 && page < a.num_pages ? a.weight + (((static_cast<int64_t>(page) * a.Hkv + hk) << a.shift) + (j & page_mask)) : nullptr;
     };
+    auto load4 = [&](int j, int page, float4& w) {   // page: that of j
+        w = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
+        const float* src = weights_of(page, j);
+        if (wide) {
+            if (src != nullptr) w = *reinterpret_cast<const float4*>(src);
+        } else {
+            const float *s1 = weights_of(page_of(j + 1), j + 1), *s2 = weights_of(page_of(j + 2), j + 2), *s3 = weights_of(page_of(j + 3), j + 3);
+            if (src != nullptr) w.x = *src;
+            if (s1 != nullptr) w.y = *s1;
+            if (s2 != nullptr) w.z = *s2;
+            if (s3 != nullptr) w.w = *s3;
+        }
+    };
+    auto key_of = [&](int j, float w) { return j >= j1 ? kAbsent : j < lo || j >= hi ? kMust : order_key(w); };
     uint32_t keys[EACH == 0 ? 1 : EACH];
     if constexpr (EACH > 0) {
-        constexpr int kAtOnce = EACH < 16 ? EACH : 16;
+        constexpr int kAtOnce = EACH < 16 ? EACH / 4 : 4;
 #pragma unroll
-        for (int i0 = 0; i0 < EACH; i0 += kAtOnce) {
+        for (int i0 = 0; i0 < EACH / 4; i0 += kAtOnce) {
             int pages[kAtOnce];
+            float4 w[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) pages[i] = page_of(j0 + 32 * (i0 + i) + lane);
+            for (int i = 0; i < kAtOnce; ++i) pages[i] = page_of(j0 + 128 * (i0 + i) + 4 * lane);
 #pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) keys[i0 + i] = load(j0 + 32 * (i0 + i) + lane, pages[i]);
+            for (int i = 0; i < kAtOnce; ++i) load4(j0 + 128 * (i0 + i) + 4 * lane, pages[i], w[i]);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int j = j0 + 128 * (i0 + i) + 4 * lane, at = 4 * (i0 + i);
+                keys[at] = key_of(j, w[i].x);
+                keys[at + 1] = key_of(j + 1, w[i].y);
+                keys[at + 2] = key_of(j + 2, w[i].z);
+                keys[at + 3] = key_of(j + 3, w[i].w);
+            }
         }
     }
     for (int i = threadIdx.x; i < 4 * 256; i += blockDim.x) bins[0][i] = 0;
-    // what(j, key) for the thread's tokens, the whole warp together
-    auto each = [&](auto&& what) {
+    // what(j, keys of j .. j + 3) for the thread's tokens, the whole warp together
+    auto each4 = [&](auto&& what) {
         if constexpr (EACH > 0) {
 #pragma unroll
-            for (int i = 0; i < EACH; ++i) what(j0 + 32 * i + lane, keys[i]);
+            for (int i = 0; i < EACH / 4; ++i) {
+                const uint32_t k[4] = {keys[4 * i], keys[4 * i + 1], keys[4 * i + 2], keys[4 * i + 3]};
+                what(j0 + 128 * i + 4 * lane, k);
+            }
         } else {
-            for (int j = j0; j < j1; j += 32) what(j + lane, load(j + lane, page_of(j + lane)));
+            for (int at = j0; at < j1; at += 128) {
+                const int j = at + 4 * lane;
+                float4 w;
+                load4(j, page_of(j), w);
+                const uint32_t k[4] = {key_of(j, w.x), key_of(j + 1, w.y), key_of(j + 2, w.z), key_of(j + 3, w.w)};
+                what(j, k);
+            }
         }
+    };
+    auto each = [&](auto&& what) {
+        each4([&](int, const uint32_t (&k)[4]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) what(k[e]);
+        });
     };
     // the key of which `take` are left to keep when all above it are kept: digits of the
     // distance from the smallest key, so that the first ones are spread over the counts
@@ -113,7 +157,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) keep_kernel(c
     if (take > 0) {
         // (one less and one more, so that kAbsent and kMust are out of the way)
         uint32_t least = 0xFFFFFFFFu, most = 0;
-        each([&](int, uint32_t k) {
+        each([&](uint32_t k) {
             least = min(least, k - 1);
             most = max(most, k + 1);
         });
@@ -129,7 +173,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) keep_kernel(c
         for (int turn = 0; at > 0; ++turn) {
             at = max(0, at - 8);
             uint32_t* count = bins[turn];
-            each([&](int, uint32_t k) {
+            each([&](uint32_t k) {
                 if (k - prefix <= span) atomicAdd(&count[(k - prefix) >> at], 1u);
             });
             __syncthreads();
@@ -147,26 +191,34 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) keep_kernel(c
             }
             // the first lane whose count passes `take` has the digit
             const int src = __ffs(__ballot_sync(0xffffffffu, incl >= take)) - 1;
-            uint32_t before = incl - mine, digit = 0, over = 0;
+            uint32_t before = incl - mine, digit = 0, over = 0, held = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (before < take && before + c[i] >= take) {
                     digit = 255 - 8 * lane - i;
                     over = before;
+                    held = c[i];
                 }
                 before += c[i];
             }
             prefix += __shfl_sync(0xffffffffu, digit, src) << at;
             take -= __shfl_sync(0xffffffffu, over, src);
             span = min(most - prefix, (1u << at) - 1);
+            if (__shfl_sync(0xffffffffu, held, src) == take) {   // all that have the digits
+                --prefix;
+                take = 0;
+                break;
+            }
         }
     }
 
     int n_over = 0, n_same = 0;
-    each([&](int, uint32_t k) {
-        n_over += __popc(__ballot_sync(0xffffffffu, k > prefix));
-        n_same += __popc(__ballot_sync(0xffffffffu, k == prefix));
+    each([&](uint32_t k) {
+        n_over += k > prefix;
+        n_same += k == prefix;
     });
+    n_over = __reduce_add_sync(0xffffffffu, n_over);
+    n_same = __reduce_add_sync(0xffffffffu, n_same);
     if (lane == 0) above[warp] = n_over, equal[warp] = n_same;
     __syncthreads();
     // what the warps before list
@@ -175,14 +227,36 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 4 : 1) keep_kernel(c
     same_before = __reduce_add_sync(0xffffffffu, same_before);
     int place = over_before + min(same_before, static_cast<int>(take));
     const uint32_t below = (1u << lane) - 1;
-    each([&](int j, uint32_t k) {
-        const bool same = k == prefix;
-        const uint32_t sames = __ballot_sync(0xffffffffu, same);
-        const bool in = k > prefix || (same && same_before + __popc(sames & below) < static_cast<int>(take));
-        const uint32_t ins = __ballot_sync(0xffffffffu, in);
-        if (in) out[place + __popc(ins & below)] = j;
-        place += __popc(ins);
-        same_before += __popc(sames);
+    each4([&](int j, const uint32_t (&k)[4]) {
+        uint32_t ins[4];
+        bool in[4];
+        if (take > 0) {
+            int rank = same_before;   // of the lane's first token among those that have the smallest kept key
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t sames = __ballot_sync(0xffffffffu, k[e] == prefix);
+                rank += __popc(sames & below);
+                same_before += __popc(sames);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                in[e] = k[e] > prefix || (k[e] == prefix && rank < static_cast<int>(take));
+                rank += k[e] == prefix;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) in[e] = k[e] > prefix;
+        }
+        int at = place;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            ins[e] = __ballot_sync(0xffffffffu, in[e]);
+            at += __popc(ins[e] & below);
+            place += __popc(ins[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (in[e]) out[at++] = j + e;
     });
 }
 
@@ -317,6 +391,7 @@ cudaError_t launch_keep(const KeepCall& c, cudaStream_t stream) {
     a.shift = c.page_shift;
     // registers for every token that there may be; small sequences in few threads
     const dim3 grid(static_cast<unsigned>(c.B * c.Hkv));
+    if (!by_four(a)) return launch_after(keep_kernel<0, 1024>, grid, 1024, 0, stream, a);
     if (a.capacity <= 1024) return launch_after(keep_kernel<4, 256>, grid, 256, 0, stream, a);
     if (a.capacity <= 2048) return launch_after(keep_kernel<8, 256>, grid, 256, 0, stream, a);
     if (a.capacity <= 4096) return launch_after(keep_kernel<16, 256>, grid, 256, 0, stream, a);

@@ -282,3 +282,30 @@ def test_captured():
     graph.replay()
     assert np.array_equal(lists.cpu().numpy(), want_lists) and new.tolist() == [128, 90]
     same(c, want)
+
+
+@pytest.mark.parametrize("page", [1, 2, 4, 16])
+@pytest.mark.parametrize("n", [130, 700, 3001, 40001])
+def test_keep_of_a_plane_at_any_place(page, n):
+    """Weights that begin at any fp32 number, and pages that hold fewer tokens than one access."""
+    c = Cache(n + page, [n, n // 3, 0, 127], 2, 16, page, "x16")
+    want = c.weight
+    room = torch.empty(want.numel() + 4, device=DEV)
+    for shift in range(4):
+        c.weight = room[shift:shift + want.numel()].view(want.shape).copy_(want)
+        check_keep(c, n // 2, 3, 20)
+
+
+def test_keep_where_a_digit_settles_it():
+    """As many tokens as are left to keep share the digits that are known: all of them, and no other."""
+    n = 600
+    for low in (0, 1, 7, 300):                       # of equal top digits, more than are kept or as many
+        c = Cache(low, [n], 1, 16, 16, "x16")
+        plane = torch.cat([torch.full((low,), 1.0) + torch.arange(low) * 2.0 ** -23, torch.linspace(50.0, 90.0, n - low)])
+        flat = plane[torch.randperm(n, generator=torch.Generator().manual_seed(low))]
+        page, row = c.slots(0)
+        weight = c.weight.cpu()
+        weight[page[:n], 0, row[:n]] = flat
+        c.weight.copy_(weight)
+        for budget in {max(1, n - low - 1), max(1, n - low), min(n - 1, n - low + 1), n - 1}:
+            check_keep(c, budget, 0, 0)
