@@ -6,9 +6,9 @@
 // is found digit by digit, 8 bits of its distance from the smallest key at a time, by
 // counting; of the tokens that have it the first ones are kept.  Counts are whole
 // numbers, so the result does not depend on the order of the atomics.  What bounds the
-// choice: a chain of loads, counts and votes per row.  (512 of 577 tokens of 8 heads 4.0 us,
-// 4096 of 8192 of 512 rows 33 us; digits of the keys themselves, whose counts meet in few
-// places, and 128 registers a thread 52 us.)
+// choice: a chain of loads, counts and votes per row.  (512 of 577 tokens of 8 heads 3.1 us
+// in a CUDA graph, 4096 of 8192 of 512 rows 21 us; digits of the keys themselves, whose counts
+// meet in few places, and 128 registers a thread 52 us; a load for each token 33 us.)
 //
 // Moves.  A list of kept tokens ascends, so entry j is at or behind place j: tokens
 // taken in order, a block of places at a time, never write what a later block
@@ -57,7 +57,7 @@ __host__ __device__ __forceinline__ bool by_four(const KeepArgs& a) {
 }
 
 // Four tokens beside one another are one lane's, one page look-up and one load (with a
-// load for each of them the 512 rows below spent half of 33 us on it); 128 of them are a
+// load for each of them half of the time of 512 rows went there); 128 of them are a
 // step of the warp, which lists its tokens in order with votes.  EACH keys of a thread stay
 // in registers; EACH == 0: more tokens than that, or pages and planes that do not take four
 // weights in one access; each pass loads them again.

@@ -222,3 +222,50 @@ def test_streams_and_graphs():
     graph.replay()
     _, y = reference(x2, r2, w, 0.0, 1e-6, 1)
     close(Y, y, y_bound(y, "bf16"), "replayed")
+
+
+@pytest.mark.parametrize("K,lanes", [(40, 8), (64, 8), (96, 16), (128, 16), (136, 32), (256, 32)])
+@pytest.mark.parametrize("t,inp,res", [("bf16", "bf16", None), ("f16", "f32", None), ("bf16", "bf16", "bf16"), ("f16", "f16", "f32"),
+                                       ("bf16", "f32", "f32"), ("f16", "f32", "f16")])
+def test_many_short_rows(K, lanes, t, inp, res):
+    """Rows enough that a lane takes two runs of each, in 7 heads, some rows beyond fp32's squares."""
+    H = 7
+    T = -(-4096 * 160 // (lanes * H)) + 3
+    x, r, w = inputs(K, T, H * K, inp, res, K, t)
+    if inp == "f32":
+        x[5::97] *= 1e25
+        x[7::89] *= 1e-30
+    if res in ("bf16", "f16"):                      # sums within the stream's type
+        x = x.clamp(-1e4, 1e4)
+    X, R = padded(x, 8), None if r is None else padded(r, 16)
+    S = None if r is None else torch.full((T, H * K + 24), 7.0, dtype=DTYPE[res], device=DEV)
+    Y = torch.full((T, H * K + 8), 7.0, dtype=TYPES[t], device=DEV)
+    tb.tern_rms_norm(X16[t], ELEM[inp], T, H, K, X, H * K + 8, ELEM[res or "f32"], R, H * K + 16, S, H * K + 24, w.to(DEV), 0.5,
+                     1e-6, Y, H * K + 8)
+    s, y = reference(x, r, w, 0.5, 1e-6, H)
+    close(Y[:, :H * K], y, y_bound(y, t), "y")
+    assert (Y[:, H * K:] == 7.0).all()
+    if r is not None:
+        close(S[:, :H * K], s, np.abs(s) * (STEP[res] + 2.0 ** -23) + 2.0 ** -25, "s")
+
+
+@pytest.mark.parametrize("K,lanes", [(128, 16), (256, 32)])
+@pytest.mark.parametrize("inp,res", [("bf16", None), ("f32", "bf16")])
+def test_codes_of_many_short_rows(K, lanes, inp, res):
+    """The codes of a call with rows enough for the other form are those of its parts."""
+    T = -(-4096 * 160 // lanes) + 3
+    x, r, w = inputs(K + 1, T, K, inp, res, K, "bf16")
+    out = []
+    for parts in (1, 16):
+        q, a = torch.zeros((T, K), dtype=torch.int8, device=DEV), torch.zeros(T, device=DEV)
+        S = None if r is None else torch.zeros((T, K), dtype=r.dtype, device=DEV)
+        for i in range(parts):
+            lo, hi = T * i // parts, T * (i + 1) // parts
+            X, R = x[lo:hi].to(DEV), None if r is None else r[lo:hi].to(DEV)
+            tb.tern_rms_norm_i8(0, ELEM[inp], hi - lo, K, X, K, ELEM[res or "f32"], R, K, None if S is None else S[lo:hi], K,
+                                w.to(DEV), 0.0, 1e-6, q[lo:hi], a[lo:hi])
+        out.append((q, a, S))
+    # sums of squares in another order: within 2^-18 as above, so a code moves by one at most
+    assert (out[0][0].int() - out[1][0].int()).abs().max() <= 1
+    assert ((out[0][1] - out[1][1]).abs() <= 2.0 ** -17 * out[1][1]).all()
+    assert r is None or torch.equal(out[0][2], out[1][2])
