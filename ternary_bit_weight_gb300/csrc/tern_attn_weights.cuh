@@ -8,7 +8,7 @@
 namespace tern {
 namespace weights {
 
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
 
 struct Args {
     const int32_t* cu_q;
@@ -25,8 +25,7 @@ struct Args {
     int64_t capacity;      // max_pages * page_size
     int B, Tq, Hq, Hkv, G, D;
     int shift;
-    float scale2;          // scale * log2(e)
-    float decay;
+    float scale, decay;
 };
 
 struct Sequence {

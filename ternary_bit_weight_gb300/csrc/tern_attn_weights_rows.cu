@@ -52,6 +52,12 @@ constexpr int kQStagesOf = DP == 64 ? 6 : 3;
 constexpr int kHalfBytes = kColumns * 128;   // 64 dimensions of a column tile
 constexpr int kSCol = 128;               // tensor memory: two key buffers of 64 columns, two of scores
 constexpr int kTmemCols = 512;
+// Scores are taken to base 2 by their scale, and the logarithms with them, each rounded at its
+// own size, which moves a weight by 2^-23 |lse| of itself.  A column tile that has a logarithm
+// past this is summed with care: the difference alone is taken to base 2.
+constexpr float kFarLse = 64.0f;
+// So is a call whose scale is not within 2^-90 and 2^90.
+constexpr float kFarScale = 0x1p90f;
 static_assert(kSCol + 2 * kColumns <= kTmemCols, "tensor-memory budget");
 
 // control block
@@ -64,7 +70,8 @@ constexpr int kBarDrain = kBarKEmpty + 16;
 constexpr int kTmemPtr = kBarDrain + 8, kAbort = kTmemPtr + 4;
 constexpr int kPartial = 256;                          // [2][128] sums of the second halves
 constexpr int kOff = kPartial + 2 * kKeys * 4;         // [stages][columns]
-constexpr int kCtrlBytes = kOff + kOffStages * kColumns * 4;
+constexpr int kFar = kOff + kOffStages * kColumns * 4; // [stages] whether a tile is summed with care
+constexpr int kCtrlBytes = kFar + kOffStages * 4;
 static_assert(kAbort + 4 <= kPartial, "control block");
 
 template <int DP>
@@ -184,6 +191,43 @@ __device__ __forceinline__ void decode4_as(uint32_t w, uint32_t& lo, uint32_t& h
         asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(bx));
         asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(by));
     }
+}
+
+// The exponentials of 32 columns' scores, to `part` (pairs of sums).  MASKED: of columns from
+// lo to hi only.
+template <bool MASKED>
+__device__ __forceinline__ void add_scores(const uint32_t (&v)[32], uint64_t ff, const ulonglong2* off, int lo, int hi, uint64_t (&part)[2]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const ulonglong2 o = off[j / 2];
+        float x0, x1;
+        unpair(fma_x2(pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), ff, j & 1 ? o.y : o.x), x0, x1);
+        if (MASKED) {
+            x0 = 2 * j >= lo && 2 * j < hi ? exp2_approx(x0) : 0.0f;
+            x1 = 2 * j + 1 >= lo && 2 * j + 1 < hi ? exp2_approx(x1) : 0.0f;
+        } else {
+            x0 = exp2_approx(x0);
+            x1 = exp2_approx(x1);
+        }
+        part[j & 1] = add_x2(part[j & 1], pair(x0, x1));
+    }
+}
+
+// What half a tile's columns, from c0 on, give the thread's key, those from lo to hi: `offs` times
+// `unit` are the logarithms' negatives.
+static __device__ __noinline__ float sum_with_care(uint32_t scores, int c0, const float* offs, float unit, int lo, int hi, float scale) {
+    float sum = 0.0f;
+    for (int c = c0; c < min(hi, c0 + kColumns / 2); c += 32) {
+        uint32_t v[32];
+        tmem_ld32_sync(scores + c, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float off = offs[c + j] * unit, y = __uint_as_float(v[j]);
+            if (c + j < lo || c + j >= hi) continue;
+            sum += exp2_approx(fmaf(y, scale, off) * kLog2e);
+        }
+    }
+    return sum;
 }
 
 template <int DP, int KV, bool F16>
@@ -309,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         constexpr int kAhead = 3, kEach = kColumns / 32;
         Walker walk(a, lane);
         float* ring = reinterpret_cast<float*>(ctrl + kOff) + lane;
+        int* far = reinterpret_cast<int*>(ctrl + kFar);
         int64_t place[kEach];   // of the lane's columns among the logarithms of a tile
         int row[kEach];
 #pragma unroll
@@ -347,15 +392,27 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 const int st = n % kOffStages;
                 ok = __all_sync(0xffffffffu, mbar_wait(cb + kBarOffEmpty + 8 * st, (n / kOffStages + 1) & 1, abort_flag));
                 if (!ok) break;
+                bool near = true;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) near = near && (fabsf(x[now][e]) <= kFarLse || x[now][e] == -CUDART_INF_F);
+                near = __all_sync(0xffffffffu, near);
+                const float unit = near ? kLog2e : 1.0f;
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) {   // a row that saw nothing gives nothing
                     const float l = x[now][e];
-                    ring[st * kColumns + 32 * e] = l == -CUDART_INF_F ? l : -l * kLog2e;
+                    ring[st * kColumns + 32 * e] = l == -CUDART_INF_F ? l : -l * unit;
                 }
+                if (lane == 0) far[st] = !near;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(cb + kBarOffFull + 8 * st);
                 ++n;
             }
+        }
+        // one more, of no columns: the sums look up a tile's `far` a tile ahead
+        const int st = n % kOffStages;
+        if (ok && __all_sync(0xffffffffu, mbar_wait(cb + kBarOffEmpty + 8 * st, (n / kOffStages + 1) & 1, abort_flag)) && lane == 0) {
+            far[st] = 0;
+            mbar_arrive(cb + kBarOffFull + 8 * st);
         }
     } else if (warp >= 4 && warp < 8) {
         // --------------------------------------------------------- keys
@@ -411,8 +468,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         const uint32_t scores = tmem + kSCol + ((warp & 3) << 21);
         float* partial = reinterpret_cast<float*>(ctrl + kPartial);
         const float* ring = reinterpret_cast<const float*>(ctrl + kOff);
+        const int* far_of = reinterpret_cast<const int*>(ctrl + kFar);
         int n = 0, k = 0;
-        bool ok = true;
+        bool ok = __all_sync(0xffffffffu, mbar_wait(cb + kBarOffFull, 0, abort_flag));
+        bool far = ok && far_of[0] != 0;   // of tile n
         while (walk.next(a, lane, it)) {
             const int key = it.j0 + row, before = it.len - it.nq;
             int64_t cell = -1;
@@ -421,63 +480,71 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 if (page >= 0 && page < a.num_pages)
                     cell = ((static_cast<int64_t>(page) * a.Hkv + it.hk) << a.shift) + (key & ((1 << a.shift) - 1));
             }
-            float f = a.scale2, old = 0.0f;
+            float f = a.scale, old = 0.0f;
             if (kCoded && cell >= 0) f *= a.kscale[cell];
+            const bool wild = a.scale < 1.0f / kFarScale || a.scale > kFarScale;
             bool had = false;
             if (half == 0 && cell >= 0) {
                 had = key < (a.known == nullptr ? it.len : a.known[it.b]);
                 if (had) old = a.weight[cell];
             }
             float sum = 0.0f;
-            for (int i = it.i0; i < it.nq; i += R, ++n) {
-                const int st = n % kOffStages, sb = n & 1;
-                const int columns = min(R, it.nq - i) * a.G;
-                const bool full = it.j0 + kKeys - 1 <= before + i;   // every row of the tile sees every key
-                const int first = max(0, key - before - i) * a.G;    // column from which the key is seen
-                // (one vote for both)
-                ok = ok && vote_wait(lane == 0 ? cb + kBarOffFull + 8 * st : cb + kBarSFull + 8 * sb,
-                                     lane == 0 ? (n / kOffStages) & 1 : (n >> 1) & 1, lane < 2, abort_flag);
-                __syncwarp();
-                if (!ok) break;
-                tc_fence_after_sync();
-                uint64_t part[2] = {0, 0};   // pairs of sums
-                const uint64_t ff = pair(f, f);
+            // Tiles in turn, those with care in a loop of their own (as a choice inside the one
+            // loop they made it 5 % slower).  One vote for both: that scores of tile n have come,
+            // and of tile n + 1 whether it is to be summed with care.
+            for (int i = it.i0; ok && i < it.nq;) {
+                for (; i < it.nq && !far && !wild; i += R, ++n) {
+                    const int st = n % kOffStages, sb = n & 1, ahead = (n + 1) % kOffStages;
+                    const int columns = min(R, it.nq - i) * a.G;
+                    const bool full = it.j0 + kKeys - 1 <= before + i;   // every row of the tile sees every key
+                    const int first = max(0, key - before - i) * a.G;    // column from which the key is seen
+                    ok = ok && vote_wait(lane == 0 ? cb + kBarOffFull + 8 * ahead : cb + kBarSFull + 8 * sb,
+                                         lane == 0 ? ((n + 1) / kOffStages) & 1 : (n >> 1) & 1, lane < 2, abort_flag);
+                    __syncwarp();
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const int next_far = far_of[ahead];
+                    uint64_t part[2] = {0, 0};   // pairs of sums
+                    const uint64_t ff = pair(f * kLog2e, f * kLog2e);
 #pragma unroll 1
-                for (int c = half * (kColumns / 2); c < min(columns, (half + 1) * (kColumns / 2)); c += 32) {
-                    uint32_t v[32];
-                    tmem_ld32_sync(scores + sb * kColumns + c, v);
-                    const ulonglong2* off = reinterpret_cast<const ulonglong2*>(ring + st * kColumns + c);
-                    if (full && c + 32 <= columns) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const ulonglong2 o = off[j / 2];
-                            float x0, x1;
-                            unpair(fma_x2(pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), ff, j & 1 ? o.y : o.x), x0, x1);
-                            part[j & 1] = add_x2(part[j & 1], pair(exp2_approx(x0), exp2_approx(x1)));
-                        }
-                    } else {
-                        // columns before lo are of rows before the key, those from hi on of none
-                        const int lo = first - c, hi = columns - c;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const ulonglong2 o = off[j / 2];
-                            float x0, x1;
-                            unpair(fma_x2(pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), ff, j & 1 ? o.y : o.x), x0, x1);
-                            x0 = 2 * j >= lo && 2 * j < hi ? exp2_approx(x0) : 0.0f;
-                            x1 = 2 * j + 1 >= lo && 2 * j + 1 < hi ? exp2_approx(x1) : 0.0f;
-                            part[j & 1] = add_x2(part[j & 1], pair(x0, x1));
-                        }
+                    for (int c = half * (kColumns / 2); c < min(columns, (half + 1) * (kColumns / 2)); c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32_sync(scores + sb * kColumns + c, v);
+                        const ulonglong2* off = reinterpret_cast<const ulonglong2*>(ring + st * kColumns + c);
+                        if (full && c + 32 <= columns)
+                            add_scores<false>(v, ff, off, 0, 0, part);
+                        else   // columns before lo are of rows before the key, those from hi on of none
+                            add_scores<true>(v, ff, off, first - c, columns - c, part);
                     }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(cb + kBarSEmpty + 8 * sb);
+                        mbar_arrive(cb + kBarOffEmpty + 8 * st);
+                    }
+                    float p0, p1;
+                    unpair(add_x2(part[0], part[1]), p0, p1);
+                    sum += p0 + p1;
+                    far = next_far != 0;
                 }
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(cb + kBarSEmpty + 8 * sb);
-                    mbar_arrive(cb + kBarOffEmpty + 8 * st);
+                for (; ok && i < it.nq && (far || wild); i += R, ++n) {
+                    const int st = n % kOffStages, sb = n & 1, ahead = (n + 1) % kOffStages;
+                    ok = vote_wait(lane == 0 ? cb + kBarOffFull + 8 * ahead : cb + kBarSFull + 8 * sb,
+                                   lane == 0 ? ((n + 1) / kOffStages) & 1 : (n >> 1) & 1, lane < 2, abort_flag);
+                    __syncwarp();
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const int next_far = far_of[ahead];
+                    sum += sum_with_care(scores + sb * kColumns, half * (kColumns / 2), ring + st * kColumns, far ? 1.0f : kLn2,
+                                         max(0, key - before - i) * a.G, min(R, it.nq - i) * a.G, f);
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(cb + kBarSEmpty + 8 * sb);
+                        mbar_arrive(cb + kBarOffEmpty + 8 * st);
+                    }
+                    far = next_far != 0;
                 }
-                float p0, p1;
-                unpair(add_x2(part[0], part[1]), p0, p1);
-                sum += p0 + p1;
             }
             if (!ok) sum = CUDART_NAN_F;
             if (half == 1) partial[(k & 1) * kKeys + row] = sum;
