@@ -214,7 +214,7 @@ __device__ __forceinline__ void add_scores(const uint32_t (&v)[32], uint64_t ff,
 }
 
 // What half a tile's columns, from c0 on, give the thread's key, those from lo to hi: `offs` times
-// `unit` are the logarithms' negatives.
+// `unit` are the logarithms' negatives, +infinity where a row saw nothing.
 static __device__ __noinline__ float sum_with_care(uint32_t scores, int c0, const float* offs, float unit, int lo, int hi, float scale) {
     float sum = 0.0f;
     for (int c = c0; c < min(hi, c0 + kColumns / 2); c += 32) {
@@ -223,7 +223,7 @@ static __device__ __noinline__ float sum_with_care(uint32_t scores, int c0, cons
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const float off = offs[c + j] * unit, y = __uint_as_float(v[j]);
-            if (c + j < lo || c + j >= hi) continue;
+            if (c + j < lo || c + j >= hi || off == CUDART_INF_F) continue;
             sum += exp2_approx(fmaf(y, scale, off) * kLog2e);
         }
     }
@@ -394,14 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 if (!ok) break;
                 bool near = true;
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) near = near && (fabsf(x[now][e]) <= kFarLse || x[now][e] == -CUDART_INF_F);
+                for (int e = 0; e < kEach; ++e) near = near && fabsf(x[now][e]) <= kFarLse;   // (not where a row saw nothing)
                 near = __all_sync(0xffffffffu, near);
                 const float unit = near ? kLog2e : 1.0f;
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) {   // a row that saw nothing gives nothing
-                    const float l = x[now][e];
-                    ring[st * kColumns + 32 * e] = l == -CUDART_INF_F ? l : -l * unit;
-                }
+                for (int e = 0; e < kEach; ++e) ring[st * kColumns + 32 * e] = -x[now][e] * unit;
                 if (lane == 0) far[st] = !near;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(cb + kBarOffFull + 8 * st);

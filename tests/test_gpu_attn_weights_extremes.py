@@ -94,3 +94,20 @@ def test_tiny_queries_against_large_keys(page, rows, kv, power):
     lse = lse_of(c, Q, cu, HQ, scale)
     want, bound = reference(c, Q, cu, f64(lse), HQ, scale, [0, 0], 1.0)
     check(run(c, Q, HQ * D, cu, lse.to(DEV), HQ, scale, [0, 0], 1.0), want, bound, f"2^{power}")
+
+
+@pytest.mark.parametrize("page,rows", FORMS)
+@pytest.mark.parametrize("kv,t", [("x16", "bf16"), ("x16", "f16"), ("e4m3", "bf16"), ("i8", "f16")])
+def test_rows_that_saw_nothing_add_nothing_whatever_they_hold(page, rows, kv, t):
+    """A row whose logarithm is -infinity, of NaN and infinities, between rows that have weights."""
+    D = 64
+    c = Cache(5, LENS, HKV, D, page, kv, t)
+    cu = np.concatenate([[0], np.cumsum(rows)]).tolist()
+    Q = heads(6, cu[-1], HQ, D, t)
+    lse = lse_of(c, Q, cu, HQ, 0.125)
+    for i, x in ((0, float("nan")), (cu[-1] - 1, float("inf"))):
+        Q[i, :D] = x                    # one head of two that share keys
+        lse[i, 0] = float("-inf")
+    finite = torch.nan_to_num(Q, nan=0.0, posinf=0.0)
+    want, bound = reference(c, finite, cu, f64(lse), HQ, 0.125, [0, 0], 1.0)
+    check(run(c, Q, HQ * D, cu, lse.to(DEV), HQ, 0.125, [0, 0], 1.0, t), want, bound)
