@@ -56,7 +56,7 @@ constexpr int kTmemCols = 512;
 // own size, which moves a weight by 2^-23 |lse| of itself.  A column tile that has a logarithm
 // past this is summed with care: the difference alone is taken to base 2.
 constexpr float kFarLse = 64.0f;
-// So is a call whose scale is not within 2^-90 and 2^90.
+// So are the tiles of an item with a key whose factor times the scale is not within 2^-90 and 2^90.
 constexpr float kFarScale = 0x1p90f;
 static_assert(kSCol + 2 * kColumns <= kTmemCols, "tensor-memory budget");
 
@@ -213,19 +213,69 @@ __device__ __forceinline__ void add_scores(const uint32_t (&v)[32], uint64_t ff,
     }
 }
 
+// Whether a scale times a key's factor is too large or small for the usual sums.
+__device__ __forceinline__ bool out_of_range(float scale, float factor) {
+    const float size = fabsf(scale);
+    return factor != 0.0f && (size < 1.0f / kFarScale || size > kFarScale);
+}
+
+// scale * q.k of a query and a coded key, whatever their sizes: the query times a power of two,
+// so that its largest value lies in [1, 2).
+template <int KV, bool F16>
+__device__ __noinline__ double score_of_codes(const Args& a, const uint16_t* q, const uint8_t* codes, float factor) {
+    float top = 0.0f;
+    for (int d = 0; d < a.D; d += 2) {
+        const float2 x = unpack_x2<F16>(*reinterpret_cast<const uint32_t*>(q + d));
+        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+    const int e = top > 0.0f && top <= FLT_MAX ? -ilogbf(top) : 0;
+    // in two steps: 2^e may pass fp32's range
+    const float up0 = exp2f(static_cast<float>(e / 2)), up1 = exp2f(static_cast<float>(e - e / 2));
+    float sum = 0.0f;
+    for (int d = 0; d < a.D; d += 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(q + d);
+        uint32_t lo, hi;
+        decode4<KV>(*reinterpret_cast<const uint32_t*>(codes + d), lo, hi);
+        const float2 x = unpack_x2<F16>(u.x), y = unpack_x2<F16>(u.y), c = unpack_x2<true>(lo), f = unpack_x2<true>(hi);
+        sum = fmaf(x.x * up0 * up1, c.x, sum);
+        sum = fmaf(x.y * up0 * up1, c.y, sum);
+        sum = fmaf(y.x * up0 * up1, f.x, sum);
+        sum = fmaf(y.y * up0 * up1, f.y, sum);
+    }
+    return static_cast<double>(sum) * factor * a.scale * exp2(static_cast<double>(-e));
+}
+
 // What half a tile's columns, from c0 on, give the thread's key, those from lo to hi: `offs` times
-// `unit` are the logarithms' negatives, +infinity where a row saw nothing.
-static __device__ __noinline__ float sum_with_care(uint32_t scores, int c0, const float* offs, float unit, int lo, int hi, float scale) {
+// `unit` are the logarithms' negatives, +infinity where a row saw nothing.  Products of codes that are out
+// of fp32's range are formed anew; row0 is the tile's first row.
+template <int KV, bool F16>
+__device__ __noinline__ float sum_with_care(const Args& a, uint32_t scores, int c0, const float* offs, float unit, int lo, int hi,
+                                            int64_t cell, int row0, int hk) {
+    const float factor = KV == kKvX16 ? 1.0f : cell >= 0 ? a.kscale[cell] : 0.0f, scale = a.scale * factor;
+    const bool anew = out_of_range(scale, factor);
     float sum = 0.0f;
     for (int c = c0; c < min(hi, c0 + kColumns / 2); c += 32) {
         uint32_t v[32];
         tmem_ld32_sync(scores + c, v);
+        uint32_t again = 0;   // columns whose product is of no use
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             const float off = offs[c + j] * unit, y = __uint_as_float(v[j]);
             if (c + j < lo || c + j >= hi || off == CUDART_INF_F) continue;
-            sum += exp2_approx(fmaf(y, scale, off) * kLog2e);
+            if (KV != kKvX16 && (anew || !(fabsf(y) <= FLT_MAX)))
+                again |= 1u << j;
+            else
+                sum += exp2_approx(fmaf(y, scale, off) * kLog2e);
         }
+        if (KV != kKvX16 && cell >= 0) {
+            for (; again != 0; again &= again - 1) {
+                const int j = c + __ffs(again) - 1, row = j / static_cast<uint32_t>(a.G);
+                const uint16_t* q = a.q + (static_cast<int64_t>(row0) + row) * a.ldq + (hk * a.G + j - row * a.G) * a.D;
+                const double x = score_of_codes<KV, F16>(a, q, a.k + cell * a.D, factor) + offs[j] * unit;
+                sum += exp2_approx(static_cast<float>(x * kLog2e));
+            }
+        }
+        __syncwarp();
     }
     return sum;
 }
@@ -478,8 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     cell = ((static_cast<int64_t>(page) * a.Hkv + it.hk) << a.shift) + (key & ((1 << a.shift) - 1));
             }
             float f = a.scale, old = 0.0f;
-            if (kCoded && cell >= 0) f *= a.kscale[cell];
-            const bool wild = a.scale < 1.0f / kFarScale || a.scale > kFarScale;
+            bool wild;
+            if constexpr (kCoded) {
+                const float factor = cell >= 0 ? a.kscale[cell] : 0.0f;
+                f *= factor;
+                wild = __any_sync(0xffffffffu, out_of_range(f, factor));
+            } else {
+                wild = out_of_range(f, 1.0f);
+            }
             bool had = false;
             if (half == 0 && cell >= 0) {
                 had = key < (a.known == nullptr ? it.len : a.known[it.b]);
@@ -532,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     if (!ok) break;
                     tc_fence_after_sync();
                     const int next_far = far_of[ahead];
-                    sum += sum_with_care(scores + sb * kColumns, half * (kColumns / 2), ring + st * kColumns, far ? 1.0f : kLn2,
-                                         max(0, key - before - i) * a.G, min(R, it.nq - i) * a.G, f);
+                    sum += sum_with_care<KV, F16>(a, scores + sb * kColumns, half * (kColumns / 2), ring + st * kColumns, far ? 1.0f : kLn2,
+                                                  max(0, key - before - i) * a.G, min(R, it.nq - i) * a.G, cell, it.q0 + i, it.hk);
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) {

@@ -111,3 +111,61 @@ def test_rows_that_saw_nothing_add_nothing_whatever_they_hold(page, rows, kv, t)
     finite = torch.nan_to_num(Q, nan=0.0, posinf=0.0)
     want, bound = reference(c, finite, cu, f64(lse), HQ, 0.125, [0, 0], 1.0)
     check(run(c, Q, HQ * D, cu, lse.to(DEV), HQ, 0.125, [0, 0], 1.0, t), want, bound)
+
+
+@pytest.mark.parametrize("page,rows", FORMS)
+@pytest.mark.parametrize("kv", ["e4m3", "i8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("power", [100, 104, 108, 111, 113, 115, 117, 118, -100, -108, -112, -116, -120])
+def test_queries_and_factors_that_make_up_for_one_another(page, rows, kv, D, power):
+    """Queries times 2^power, factors divided by it: the scores stay of ordinary size while their
+    products with the codes would leave fp32's range, or fall below it."""
+    c = Cache(7, LENS, HKV, D, page, kv, "bf16")
+    cu = np.concatenate([[0], np.cumsum(rows)]).tolist()
+    Q = (heads(8, cu[-1], HQ, D, "bf16").double() * 2.0 ** power).to(torch.bfloat16)
+    c.ks = (c.ks.double() * 2.0 ** -power).float()
+    assert torch.isfinite(c.ks).all() and torch.isfinite(Q.float()).all()
+    scale = float(np.float32(D ** -0.5))
+    lse = lse_of(c, Q, cu, HQ, scale)
+    want, bound = reference(c, Q, cu, f64(lse), HQ, scale, [0, 0], 1.0)
+    check(run(c, Q, HQ * D, cu, lse.to(DEV), HQ, scale, [0, 0], 1.0), want, bound, f"2^{power}")
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "i8"])
+@pytest.mark.parametrize("page,rows", FORMS)
+def test_some_rows_and_keys_far_from_the_others(page, rows, kv):
+    """Rows of ordinary size and rows of 2^115, against keys whose factors undo that (to rows of ordinary
+    size they are next to nothing) and keys of ordinary factors that are zero."""
+    D = 128
+    c = Cache(9, LENS, HKV, D, page, kv, "bf16")
+    cu = np.concatenate([[0], np.cumsum(rows)]).tolist()
+    Q = heads(10, cu[-1], HQ, D, "bf16")
+    far = (torch.arange(cu[-1]) % 3 == 1).to(DEV)
+    Q = torch.where(far[:, None], (Q.double() * 2.0 ** 115).to(torch.bfloat16), Q)
+    c.ks[:, :, ::2] = (c.ks[:, :, ::2].double() * 2.0 ** -115).float()
+    c.k[:, :, 1::2] = 0
+    scale = float(np.float32(D ** -0.5))
+    lse = lse_of(c, Q, cu, HQ, scale)
+    want, bound = reference(c, Q, cu, f64(lse), HQ, scale, [0, 0], 1.0)
+    check(run(c, Q, HQ * D, cu, lse.to(DEV), HQ, scale, [0, 0], 1.0), want, bound)
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "i8"])
+@pytest.mark.parametrize("page,rows", FORMS)
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_a_factor_that_is_not_a_number_stays_with_its_token(page, rows, kv, t):
+    """NaN and zero factors: the token's weight is NaN, or that of a score of zero."""
+    D = 64
+    c = Cache(11, LENS, HKV, D, page, kv, t)
+    p, r = c.slots(0)
+    c.ks[p[5], 0, r[5]], c.ks[p[20], 1, r[20]] = 0.0, float("nan")
+    cu = np.concatenate([[0], np.cumsum(rows)]).tolist()
+    Q = heads(12, cu[-1], HQ, D, t)
+    lse = torch.full((cu[-1], HQ), 3.0)
+    got = run(c, Q, HQ * D, cu, lse.to(DEV), HQ, 0.125, [0, 0], 1.0, t)
+    assert torch.isnan(got).nonzero().tolist() == [[int(p[20]), 1, int(r[20])]]
+    c.ks[p[20], 1, r[20]] = 1.0
+    want, bound = reference(c, Q, cu, f64(lse), HQ, 0.125, [0, 0], 1.0)
+    skip = (int(p[20]), 1, int(r[20]))
+    got[skip], want[skip] = 0.0, 0.0
+    check(got, want, bound)
