@@ -349,11 +349,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 __syncwarp();
             }
         }
-        if (!ok) {   // let the copies land
-            volatile int no_abort = 0;
-            for (int i = n < kQStages ? 0 : n - kQStages; i < n; ++i)
-                (void)mbar_wait(cb + kBarQFull + 8 * (i % kQStages), (i / kQStages) & 1, &no_abort);
-        }
+        // let the copies land: after a timeout elsewhere nobody else waits for the last ones
+        volatile int no_abort = 0;
+        for (int i = n < kQStages ? 0 : n - kQStages; i < n; ++i)
+            (void)mbar_wait(cb + kBarQFull + 8 * (i % kQStages), (i / kQStages) & 1, &no_abort);
     } else if (warp == 1) {
         // ----------------------------------------------------- products
         Walker walk(a, lane);
@@ -390,12 +389,11 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             __syncwarp();
             ++k;
         }
-        if (!ok) {   // let the products finish
-            volatile int no_abort = 0;
-            if (elect_one()) umma_commit(cb + kBarDrain);
-            __syncwarp();
-            (void)mbar_wait(cb + kBarDrain, 0, &no_abort);
-        }
+        // let the products finish: after a timeout elsewhere nobody else waits for the last ones
+        volatile int no_abort = 0;
+        if (elect_one()) umma_commit(cb + kBarDrain);
+        __syncwarp();
+        (void)mbar_wait(cb + kBarDrain, 0, &no_abort);
     } else if (warp == 2) {
         // --------------------------------------------------- logarithms
         // Loaded two tiles ahead: they come from L2, 1000 cycles away, and a tile takes not
