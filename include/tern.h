@@ -409,11 +409,13 @@ tern_status tern_linear_i8(const void* d_xq, const float* d_a, const void* d_til
  *   d_S      optional (with d_R only) [T, lds] of res_type: receives s; it may
  *            be d_R or d_X, with the same type and leading dimension
  *   d_W      device [K]; NULL: ones, and w_add is not used
- *   d_Y      device [T, ldy]; it may be d_X, with the same type and leading
- *            dimension (unless d_S is)
- * K is a multiple of 8 up to 32768; data pointers are 16-byte aligned and every
- * ld is a multiple of 8, at least H * K; eps and w_add are finite, eps not
- * negative; T * H is at most 2^30.  T == 0 is a no-op. */
+ *   d_Y      device [T, ldy]; it may be d_X or d_R, with the same type and
+ *            leading dimension (unless d_S is)
+ * Apart from that an output overlaps neither an input nor another output: rows are
+ * taken in any order.  K is a multiple of 8 up to 32768, H at most 4096 and T * H at
+ * most 2^30; data pointers are 16-byte aligned and every ld is a multiple of 8, at
+ * least H * K and at most 2^40; eps and w_add are finite, eps not negative.  T == 0 is
+ * a no-op. */
 tern_status tern_rms_norm(int x_type, int in_type, int64_t T, int64_t H, int64_t K, const void* d_X, int64_t ldx,
                           int res_type, const void* d_R, int64_t ldr, void* d_S, int64_t lds, const void* d_W,
                           float w_add, float eps, void* d_Y, int64_t ldy, void* stream);
@@ -421,8 +423,8 @@ tern_status tern_rms_norm(int x_type, int in_type, int64_t T, int64_t H, int64_t
 /* The same with int8 codes for tern_linear_i8: y is not rounded to 16 bits in
  * between, and a[m] = max_k |y| / 127, q[m, k] = rint(y * (127 / max_k |y|)) are
  * written as tern_quantize_x writes them (d_xq of tern_xq_bytes(M, K) bytes, d_a
- * fp32 [M]).  A row that holds a NaN or an infinity gets a = NaN and codes 0.
- * K is a multiple of 128 up to 32768. */
+ * fp32 [M]; in the place of no input and of no other output).  A row that holds a NaN
+ * or an infinity gets a = NaN and codes 0.  K is a multiple of 128 up to 32768. */
 tern_status tern_rms_norm_i8(int x_type, int in_type, int64_t M, int64_t K, const void* d_X, int64_t ldx, int res_type,
                              const void* d_R, int64_t ldr, void* d_S, int64_t lds, const void* d_W, float w_add,
                              float eps, void* d_xq, float* d_a, void* stream);

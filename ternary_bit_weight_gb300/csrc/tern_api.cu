@@ -489,7 +489,9 @@ tern_status tern_rms_norm(int x_type, int in_type, int64_t T, int64_t H, int64_t
     if (d_Y == nullptr) return TERN_ERR_NULL;
     if (ldy < H * K || ldy > (int64_t(1) << 40)) return TERN_ERR_SHAPE;
     if (!aligned(d_Y, 16) || ldy % 8 != 0) return TERN_ERR_ALIGN;
-    if (d_Y == d_S || (d_Y == d_X && ((x_type == TERN_X_F16 ? TERN_OUT_F16 : TERN_OUT_BF16) != in_type || ldy != ldx)))
+    const int y_type = x_type == TERN_X_F16 ? TERN_OUT_F16 : TERN_OUT_BF16;
+    if (d_Y == d_S || d_Y == d_W || (d_S != nullptr && d_S == d_W) || (d_Y == d_X && (y_type != in_type || ldy != ldx)) ||
+        (d_Y == d_R && (y_type != res_type || ldy != ldr)))
         return TERN_ERR_SHAPE;
     n.y = static_cast<uint16_t*>(d_Y);
     n.ldy = ldy;
@@ -507,6 +509,10 @@ tern_status tern_rms_norm_i8(int x_type, int in_type, int64_t M, int64_t K, cons
     if (st != TERN_OK || done) return st;
     if (d_xq == nullptr || d_a == nullptr) return TERN_ERR_NULL;
     if (!aligned(d_xq, 16) || !aligned(d_a, 4)) return TERN_ERR_ALIGN;
+    // a row's codes or factor in the place of another row's values would be written before those are read
+    for (const void* out : {static_cast<const void*>(d_xq), static_cast<const void*>(d_a)})
+        if (out == d_X || out == d_R || out == d_S || out == d_W) return TERN_ERR_SHAPE;
+    if (d_xq == d_a || (d_S != nullptr && d_S == d_W)) return TERN_ERR_SHAPE;
     n.q = static_cast<int8_t*>(d_xq);
     n.a = d_a;
     return from_cuda(tern::launch_norm(n, as_stream(stream)));

@@ -49,3 +49,34 @@ def test_in_place_only_element_by_element(change):
 @pytest.mark.parametrize("change", [dict(S=FAKE, lds=264), dict(S=FAKE, res_type=1), dict(S=FAKE + 12288, lds=264)])
 def test_i8_in_place_only_element_by_element(change):
     assert call("tern_rms_norm_i8", NORM_I8, **{**dict(S=FAKE + 4096, R=FAKE + 12288), **change}) == SHAPE
+
+
+@pytest.mark.parametrize("change", [
+    dict(Y=FAKE + 12288, res_type=0), dict(Y=FAKE + 12288, res_type=2), dict(Y=FAKE + 12288, ldy=264),
+    dict(Y=FAKE + 12288, S=None, res_type=0), dict(Y=FAKE + 12288, S=None, x_type=1), dict(Y=FAKE + 16384, W=FAKE + 16384),
+    dict(S=FAKE + 16384, W=FAKE + 16384)])
+def test_outputs_over_the_stream_and_the_weights(change):
+    """The normalised rows in the residual stream's place by another type or leading dimension, an output in the weights'."""
+    assert call("tern_rms_norm", NORM, **{**APART, **change}) == SHAPE
+
+
+I8_APART = dict(X=FAKE, R=FAKE + 4096, S=FAKE + 8192, W=FAKE + 12288, q=FAKE + 16384, a=FAKE + 20480)
+
+
+@pytest.mark.parametrize("out", ["q", "a"])
+@pytest.mark.parametrize("over", ["X", "R", "S", "W"])
+def test_codes_and_factors_have_a_place_of_their_own(out, over):
+    assert call("tern_rms_norm_i8", NORM_I8, **{**I8_APART, out: I8_APART[over]}) == SHAPE
+    if over != "W":
+        assert call("tern_rms_norm_i8", NORM_I8, **{**I8_APART, "R": I8_APART["S"], out: I8_APART["S"]}) == SHAPE
+
+
+def test_codes_beside_their_factors():
+    assert call("tern_rms_norm_i8", NORM_I8, **{**I8_APART, "a": I8_APART["q"]}) == SHAPE
+
+
+@pytest.mark.parametrize("change,status", [(dict(H=4096, T=4, K=8, ldx=32768, ldr=32768, lds=32768, ldy=32768, W=FAKE + 8), ALIGN),
+                                           (dict(ldy=(1 << 40) + 8), SHAPE), (dict(ldr=(1 << 40) + 8), SHAPE)])
+def test_limits(change, status):
+    """The largest head count passes the shape (the weights' alignment is what is refused), leading dimensions end at 2^40."""
+    assert call("tern_rms_norm", NORM, **{**APART, **change}) == status
