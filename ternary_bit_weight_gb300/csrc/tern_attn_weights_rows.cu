@@ -53,9 +53,10 @@ constexpr int kHalfBytes = kColumns * 128;   // 64 dimensions of a column tile
 constexpr int kSCol = 128;               // tensor memory: two key buffers of 64 columns, two of scores
 constexpr int kTmemCols = 512;
 // Scores are taken to base 2 by their scale, and the logarithms with them, each rounded at its
-// own size, which moves a weight by 2^-23 |lse| of itself.  A column tile that has a logarithm
-// past this is summed with care: the difference alone is taken to base 2.
-constexpr float kFarLse = 64.0f;
+// own size, which moves a weight by 2^-23 |lse| of itself, as the roundings of the product's sum
+// may.  A column tile that has a logarithm past this is summed with care: the difference alone is
+// taken to base 2 (a prompt of 4096 tokens 142 us, over int8 codes 190; 89 without).
+constexpr float kFarLse = 128.0f;
 // So are the tiles of an item with a key whose factor times the scale is not within 2^-90 and 2^90.
 constexpr float kFarScale = 0x1p90f;
 static_assert(kSCol + 2 * kColumns <= kTmemCols, "tensor-memory budget");
@@ -246,35 +247,47 @@ __device__ __noinline__ double score_of_codes(const Args& a, const uint16_t* q, 
 }
 
 // What half a tile's columns, from c0 on, give the thread's key, those from lo to hi: `offs` times
-// `unit` are the logarithms' negatives, +infinity where a row saw nothing.  Products of codes that are out
-// of fp32's range are formed anew; row0 is the tile's first row.
+// `unit` are the logarithms' negatives, +infinity where a row saw nothing.  Where a product of
+// codes is out of fp32's range, 32 scores are formed anew; row0 is the tile's first row.
 template <int KV, bool F16>
 __device__ __noinline__ float sum_with_care(const Args& a, uint32_t scores, int c0, const float* offs, float unit, int lo, int hi,
                                             int64_t cell, int row0, int hk) {
-    const float factor = KV == kKvX16 ? 1.0f : cell >= 0 ? a.kscale[cell] : 0.0f, scale = a.scale * factor;
-    const bool anew = out_of_range(scale, factor);
+    constexpr bool kCoded = KV != kKvX16;
+    const float factor = !kCoded ? 1.0f : cell >= 0 ? a.kscale[cell] : 0.0f, scale = a.scale * factor;
+    const uint64_t ff = pair(scale, scale), uu = pair(unit, unit), to2 = pair(kLog2e, kLog2e);
     float sum = 0.0f;
     for (int c = c0; c < min(hi, c0 + kColumns / 2); c += 32) {
         uint32_t v[32];
         tmem_ld32_sync(scores + c, v);
-        uint32_t again = 0;   // columns whose product is of no use
+        const ulonglong2* off = reinterpret_cast<const ulonglong2*>(offs + c);
+        const int first = lo - c, end = hi - c;
+        uint64_t part[2] = {0, 0}, bad = 0;   // `bad` becomes NaN by a product that is not finite
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float off = offs[c + j] * unit, y = __uint_as_float(v[j]);
-            if (c + j < lo || c + j >= hi || off == CUDART_INF_F) continue;
-            if (KV != kKvX16 && (anew || !(fabsf(y) <= FLT_MAX)))
-                again |= 1u << j;
-            else
-                sum += exp2_approx(fmaf(y, scale, off) * kLog2e);
+        for (int j = 0; j < 16; ++j) {
+            const ulonglong2 two = off[j / 2];
+            const uint64_t o = mul_x2(j & 1 ? two.y : two.x, uu);
+            float y0 = __uint_as_float(v[2 * j]), y1 = __uint_as_float(v[2 * j + 1]), x0, x1, o0, o1;
+            unpair(mul_x2(fma_x2(pair(y0, y1), ff, o), to2), x0, x1);
+            unpair(o, o0, o1);
+            const bool in0 = 2 * j >= first && 2 * j < end && o0 != CUDART_INF_F, in1 = 2 * j + 1 >= first && 2 * j + 1 < end && o1 != CUDART_INF_F;
+            part[j & 1] = add_x2(part[j & 1], pair(in0 ? exp2_approx(x0) : 0.0f, in1 ? exp2_approx(x1) : 0.0f));
+            if (kCoded) bad = fma_x2(pair(in0 ? y0 : 0.0f, in1 ? y1 : 0.0f), 0, bad);
         }
-        if (KV != kKvX16 && cell >= 0) {
-            for (; again != 0; again &= again - 1) {
-                const int j = c + __ffs(again) - 1, row = j / static_cast<uint32_t>(a.G);
+        float p0, p1, b0, b1;
+        unpair(add_x2(part[0], part[1]), p0, p1);
+        unpair(bad, b0, b1);
+        p0 += p1;
+        if (kCoded && cell >= 0 && (b0 != 0.0f || b1 != 0.0f || out_of_range(scale, factor))) {
+            p0 = 0.0f;
+            for (int j = max(lo, c); j < min(hi, c + 32); ++j) {
+                const int row = j / static_cast<uint32_t>(a.G);
                 const uint16_t* q = a.q + (static_cast<int64_t>(row0) + row) * a.ldq + (hk * a.G + j - row * a.G) * a.D;
+                if (offs[j] == CUDART_INF_F) continue;
                 const double x = score_of_codes<KV, F16>(a, q, a.k + cell * a.D, factor) + offs[j] * unit;
-                sum += exp2_approx(static_cast<float>(x * kLog2e));
+                p0 += exp2_approx(static_cast<float>(x * kLog2e));
             }
         }
+        sum += p0;
         __syncwarp();
     }
     return sum;

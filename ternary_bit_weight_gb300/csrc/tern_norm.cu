@@ -74,12 +74,6 @@ __device__ __forceinline__ uint4 narrow8(const float (&v)[8], int f16) {
     return make_uint4(pack_x2<false>(v[0], v[1]), pack_x2<false>(v[2], v[3]), pack_x2<false>(v[4], v[5]), pack_x2<false>(v[6], v[7]));
 }
 
-__device__ __forceinline__ uint64_t mul_x2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // A run of 8 elements of 16 or 32 bits as it lies in memory.
 template <bool WIDE>
 struct Run {
