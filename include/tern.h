@@ -610,8 +610,10 @@ tern_status tern_attn_decode(int x_type, int kv_type, int64_t B, int64_t Hq, int
  * what lies there is not read, so that a step of one token each passes lens - 1.
  * A row with lse = -infinity saw nothing and adds nothing.  A sequence without rows
  * or tokens is left as it is, and so are cells of no token.  Keys as tern_kv_read
- * gives them before rounding; products, exponentials and sums are fp32, and the
- * order of a sum does not depend on timing.  scale and decay are finite and not
+ * gives them before rounding (over a coded cache as tern_attn_decode takes them; a
+ * prompt's logarithms are of keys that tern_kv_read has rounded to 16 bits, so that what
+ * one row adds there comes to 1 up to that rounding of its scores); products, exponentials
+ * and sums are fp32, and the order of a sum does not depend on timing.  scale and decay are finite and not
  * negative; offsets, lengths and page ids are read as tern_attn_prompt and
  * tern_attn_decode read them, but max_pages * page_size is at most 2^30.  The sequences
  * of one call have different pages: what a token gets that two of them share is not

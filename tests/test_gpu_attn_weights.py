@@ -305,3 +305,32 @@ def test_repeats_streams_and_graphs():
     graph.replay()
     want, bound = reference(c, q, cu, f64(lse), 10, scale, kn, 1.0)
     check(w, want, bound, "replayed")
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "i8"])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+def test_weights_of_a_prompt_over_codes_add_to_its_rows(kv, t):
+    """tern_attn_prompt's logarithms are of the keys that tern_kv_read rounded to 16 bits, the weights of the keys before
+    that: a row's scores differ by u S, u the type's half step, beside both calls' own errors."""
+    lens, rows, Hq, Hkv, D, page = [300, 130], [300, 40], 10, 2, 128, 16
+    c = Cache(17, lens, Hkv, D, page, kv, t)
+    q = heads(33, sum(rows), Hq, D, t, spread=0.2)
+    slots = torch.cat([torch.from_numpy(p[:n].astype(np.int64) * page + r[:n]) for n, (p, r) in
+                       ((n, c.slots(b)) for b, n in enumerate(lens))]).to(DEV)
+    k, v = (torch.empty((sum(lens), Hkv * D), dtype=TYPES[t], device=DEV) for _ in range(2))
+    tb.tern_kv_read(X16[t], KV[kv], sum(lens), Hkv, D, slots, c.pages, page, c.k, c.v, c.ks, c.vs, k, Hkv * D, v, Hkv * D)
+    cu_q, cu_k = (torch.tensor([0, *np.cumsum(x)], dtype=torch.int32, device=DEV) for x in (rows, lens))
+    o, lse = torch.empty_like(q), torch.empty((sum(rows), Hq), device=DEV)
+    ws = torch.zeros(tb.tern_attn_prompt_workspace_bytes(2, sum(rows), sum(lens), Hq, Hkv, D), dtype=torch.uint8, device=DEV)
+    scale = float(np.float32(D ** -0.5))
+    tb.tern_attn_prompt(X16[t], 2, cu_q, cu_k, sum(rows), sum(lens), Hq, Hkv, D, True, scale, q, Hq * D, k, Hkv * D, v, Hkv * D, o,
+                        Hq * D, lse, ws)
+    cu = cu_q.tolist()
+    w = f64(run(c, q, Hq * D, cu, lse, Hq, scale, [0, 0], 1.0, t))
+    for b, n in enumerate(lens):
+        p, r = c.slots(b)
+        for g in range(Hkv):
+            S = max(scores(c, q, (cu[b], cu[b + 1]), b, h, Hq // Hkv, scale)[1].max() for h in range(g * Hq // Hkv, (g + 1) * Hq // Hkv))
+            e = (2.0 ** -8 if t == "bf16" else 2.0 ** -11) * S + 2 * (D * 2.0 ** -23 * S + 2.0 ** -20) + 2.0 ** -20 * np.abs(f64(lse)).max()
+            want = rows[b] * Hq // Hkv
+            assert abs(w[p[:n], g, r[:n]].sum() - want) <= want * np.expm1(e)
