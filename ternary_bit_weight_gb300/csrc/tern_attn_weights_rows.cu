@@ -225,25 +225,38 @@ __device__ __forceinline__ bool out_of_range(float scale, float factor) {
 template <int KV, bool F16>
 __device__ __noinline__ double score_of_codes(const Args& a, const uint16_t* q, const uint8_t* codes, float factor) {
     float top = 0.0f;
-    for (int d = 0; d < a.D; d += 2) {
-        const float2 x = unpack_x2<F16>(*reinterpret_cast<const uint32_t*>(q + d));
-        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+    for (int d = 0; d < a.D; d += 16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 u = *reinterpret_cast<const uint4*>(q + d + 8 * h);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = unpack_x2<F16>(w[i]);
+                top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+            }
+        }
     }
     const int e = top > 0.0f && top <= FLT_MAX ? -ilogbf(top) : 0;
     // in two steps: 2^e may pass fp32's range
     const float up0 = exp2f(static_cast<float>(e / 2)), up1 = exp2f(static_cast<float>(e - e / 2));
     float sum = 0.0f;
-    for (int d = 0; d < a.D; d += 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(q + d);
-        uint32_t lo, hi;
-        decode4<KV>(*reinterpret_cast<const uint32_t*>(codes + d), lo, hi);
-        const float2 x = unpack_x2<F16>(u.x), y = unpack_x2<F16>(u.y), c = unpack_x2<true>(lo), f = unpack_x2<true>(hi);
-        sum = fmaf(x.x * up0 * up1, c.x, sum);
-        sum = fmaf(x.y * up0 * up1, c.y, sum);
-        sum = fmaf(y.x * up0 * up1, f.x, sum);
-        sum = fmaf(y.y * up0 * up1, f.y, sum);
+    for (int d = 0; d < a.D; d += 16) {
+        const uint4 u = *reinterpret_cast<const uint4*>(codes + d);
+        const uint32_t k[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint2 w = *reinterpret_cast<const uint2*>(q + d + 4 * i);
+            uint32_t lo, hi;
+            decode4<KV>(k[i], lo, hi);
+            const float2 x = unpack_x2<F16>(w.x), y = unpack_x2<F16>(w.y), c = unpack_x2<true>(lo), f = unpack_x2<true>(hi);
+            sum = fmaf(x.x * up0 * up1, c.x, sum);
+            sum = fmaf(x.y * up0 * up1, c.y, sum);
+            sum = fmaf(y.x * up0 * up1, f.x, sum);
+            sum = fmaf(y.y * up0 * up1, f.y, sum);
+        }
     }
-    return static_cast<double>(sum) * factor * a.scale * exp2(static_cast<double>(-e));
+    return static_cast<double>(sum) * factor * a.scale * scalbn(1.0, -e);
 }
 
 // What half a tile's columns, from c0 on, give the thread's key, those from lo to hi: `offs` times
