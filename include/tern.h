@@ -607,17 +607,18 @@ tern_status tern_attn_decode(int x_type, int kv_type, int64_t B, int64_t Hq, int
  *               exp(scale * Q[i, h].K[j, g] - lse[i, h]),
  *   weight[j, g] = (j < d_known[b] ? decay * weight[j, g] : 0) + add[j, g].
  * d_known (device int32 [B], NULL: all): tokens at or past it have no weight yet and
- * what lies there is not read, so that a step of one token each passes lens - 1.
+ * what lies there has no effect, so that a step of one token each passes lens - 1.
  * A row with lse = -infinity saw nothing and adds nothing.  A sequence without rows
  * or tokens is left as it is, and so are cells of no token.  Keys as tern_kv_read
  * gives them before rounding (over a coded cache as tern_attn_decode takes them; a
  * prompt's logarithms are of keys that tern_kv_read has rounded to 16 bits, so that what
  * one row adds there comes to 1 up to that rounding of its scores); products, exponentials
- * and sums are fp32, and the order of a sum does not depend on timing.  scale and decay are finite and not
- * negative; offsets, lengths and page ids are read as tern_attn_prompt and
- * tern_attn_decode read them, but max_pages * page_size is at most 2^30.  The sequences
- * of one call have different pages: what a token gets that two of them share is not
- * defined.  d_err (optional device int32) is set non-zero only if a pipeline wait timed
+ * and sums are fp32, and the order of a sum does not depend on timing.  The kernel is
+ * chosen for the whole call by its rows per sequence: a batch of single tokens and of
+ * parts of prompts is faster as two calls.  scale and decay are finite and not negative;
+ * offsets, lengths and page ids are read as tern_attn_prompt and tern_attn_decode read
+ * them, but max_pages * page_size is at most 2^30.  The sequences of one call have
+ * different pages: what a token gets that two of them share is not defined.  d_err (optional device int32) is set non-zero only if a pipeline wait timed
  * out (2 s), which correct inputs never cause; the weights that were waited for are
  * NaN then. */
 tern_status tern_attn_weights(int x_type, int kv_type, int64_t B, const int32_t* d_cu_q, int64_t Tq, int64_t Hq,

@@ -12,8 +12,8 @@
 // its own size, one operation less: weights of equal scores of 9e6 were off by up to 38 %.)
 //
 // What bounds it: for single tokens the keys, read once.  Measured, 40 / 8 heads of 128:
-// 128 sequences of 8192 over int8 codes 206 us (5.7 TB/s), 32 of up to 8192 over e4m3 codes
-// 21 us, one of 701 in bf16 3.8 us a launch in a CUDA graph.
+// 128 sequences of 8192 over int8 codes 208 us (5.6 TB/s), in bf16 347 us (6.4 TB/s), 32 of up
+// to 8192 over e4m3 codes 21 us, one of 701 in bf16 3.8 us a launch in a CUDA graph.
 //
 // Layout of the work.  The product is mma.sync m16n8k16 with 16 keys as its rows and 8
 // columns, a column being one query row and head (tcgen05 would take 128 columns of which
@@ -26,7 +26,7 @@
 //     loaded a tile ahead, one key per lane.
 //   * any_pages_kernel: pages of fewer than 16 tokens, which a copy does not take: 8 KB of keys
 //     at a time straight into registers (the first form of the above: 762 us for the 128
-//     sequences).
+//     sequences over int8 codes, 920 in pages of 8).
 
 #include <float.h>
 #include <math_constants.h>

@@ -7,9 +7,9 @@
 //
 // What bounds it: the tensor cores and beside them the warps that take a score out of
 // tensor memory, its exponential and its sum; for windows of few rows what an item
-// costs besides.  Measured, 40 / 8 heads of 128, bf16: a prompt of 4096 tokens 88 us (980
-// TFLOP/s of the pairs that see one another), of 8192 298 us (1150), windows of 32 rows
-// over 4 x 8191 tokens 35.7 us.  A tile of 192 columns costs the summing warps some 900
+// costs besides.  Measured, 40 / 8 heads of 128, bf16: a prompt of 4096 tokens 89 us (960
+// TFLOP/s of the pairs that see one another; over codes the same), of 8192 305 us (1125),
+// windows of 32 rows over 4 x 8191 tokens 35.3 us.  A tile of 192 columns costs the summing warps some 900
 // cycles of exponentials and 500 of waits, accumulations and arrivals, so tiles are as
 // wide as tensor memory allows.  Tried and slower, against 94 us for the prompt at the
 // time: tiles of 128 columns in three buffers (115), twelve or sixteen summing warps
@@ -31,6 +31,12 @@
 //                an item ahead
 //   warps 8-15   exponentials and sums: a thread has a key and half of the columns
 // Every wait is bounded; after a timeout the weights not yet written become NaN.
+//
+// Sums with care.  A column tile with a logarithm far from zero or of a row that saw nothing,
+// and every tile of an item with a key whose factor is out of the ordinary, go through a
+// slower form of the sums, right for any size of values (see kFarLse, kFarScale).  Of codes
+// it forms a score anew where their product with the query is beyond fp32: 0.3 ms a tile if
+// all of them are, so that past 200000 rows of such values the waits would run out.
 
 #include <float.h>
 #include <math_constants.h>

@@ -12,9 +12,9 @@
 // store for a few tokens.
 //
 // Measured: 8191 rows of 5120 in bf16 with the residual 50 us (6.7 TB/s), fp32 input and
-// codes 61 us (6.2 TB/s), 40 heads of 128 of 4095 tokens 14.5 us (5.8 TB/s; with a choice of
-// type for every element, and twice the lanes to a row, instructions bounded it: 20.2), 16
-// rows 1.9 us a launch in a CUDA graph.
+// codes 61 us (6.2 TB/s), bf16 input and an fp32 stream 83 us (6.1 TB/s), 40 heads of 128 of
+// 4095 tokens 15.1 us (5.5 TB/s; with a choice of type for every element, and twice the lanes
+// to a row, instructions bounded it: 20.2), 16 rows 1.9 us a launch in a CUDA graph.
 //
 // Layout of the work: a thread holds NV runs of 8 elements.  Rows of up to 256
 // elements are taken by 4 to 32 lanes, several rows to a warp, up to 1024 by a
@@ -132,8 +132,10 @@ struct Most {
     __device__ __forceinline__ float none() const { return 0.0f; }
 };
 
-// CTAs of an SM, so that short rows' loads are many: as many as fit without spilling
-// more than a few bytes (163800 rows of 128: 16.1 us at 58 registers a thread, 15.1 at 40).
+// CTAs of an SM, so that short rows' loads are many: as many as fit with spills of 48 bytes a
+// thread at most (163800 rows of 128: 16.1 us at 58 registers a thread, 15.1 at 40).  CTAs of
+// one row are held to 64 registers, whatever their size: their four-run form spills some 30
+// bytes where there is no stream or all values have 16 bits, else 96 to 192.
 template <bool X32, int RES, int LANES, int NV, bool CTA>
 constexpr int kCtas = CTA || NV == 1 || LANES == 32 ? 1 : X32 || RES == kRes32 ? 8 : RES == kRes16 ? 10 : 12;
 
